@@ -265,6 +265,40 @@ int pa_prefill(void *out, int32_t out_dtype, const void *query, const int32_t *q
                int32_t num_kv_heads, float scale, void *stream);
 
 /*
+ * Attention over whole prompts ("PagedAttention 论文精读笔记", §2.1 attention
+ * equation, §5.3 prompt step): causal attention of the tokens of num_seqs
+ * packed sequences over themselves, keys and values taken from the
+ * projections' rows rather than from the pools -- for prompts that have no
+ * cached prefix (with one: pa_prefill; for single tokens: pa_decode).
+ * Sequence s owns rows query_start_loc[s] .. query_start_loc[s+1]-1 of every
+ * array; its token i attends to its tokens 0 .. i:
+ *   out[q][h][:] = sum_j softmax_j(scale * query[q][h] . key_j) value_j,
+ * query head h reading KV head h / G, G = num_heads / num_kv_heads.
+ *   out               device, [num_tokens][num_heads][head_dim] of `dtype`;
+ *                     rows not covered by a sequence are not written
+ *   query, key, value device, of `dtype`: rows of num_heads (num_kv_heads)
+ *                     heads of head_dim contiguous elements, *_stride elements
+ *                     from one token's row to the next: at least the row, a
+ *                     multiple of head_dim (slices of a fused projection's
+ *                     rows, say).  out must not overlap them.
+ *   query_start_loc   device, int32 [num_seqs + 1], non-decreasing, first
+ *                     entry >= 0, last <= num_tokens; sequences may be empty
+ * scale must be > 0.  Computed on the tensor cores; scores, softmax and sums
+ * in binary32, the weights rounded to `dtype` before they multiply the values.
+ * Rows that a query does not attend -- later tokens of its sequence, other
+ * sequences, rows outside every sequence -- may hold anything, NaN included.
+ * Supported: f16 or bf16, head_dim 64 or 128, G <= 128; else
+ * PA_ERR_UNSUPPORTED.  A sequence whose start rows break the rules above sets
+ * PA_DEVERR_CONTEXT_LEN and is skipped.  No workspace.
+ */
+int pa_prompt_attention(void *out, const void *query, int64_t query_stride,
+                        const void *key, int64_t key_stride,
+                        const void *value, int64_t value_stride,
+                        const int32_t *query_start_loc, int32_t num_seqs, int32_t num_tokens,
+                        int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, int32_t dtype,
+                        float scale, void *stream);
+
+/*
  * Copy-on-write block copy, one launch for all pairs and layers.  For every
  * pair i and layer l, copies the K block (num_kv_heads * B * head_dim
  * elements) of k_caches[l] from physical block pairs[i][0] to pairs[i][1],

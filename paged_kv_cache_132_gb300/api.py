@@ -217,6 +217,70 @@ def prefill(query: torch.Tensor, query_start_loc: torch.Tensor, k_cache: torch.T
     return out
 
 
+def _require_here(*tensors: torch.Tensor) -> None:
+    """The library works on the current device: tensors of another one are refused."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if not t.is_cuda or t.device.index != dev:
+            raise ValueError("tensors must be on the current CUDA device")
+
+
+def _empty(shape: Sequence[int], dtype: torch.dtype, device: torch.device,
+           stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+    """An output that the call makes, from the memory of the stream that it is written on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _token_stride(t: torch.Tensor, name: str) -> int:
+    """Elements from one token's row of heads to the next; the heads of a token are contiguous."""
+    tokens, heads, d = t.shape
+    by_token, by_head, by_elem = t.stride()
+    if (by_elem != 1 and d > 1) or (by_head != d and heads > 1):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    if tokens <= 1:
+        return heads * d
+    if by_token < heads * d:
+        raise ValueError(f"{name}: rows of tokens must not overlap")
+    return by_token
+
+
+def prompt_attention(query: torch.Tensor, key: torch.Tensor, value: torch.Tensor, query_start_loc: torch.Tensor,
+                     scale: float, *, out: Optional[torch.Tensor] = None,
+                     stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Causal attention of whole packed prompts over themselves; returns
+    out [T][H][d] in the inputs' type (f16 or bf16).
+
+    Sequence s owns rows query_start_loc[s] .. query_start_loc[s+1]-1 of query
+    [T][H][d], key and value [T][Hkv][d]; its token i attends to its tokens
+    0 .. i.  The rows may be slices of a fused projection's rows (a token's
+    heads contiguous, the token stride a multiple of d).  Rows outside every
+    sequence are neither used nor written: a given ``out`` keeps them."""
+    lib = native.load()
+    _require(query.dim() == 3 and key.dim() == 3, "query is [num_tokens][num_heads][head_dim], key its KV heads")
+    t, h, d = query.shape
+    hkv = key.shape[1]
+    _require(key.shape == value.shape and key.shape[0] == t and key.shape[2] == d,
+             "key/value are [num_tokens][num_kv_heads][head_dim]")
+    _require(query.dtype in DTYPE_CODE and key.dtype == query.dtype and value.dtype == query.dtype,
+             "query, key and value share one dtype")
+    _require(query_start_loc.dtype == torch.int32 and query_start_loc.dim() == 1 and query_start_loc.numel() > 0
+             and query_start_loc.is_contiguous(), "query_start_loc is int32 [num_seqs + 1]")
+    if out is None:
+        out = _empty((t, h, d), query.dtype, query.device, stream)
+    _require(out.shape == query.shape and out.dtype == query.dtype and out.is_contiguous(),
+             "out is contiguous [num_tokens][num_heads][head_dim] of the inputs' dtype")
+    _require_here(query, key, value, query_start_loc, out)
+    _raise(lib.pa_prompt_attention(out.data_ptr(), query.data_ptr(), _token_stride(query, "query"), key.data_ptr(),
+                                   _token_stride(key, "key"), value.data_ptr(), _token_stride(value, "value"),
+                                   query_start_loc.data_ptr(), query_start_loc.numel() - 1, t, h, hkv, d,
+                                   DTYPE_CODE[query.dtype], float(scale), _stream_ptr(stream)),
+           "pa_prompt_attention")
+    return out
+
+
 def copy_blocks(k_caches: Sequence[torch.Tensor], v_caches: Sequence[torch.Tensor], src_dst_pairs: torch.Tensor,
                 stream: Optional[torch.cuda.Stream] = None) -> None:
     """Copy-on-write: copy K and V block pairs[i][0] -> pairs[i][1] in every layer."""

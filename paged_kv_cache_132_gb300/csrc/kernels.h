@@ -158,4 +158,25 @@ struct PrefillParams {
 cudaError_t launch_prefill(const PrefillParams& p, int dtype, int head_dim, const CUtensorMap* tmap_q,
                            const CUtensorMap* tmap_k, const CUtensorMap* tmap_v, cudaStream_t stream);
 
+// ---- attention over whole packed prompts (prompt*.cu) ---------------------------
+struct PromptParams {
+    void* out;                    // [num_tokens][num_heads][head_dim], the inputs' type
+    const int32_t* query_start;   // [num_seqs + 1] first row of each sequence
+    int num_seqs;
+    int num_tokens;               // rows of the query / key / value / output arrays
+    int num_heads;
+    int num_kv_heads;
+    int group;                    // num_heads / num_kv_heads, 1..128
+    int tile_tokens;              // tokens per query tile: 128 / group
+    float scale_log2;             // scale * log2(e), > 0
+    int* err;
+    unsigned long long wait_limit_ns;
+};
+
+// tmap_q, tmap_k, tmap_v: the rows as 3-D tensors {head_dim, heads, tokens} with
+// the 128-byte swizzle, box {64, group, tile_tokens} for q and {64, 1, 64} for k
+// and v.  sms: CTAs at most.  dtype PA_F16 or PA_BF16.
+cudaError_t launch_prompt(const PromptParams& p, int dtype, int head_dim, int sms, const CUtensorMap* tmap_q,
+                          const CUtensorMap* tmap_k, const CUtensorMap* tmap_v, cudaStream_t stream);
+
 }  // namespace pa

@@ -194,19 +194,19 @@ bool encode_pool_map(CUtensorMap* map, const void* base, int dtype, const pa::Po
     return r == CUDA_SUCCESS;
 }
 
-// The query [num_tokens][num_heads][d] as a 3-D tensor {d, heads, tokens};
-// a box is 64 elements x the G heads of one KV head x 128/G tokens, i.e. the
-// 128 rows (token, grouped head) of one prefill tile, 128 bytes each.
-bool encode_query_map(CUtensorMap* map, const void* base, int dtype, int num_tokens, int num_heads, int head_dim,
-                      int group) {
+// Rows [num_tokens][num_heads][d] of 16-bit elements, `token_stride` elements
+// from token to token, as a 3-D tensor {d, heads, tokens}; a box is 64 elements
+// x box_heads heads x box_tokens tokens, 128 bytes per (token, head) row.
+bool encode_rows_map(CUtensorMap* map, const void* base, int dtype, int num_tokens, int num_heads, int head_dim,
+                     int64_t token_stride, int box_heads, int box_tokens) {
     PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
     if (!encode || head_dim % 64 != 0) return false;
     const CUtensorMapDataType type =
         dtype == PA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     std::memset(map, 0, sizeof(*map));
     const cuuint64_t dims[3] = {(cuuint64_t)head_dim, (cuuint64_t)num_heads, (cuuint64_t)num_tokens};
-    const cuuint64_t strides[2] = {(cuuint64_t)head_dim * 2, (cuuint64_t)num_heads * head_dim * 2};
-    const cuuint32_t box[3] = {64, (cuuint32_t)group, (cuuint32_t)(128 / group)};
+    const cuuint64_t strides[2] = {(cuuint64_t)head_dim * 2, (cuuint64_t)token_stride * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_tokens};
     const cuuint32_t elem_strides[3] = {1, 1, 1};
     return encode(map, type, 3, const_cast<void*>(base), dims, strides, box, elem_strides,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -219,12 +219,13 @@ bool encode_query_map(CUtensorMap* map, const void* base, int dtype, int num_tok
 // the memory in between.  Kernel parameters are copied at launch, so the
 // returned pointer is only used before the next lookup on this thread.
 struct MapKey {
-    int kind;  // 0: pool, 2-D view; 1: pool, decode's view; 2: query
+    int kind;  // 0: pool, 2-D view; 1: pool, decode's view; 2: rows of tokens
     int dtype;
     const void* base;
-    int64_t a, b, c, d;
+    int64_t a, b, c, d, e, f;
     bool operator==(const MapKey& o) const {
-        return kind == o.kind && dtype == o.dtype && base == o.base && a == o.a && b == o.b && c == o.c && d == o.d;
+        return kind == o.kind && dtype == o.dtype && base == o.base && a == o.a && b == o.b && c == o.c &&
+               d == o.d && e == o.e && f == o.f;
     }
 };
 struct MapSlot {
@@ -251,7 +252,7 @@ MapSlot& next_map_slot() {
 
 const CUtensorMap* pool_map(const void* base, int dtype, const pa::PoolShape& shape, bool interleave) {
     const MapKey key{interleave ? 1 : 0, dtype, base, shape.num_blocks, shape.num_kv_heads, shape.block_size,
-                     shape.head_dim};
+                     shape.head_dim, 0, 0};
     if (const CUtensorMap* m = find_map(key)) return m;
     MapSlot& slot = next_map_slot();
     if (!encode_pool_map(&slot.map, base, dtype, shape, interleave)) return nullptr;
@@ -260,11 +261,13 @@ const CUtensorMap* pool_map(const void* base, int dtype, const pa::PoolShape& sh
     return &slot.map;
 }
 
-const CUtensorMap* query_map(const void* base, int dtype, int num_tokens, int num_heads, int head_dim, int group) {
-    const MapKey key{2, dtype, base, num_tokens, num_heads, head_dim, group};
+const CUtensorMap* rows_map(const void* base, int dtype, int num_tokens, int num_heads, int head_dim,
+                            int64_t token_stride, int box_heads, int box_tokens) {
+    const MapKey key{2, dtype, base, num_tokens, num_heads, head_dim, token_stride, box_heads, box_tokens};
     if (const CUtensorMap* m = find_map(key)) return m;
     MapSlot& slot = next_map_slot();
-    if (!encode_query_map(&slot.map, base, dtype, num_tokens, num_heads, head_dim, group)) return nullptr;
+    if (!encode_rows_map(&slot.map, base, dtype, num_tokens, num_heads, head_dim, token_stride, box_heads, box_tokens))
+        return nullptr;
     slot.key = key;
     slot.valid = true;
     return &slot.map;
@@ -512,7 +515,9 @@ int pa_prefill(void* out, int32_t out_dtype, const void* query, const int32_t* q
     p.wait_limit_ns = wait_limit_ns();
 
     CUtensorMap tmap_q, tmap_k, tmap_v;  // copies: later lookups may reuse a cache slot
-    const CUtensorMap* m = query_map(query, cache->dtype, num_query_tokens, num_heads, shape.head_dim, group);
+    // One prefill tile: 128 rows (token, grouped head).
+    const CUtensorMap* m = rows_map(query, cache->dtype, num_query_tokens, num_heads, shape.head_dim,
+                                    (int64_t)num_heads * shape.head_dim, group, 128 / group);
     if (!m) return PA_ERR_UNSUPPORTED;
     tmap_q = *m;
     if (!(m = pool_map(k_cache, cache->dtype, shape, false))) return PA_ERR_UNSUPPORTED;
@@ -521,6 +526,61 @@ int pa_prefill(void* out, int32_t out_dtype, const void* query, const int32_t* q
     tmap_v = *m;
     return status_of(pa::launch_prefill(p, cache->dtype, shape.head_dim, &tmap_q, &tmap_k, &tmap_v,
                                         static_cast<cudaStream_t>(stream)));
+}
+
+int pa_prompt_attention(void* out, const void* query, int64_t query_stride, const void* key, int64_t key_stride,
+                        const void* value, int64_t value_stride, const int32_t* query_start_loc, int32_t num_seqs,
+                        int32_t num_tokens, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, int32_t dtype,
+                        float scale, void* stream) {
+    NvtxRange range("pa_prompt_attention");
+    if (elem_bytes(dtype) == 0 || num_seqs < 0 || num_tokens < 0 || num_heads <= 0 || num_kv_heads <= 0 ||
+        num_heads % num_kv_heads != 0 || head_dim <= 0 || !std::isfinite(scale) || !(scale > 0.f))
+        return PA_ERR_INVALID_ARG;
+    const int64_t q_row = (int64_t)num_heads * head_dim, kv_row = (int64_t)num_kv_heads * head_dim;
+    if (query_stride < q_row || key_stride < kv_row || value_stride < kv_row || query_stride % head_dim != 0 ||
+        key_stride % head_dim != 0 || value_stride % head_dim != 0)
+        return PA_ERR_INVALID_ARG;
+    if (num_seqs == 0 || num_tokens == 0) return PA_OK;
+    if (!aligned(out, 16) || !aligned(query, 16) || !aligned(key, 16) || !aligned(value, 16) ||
+        !aligned(query_start_loc, 4))
+        return PA_ERR_INVALID_ARG;
+    if (dtype == PA_F32) return PA_ERR_UNSUPPORTED;
+    if (!(head_dim == 64 || head_dim == 128)) return PA_ERR_UNSUPPORTED;
+    const int group = num_heads / num_kv_heads;
+    if (group > 128) return PA_ERR_UNSUPPORTED;
+    constexpr int64_t kMaxStride = (1LL << 39) - 1;  // a tensor copy's strides are below 2^40 bytes
+    if (query_stride > kMaxStride || key_stride > kMaxStride || value_stride > kMaxStride) return PA_ERR_UNSUPPORTED;
+
+    const int dev = current_device();
+    if (dev < 0) return PA_ERR_CUDA;
+    int* err = error_word(dev);
+    const int sms = sm_count(dev);
+    if (!err || sms <= 0) return PA_ERR_CUDA;
+
+    pa::PromptParams p{};
+    p.out = out;
+    p.query_start = query_start_loc;
+    p.num_seqs = num_seqs;
+    p.num_tokens = num_tokens;
+    p.num_heads = num_heads;
+    p.num_kv_heads = num_kv_heads;
+    p.group = group;
+    p.tile_tokens = 128 / group;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.err = err;
+    p.wait_limit_ns = wait_limit_ns();
+
+    CUtensorMap tmap_q, tmap_k, tmap_v;  // copies: later lookups may reuse a cache slot
+    const CUtensorMap* m = rows_map(query, dtype, num_tokens, num_heads, head_dim, query_stride, group, p.tile_tokens);
+    if (!m) return PA_ERR_UNSUPPORTED;
+    tmap_q = *m;
+    if (!(m = rows_map(key, dtype, num_tokens, num_kv_heads, head_dim, key_stride, 1, 64))) return PA_ERR_UNSUPPORTED;
+    tmap_k = *m;
+    if (!(m = rows_map(value, dtype, num_tokens, num_kv_heads, head_dim, value_stride, 1, 64)))
+        return PA_ERR_UNSUPPORTED;
+    tmap_v = *m;
+    return status_of(pa::launch_prompt(p, dtype, head_dim, sms, &tmap_q, &tmap_k, &tmap_v,
+                                       static_cast<cudaStream_t>(stream)));
 }
 
 int pa_copy_blocks(void* const* k_caches, void* const* v_caches, int32_t num_layers, const int64_t* src_dst_pairs,

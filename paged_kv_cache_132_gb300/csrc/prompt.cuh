@@ -1,0 +1,753 @@
+// prompt.cuh -- causal attention over whole packed prompts on the Blackwell
+// tensor cores (tcgen05.mma, accumulators in tensor memory).
+//
+// What it computes, for token i and query head h of each packed sequence
+// (KV head h / G; "PagedAttention 论文精读笔记", §2.1 attention equation and
+// §5.3 prompt step, with keys and values still in the projections' rows):
+//     out[i][h] = sum_{j <= i} softmax_j(scale * q[i][h] . k_j) v_j
+//
+// Work item: 2 * (128 / G) consecutive tokens of one (sequence, KV head), as
+// two query tiles of 128 rows (row = token * G + grouped head), so both tiles
+// and all G heads use every K/V tile that is loaded.  One CTA per SM takes
+// items until none is left.  Keys and values stream through a ring of
+// 128-position tiles; per tile j and query tile i:
+//   S_i  = Q_i K_j^T      tcgen05.mma M=128 N=128 K=d, into TMEM
+//   P_i  = 2^(S_i c - m)  softmax warps, one thread per row; P_i, rounded to
+//                         the inputs' 16-bit type, is written over S_i
+//   O_i += P_i V_j        tcgen05.mma with A = P_i from TMEM
+// with c = scale * log2 e, the running maximum m in base-2 units, O_i rescaled
+// only when a row's maximum grows by more than 8 (a factor of 256), and row
+// sums in binary32 over the unrounded weights.  The rounding of P to 16 bits
+// costs as much as the rounding of the output that follows it (half a step of
+// the type on independent weights), and lets P.V run at the 16-bit rate.
+//
+// The two query tiles alternate on the tensor cores: while one's softmax runs,
+// the MMAs of the other (P V_j, then S of tile j + 1) are executed.
+//
+// Values a query must not see: a row's weights after its own position are 0,
+// but 0 * NaN is NaN on the tensor cores.  So before P.V reads a V tile that
+// holds positions some row of the item does not attend (the last one or two of
+// an item), two warps clear its rows after the item's last position and
+// replace non-finite elements by 0; those are added again, to the rows that do
+// attend them, by the output warps (an infinite or NaN term decides a sum
+// whatever its weight is).  Keys need no such care: masked scores are replaced.
+//
+// Warp roles (512 threads, registers moved between the groups by setmaxnreg):
+//   warps 0-3, 4-7   softmax of query tile 0 / 1
+//   warps 8-11       outputs: O_i / row sum, rounded once, written to memory
+//   warp 12          MMA issuer (one thread), owner of the TMEM allocation
+//   warp 13          work items, Q, K and V copies (TMA)
+//   warps 14, 15     the V tiles with masked positions (above)
+// Every wait is bounded; a wait that runs out sets PA_DEVERR_TIMEOUT and makes
+// every role of the CTA leave, after what it issued has landed.
+#pragma once
+
+#include <cuda.h>
+
+#include "attn_common.cuh"
+#include "common.cuh"
+#include "decode_common.cuh"  // kFullMask
+#include "kernels.h"
+#include "tcgen05.cuh"
+
+namespace pa {
+
+template <int D>
+struct PromptShape {
+    static constexpr int BM = 128;               // query rows per tile, two tiles per item
+    static constexpr int BN = 128;               // key/value positions per tile
+    static constexpr int HALF = 64;              // positions per K/V copy: a short last tile loads one half
+    static constexpr int SLABS = D / 64;         // 64-element (128-byte) column slabs of a row
+    static constexpr int SLAB = 128 * 128;       // bytes of one slab of 128 rows
+    static constexpr int NSLOT = D == 128 ? 5 : 8;  // K/V ring: K_0, V_0, K_1, V_1, ... one tile per slot
+    static constexpr int NITEM = 4;              // work items announced ahead of their last reader
+    static constexpr int SOFTMAX_WARPS = 4;      // per query tile
+    static constexpr int OUT_WARP = 8;           // first of four
+    static constexpr int MMA_WARP = 12;
+    static constexpr int LOAD_WARP = 13;
+    static constexpr int CHECK_WARP = 14;        // first of two
+    static constexpr int THREADS = 512;
+    static constexpr int ITEM_READERS = 8 + 4 + 1 + 2;  // softmax, output, MMA and check warps
+    // Registers per thread after the split: 256 * 192 + 128 * 64 + 128 * 64
+    // = 512 * 128, the launch's total.
+    static constexpr int REGS_SOFTMAX = 192, REGS_OUT = 64, REGS_OTHER = 64;
+    static_assert(256 * REGS_SOFTMAX + 128 * REGS_OUT + 128 * REGS_OTHER <= THREADS * 128, "register split");
+    // TMEM columns: S_i (and P_i over it, two per column) at 128 i, O_i after both.
+    static constexpr uint32_t TMEM_COLS = 512;
+    static constexpr uint32_t O_COL = 2 * BN;
+    static_assert(D == 64 || D == 128, "head_dim 64 or 128");
+
+    struct Smem {
+        alignas(1024) uint8_t q[2][SLABS][SLAB];
+        alignas(1024) uint8_t kv[NSLOT][SLABS][SLAB];
+        float row_sum[2][BM];
+        int4 item[NITEM];           // first row, length, item of the sequence, KV head; length 0: no more work
+        uint32_t dirty[2][4];       // V rows with non-finite elements, per masked tile of an item (128 bits each)
+        uint64_t item_full[NITEM];  // announced (load warp)
+        uint64_t item_empty[NITEM]; // read by every role
+        uint64_t q_full[2];         // Q_i landed
+        uint64_t q_empty[2];        // last S_i of the item complete
+        uint64_t kv_full[NSLOT];    // tile landed
+        uint64_t kv_empty[NSLOT];   // the MMAs that read it complete
+        uint64_t check_go[NSLOT];   // the copy of a V tile with masked positions was issued (load warp)
+        uint64_t v_checked[NSLOT];  // ... and the tile is fit for P.V (check warps)
+        uint64_t s_full[2];         // S_i complete
+        uint64_t p_full[2];         // P_i written (softmax warps)
+        uint64_t pv_done[2];        // P_i V_j complete
+        uint64_t o_full[2];         // last P_i V_j of the item complete
+        uint64_t l_full[2];         // row sums written (softmax warps)
+        uint64_t o_empty[2];        // O_i and the row sums read (output warps)
+        uint64_t mma_done;
+        uint32_t tmem_base;
+        int abort_flag;
+    };
+    static constexpr int SMEM_BYTES = (int)sizeof(Smem) + 1024;
+    static_assert(SMEM_BYTES <= 232448, "shared memory of one CTA");
+};
+
+// 2^x as exp2_approx (common.cuh), free to be moved by the compiler.
+__device__ __forceinline__ float prompt_exp2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint64_t desc_of(uint32_t lo, uint32_t hi) { return ((uint64_t)hi << 32) | lo; }
+
+template <uint32_t REGS>
+__device__ __forceinline__ void regs_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+template <uint32_t REGS>
+__device__ __forceinline__ void regs_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+
+// A wait that also ends when another role of the CTA gave up.
+__device__ __forceinline__ bool prompt_wait_slow(uint64_t* bar, uint32_t parity, int* abort_flag, uint64_t lim,
+                                                 int* err) {
+    const uint64_t start = global_timer_ns();
+    while (true) {
+        for (int i = 0; i < 64; ++i)
+            if (mbar_try_wait(bar, parity)) return true;
+        if (*reinterpret_cast<volatile int*>(abort_flag)) return false;
+        if (global_timer_ns() - start > lim) {
+            set_error(err, PA_DEVERR_TIMEOUT);
+            atomicExch(abort_flag, 1);
+            return false;
+        }
+    }
+}
+template <class Smem>
+__device__ __forceinline__ bool prompt_wait(const PromptParams& p, Smem& sm, uint64_t* bar, uint32_t parity) {
+    if (mbar_try_wait(bar, parity)) return true;
+    return prompt_wait_slow(bar, parity, &sm.abort_flag, p.wait_limit_ns, p.err);
+}
+// The same for a whole warp: every lane observes the barrier, all leave together.
+template <class Smem>
+__device__ __forceinline__ bool prompt_wait_warp(const PromptParams& p, Smem& sm, uint64_t* bar, uint32_t parity) {
+    return __all_sync(kFullMask, prompt_wait(p, sm, bar, parity));
+}
+
+// What an item is made of, for every role alike.
+struct PromptItem {
+    int row0;     // first row of the sequence
+    int len;      // its tokens
+    int kv_head;
+    int t0;       // first token of query tile 0; tile 1 starts tile_tokens later
+    int end0, end1;  // positions [0, end_i) are read by tile i; 0: the tile is empty
+    int first_masked;  // first K/V tile with a position some row does not attend
+    __device__ __forceinline__ int end(int i) const { return i ? end1 : end0; }
+    __device__ __forceinline__ int tiles(int i) const { return (end(i) + 127) >> 7; }  // its K/V tiles
+    __device__ __forceinline__ int last() const { return max(end0, end1); }
+};
+
+__device__ __forceinline__ PromptItem prompt_item(const int4& it, int tile_tokens) {
+    PromptItem w;
+    w.row0 = it.x;
+    w.len = it.y;
+    w.kv_head = it.w;
+    w.t0 = it.z * 2 * tile_tokens;
+    w.end0 = min(w.t0 + tile_tokens, w.len);
+    w.end1 = w.len > w.t0 + tile_tokens ? min(w.t0 + 2 * tile_tokens, w.len) : 0;
+    w.first_masked = w.t0 >> 7;
+    return w;
+}
+
+// Reader side of the item ring (one warp): the next item, or false at the end
+// of the work or of the kernel.
+template <class Shape>
+__device__ __forceinline__ bool prompt_next_item(const PromptParams& p, typename Shape::Smem& sm, int lane, int& n,
+                                                 PromptItem& w) {
+    const int st = n % Shape::NITEM;
+    if (!prompt_wait_warp(p, sm, &sm.item_full[st], (uint32_t)(n / Shape::NITEM) & 1u)) return false;
+    const int4 it = sm.item[st];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.item_empty[st]);
+    ++n;
+    if (it.y == 0) return false;
+    w = prompt_item(it, p.tile_tokens);
+    return true;
+}
+
+// ---------------------------------------------------------------------------
+// load warp: work items and copies
+// ---------------------------------------------------------------------------
+// Items are numbered sequence after sequence, the last query tiles (the
+// longest key ranges) of a sequence first, KV heads innermost, so that CTAs at
+// work together share keys and values in L2.  CTA c takes items c, c + grid,
+// ...; a warp finds an item's sequence by walking the start rows forward, 32
+// sequences at a time.
+struct PromptWalk {
+    int base;    // sequences [base, base + 32) are in the lanes
+    int64_t before;  // (sequence, query tile pair) units before them
+    int row0, len, nb, incl;  // this lane's sequence; inclusive sum of nb over the lanes
+};
+
+__device__ __forceinline__ void prompt_walk_load(const PromptParams& p, PromptWalk& k, int lane) {
+    const int s = k.base + lane;
+    k.row0 = k.len = 0;
+    if (s < p.num_seqs) {
+        const int a = __ldg(p.query_start + s), b = __ldg(p.query_start + s + 1);
+        if (a < 0 || b < a || b > p.num_tokens) {
+            set_error(p.err, PA_DEVERR_CONTEXT_LEN);
+        } else {
+            k.row0 = a;
+            k.len = b - a;
+        }
+    }
+    k.nb = (k.len + 2 * p.tile_tokens - 1) / (2 * p.tile_tokens);
+    k.incl = k.nb;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int up = __shfl_up_sync(kFullMask, k.incl, d);
+        if (lane >= d) k.incl += up;
+    }
+}
+
+// The item with number `index`; length 0 when there is none.
+__device__ __forceinline__ int4 prompt_walk_to(const PromptParams& p, PromptWalk& k, int lane, int64_t index) {
+    const int64_t unit = index / p.num_kv_heads;
+    while (true) {
+        const int total = __shfl_sync(kFullMask, k.incl, 31);
+        if (unit < k.before + total) break;
+        k.before += total;
+        k.base += 32;
+        if (k.base >= p.num_seqs) return make_int4(0, 0, 0, 0);
+        prompt_walk_load(p, k, lane);
+    }
+    const int u = (int)(unit - k.before);
+    const int src = __ffs(__ballot_sync(kFullMask, u < k.incl)) - 1;
+    const int row0 = __shfl_sync(kFullMask, k.row0, src), len = __shfl_sync(kFullMask, k.len, src);
+    const int incl = __shfl_sync(kFullMask, k.incl, src);
+    return make_int4(row0, len, incl - 1 - u, (int)(index - unit * p.num_kv_heads));
+}
+
+template <class Shape>
+__device__ void prompt_load(const PromptParams& p, typename Shape::Smem& sm, int lane, const CUtensorMap* tq,
+                            const CUtensorMap* tk, const CUtensorMap* tv) {
+    constexpr int HALF_BYTES = Shape::HALF * 128;
+    const uint32_t q_bytes = (uint32_t)(Shape::SLABS * p.tile_tokens * p.group * 128);
+    uint32_t q_used[2] = {0, 0};  // items that loaded Q_i
+    uint32_t slot = 0, round = 0, filled = 0;
+    bool ok = true;
+    // One K or V tile of `rows` positions (rounded up to whole halves).
+    auto load_tile = [&](const CUtensorMap* map, const PromptItem& w, int j, int end, bool check) {
+        if (!ok) return;
+        ok = prompt_wait(p, sm, &sm.kv_empty[slot], (round & 1u) ^ 1u);
+        if (!ok) return;
+        const int halves = end - j * Shape::BN > Shape::HALF ? 2 : 1;
+        mbar_arrive_expect_tx(&sm.kv_full[slot], (uint32_t)(halves * Shape::SLABS * HALF_BYTES));
+        for (int h = 0; h < halves; ++h)
+#pragma unroll
+            for (int s = 0; s < Shape::SLABS; ++s)
+                tma_load_3d_plain(sm.kv[slot][s] + h * HALF_BYTES, map, s * 64, w.kv_head,
+                                  w.row0 + j * Shape::BN + h * Shape::HALF, &sm.kv_full[slot]);
+        filled |= 1u << slot;
+        if (check) mbar_arrive(&sm.check_go[slot]);
+        if (++slot == Shape::NSLOT) {
+            slot = 0;
+            ++round;
+        }
+    };
+    auto load_q = [&](const PromptItem& w, int i) {
+        if (!ok) return;
+        ok = prompt_wait(p, sm, &sm.q_empty[i], (q_used[i] & 1u) ^ 1u);
+        if (!ok) return;
+        mbar_arrive_expect_tx(&sm.q_full[i], q_bytes);
+#pragma unroll
+        for (int s = 0; s < Shape::SLABS; ++s)
+            tma_load_3d_plain(sm.q[i][s], tq, s * 64, w.kv_head * p.group, w.row0 + w.t0 + i * p.tile_tokens,
+                              &sm.q_full[i]);
+        ++q_used[i];
+    };
+
+    PromptWalk walk{};
+    prompt_walk_load(p, walk, lane);
+    int64_t index = blockIdx.x;
+    for (int n = 0;; ++n, index += gridDim.x) {
+        const int4 it = prompt_walk_to(p, walk, lane, index);
+        const int st = n % Shape::NITEM;
+        if (!prompt_wait_warp(p, sm, &sm.item_empty[st], ((uint32_t)(n / Shape::NITEM) & 1u) ^ 1u)) break;
+        if (lane == 0) {
+            sm.item[st] = it;
+            mbar_arrive(&sm.item_full[st]);
+        }
+        if (it.y == 0) break;
+        if (lane == 0) {
+            const PromptItem w = prompt_item(it, p.tile_tokens);
+            const int end = w.last(), nt = (end + 127) >> 7;
+            load_q(w, 0);
+            load_tile(tk, w, 0, end, false);
+            if (w.end1) load_q(w, 1);
+            load_tile(tv, w, 0, end, w.first_masked == 0);
+            for (int j = 1; j < nt && ok; ++j) {
+                load_tile(tk, w, j, end, false);
+                load_tile(tv, w, j, end, j >= w.first_masked);
+            }
+        }
+        if (!__shfl_sync(kFullMask, ok, 0)) break;
+    }
+    pdl_launch_dependents();
+    // Every copy this warp issued lands before the CTA exits (bounded).
+    if (lane == 0) {
+        bool drained = true;
+        for (int i = 0; i < 2; ++i)
+            if (q_used[i]) drained = mbar_wait_bounded(&sm.q_full[i], (q_used[i] & 1u) ^ 1u, p.wait_limit_ns) && drained;
+        for (uint32_t s = 0; s < Shape::NSLOT; ++s)
+            if (filled & (1u << s))
+                drained = mbar_wait_bounded(&sm.kv_full[s], (s < slot ? round : round - 1) & 1u, p.wait_limit_ns) &&
+                          drained;
+        if (!drained) set_error(p.err, PA_DEVERR_TIMEOUT);
+    }
+    __syncwarp();
+}
+
+// ---------------------------------------------------------------------------
+// MMA issuer (one warp; lane 0 issues)
+// ---------------------------------------------------------------------------
+template <class Shape, bool BF16>
+__device__ void prompt_mma(const PromptParams& p, typename Shape::Smem& sm, uint32_t tmem, int lane) {
+    constexpr int D = Shape::SLABS * 64;
+    constexpr uint32_t IDESC_S = mma_idesc_f16(BF16, false, Shape::BM, 0);  // N is added per tile
+    constexpr uint32_t IDESC_O = mma_idesc_f16(BF16, true, Shape::BM, D);
+    // All operands share the upper half of their descriptors; the lower half
+    // (address / 16, leading offset) fits 32-bit arithmetic: every address is
+    // below 2^18, so a step of it never carries out of its 14 bits.
+    constexpr uint32_t SLOT16 = sizeof(sm.kv[0]) >> 4, Q16 = sizeof(sm.q[0]) >> 4;
+    const uint64_t dq = smem_desc_sw128(smem_addr(sm.q[0][0]), 16, 1024);
+    const uint64_t dk = smem_desc_sw128(smem_addr(sm.kv[0][0]), 16, 1024);
+    const uint64_t dv = smem_desc_sw128(smem_addr(sm.kv[0][0]), Shape::SLAB, 1024);
+    const uint32_t hi = (uint32_t)(dq >> 32);
+
+    // S_i = Q_i K^T over the first `cols` (a multiple of 16) positions of the tile.
+    auto issue_s = [&](int i, uint32_t slot, int cols) {
+        const uint32_t idesc = IDESC_S | ((uint32_t)(cols >> 3) << 17);
+        uint32_t a = (uint32_t)dq + i * Q16, b = (uint32_t)dk + slot * SLOT16;
+        asm volatile("" : "+r"(a), "+r"(b));  // the 2 * 8 sums stay out of the registers of the loop
+#pragma unroll
+        for (int ks = 0; ks < Shape::SLABS * 4; ++ks) {
+            const uint32_t off = (uint32_t)((ks >> 2) * (Shape::SLAB >> 4) + (ks & 3) * 2);
+            mma_f16_ss(tmem + i * Shape::BN, desc_of(a + off, hi), desc_of(b + off, hi), idesc, ks > 0 ? 1u : 0u);
+        }
+        mma_commit(&sm.s_full[i]);
+    };
+    // O_i (+)= P_i V over the same positions.
+    auto issue_pv = [&](int i, uint32_t slot, int cols, bool first) {
+        uint32_t a = tmem + i * Shape::BN, b = (uint32_t)dv + slot * SLOT16;
+        const uint32_t o = tmem + Shape::O_COL + i * D;
+        asm volatile("" : "+r"(a), "+r"(b));
+#pragma unroll
+        for (int ks = 0; ks < Shape::BN / 16; ++ks)
+            if (ks * 16 < cols)
+                mma_f16_ts(o, a + ks * 8, desc_of(b + ks * 128, hi), IDESC_O, (ks > 0 || !first) ? 1u : 0u);
+        mma_commit(&sm.pv_done[i]);
+    };
+    auto cols_of = [](int end, int j) { return min(Shape::BN, (end - j * Shape::BN + 15) & ~15); };
+
+    uint32_t slot = 0, round = 0;    // ring position of the next tile
+    uint32_t used[2] = {0, 0};       // items of tile i so far
+    uint32_t np[2] = {0, 0};         // P_i so far
+    uint32_t checked = 0;            // per slot: parity of its next checked V tile
+    auto advance = [&] {
+        if (++slot == Shape::NSLOT) {
+            slot = 0;
+            ++round;
+        }
+    };
+    int n = 0;
+    PromptItem w;
+    while (prompt_next_item<Shape>(p, sm, lane, n, w)) {
+        bool ok = true;
+        if (lane == 0) {
+            const int nt = (w.last() + 127) >> 7;
+            ok = prompt_wait(p, sm, &sm.kv_full[slot], round & 1u);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (!ok || !w.end(i)) continue;
+                ok = prompt_wait(p, sm, &sm.q_full[i], used[i] & 1u);
+                if (!ok) continue;
+                tc_fence_after_sync();
+                issue_s(i, slot, cols_of(w.end(i), 0));
+                if (w.tiles(i) == 1) mma_commit(&sm.q_empty[i]);
+            }
+            if (ok) mma_commit(&sm.kv_empty[slot]);
+            advance();
+            for (int j = 0; j < nt && ok; ++j) {
+                const uint32_t vslot = slot, vround = round;
+                advance();
+                const uint32_t kslot = slot, kround = round;
+                const bool more = j + 1 < nt;
+                if (more) advance();
+                if (j >= w.first_masked) {
+                    ok = prompt_wait(p, sm, &sm.v_checked[vslot], (checked >> vslot) & 1u);
+                    checked ^= 1u << vslot;
+                } else {
+                    ok = prompt_wait(p, sm, &sm.kv_full[vslot], vround & 1u);
+                }
+                bool k_ready = false;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int nti = w.tiles(i);
+                    if (!ok || j >= nti) continue;
+                    if (j == 0) ok = prompt_wait(p, sm, &sm.o_empty[i], (used[i] & 1u) ^ 1u);
+                    if (ok) ok = prompt_wait(p, sm, &sm.p_full[i], np[i] & 1u);
+                    if (!ok) continue;
+                    ++np[i];
+                    tc_fence_after_sync();
+                    issue_pv(i, vslot, cols_of(w.end(i), j), j == 0);
+                    if (j + 1 == nti) {
+                        mma_commit(&sm.o_full[i]);
+                    } else {
+                        if (!k_ready) {
+                            ok = prompt_wait(p, sm, &sm.kv_full[kslot], kround & 1u);
+                            k_ready = true;
+                            if (!ok) continue;
+                            tc_fence_after_sync();
+                        }
+                        issue_s(i, kslot, cols_of(w.end(i), j + 1));
+                        if (j + 2 == nti) mma_commit(&sm.q_empty[i]);
+                    }
+                }
+                if (ok) {
+                    mma_commit(&sm.kv_empty[vslot]);
+                    if (more) mma_commit(&sm.kv_empty[kslot]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (w.end(i)) ++used[i];
+        }
+        if (!__shfl_sync(kFullMask, ok, 0)) break;
+    }
+    // Nothing this thread issued may still be running when TMEM is released.
+    if (lane == 0) {
+        mma_commit(&sm.mma_done);
+        if (!mbar_wait_bounded(&sm.mma_done, 0, p.wait_limit_ns)) set_error(p.err, PA_DEVERR_TIMEOUT);
+    }
+    __syncwarp();
+}
+
+// ---------------------------------------------------------------------------
+// softmax warps of query tile i (thread r = row r = TMEM lane r)
+// ---------------------------------------------------------------------------
+// One K/V tile: P over S, the running maximum and sum.  MASKED: the tile holds
+// positions after some row's own, or fewer than 128 of the item's.
+template <typename T, bool MASKED>
+__device__ __forceinline__ void prompt_softmax_tile(uint32_t s_addr, float c, int last, int cols, float& m, float& l,
+                                                    float& alpha, bool& grow) {
+    constexpr int BN = 128;
+    const float NEG_INF = __int_as_float(0xff800000);
+    float x[BN];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if (!MASKED || h * 64 < cols) {
+            uint32_t u[64];
+            tmem_ld_x64(s_addr + h * 64, u);
+#pragma unroll
+            for (int k = 0; k < 64; ++k) x[h * 64 + k] = __uint_as_float(u[k]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 64; ++k) x[h * 64 + k] = NEG_INF;
+        }
+    }
+    if (MASKED) {
+#pragma unroll
+        for (int k = 0; k < BN; ++k) x[k] = k <= last ? x[k] : NEG_INF;
+    }
+    float pm[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) pm[q] = fmaxf(x[q], x[q + 8]);
+#pragma unroll
+    for (int k = 16; k < BN; k += 16)
+#pragma unroll
+        for (int q = 0; q < 8; ++q) pm[q] = fmaxf(fmaxf(pm[q], x[k + q]), x[k + 8 + q]);
+    const float mx =
+        fmaxf(fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])), fmaxf(fmaxf(pm[4], pm[5]), fmaxf(pm[6], pm[7])));
+    const float m_new = fmaxf(m, mx * c);
+    grow = m_new > m + 8.f;  // always on the first tile (m = -inf)
+    alpha = 1.f;
+    if (grow) {
+        alpha = prompt_exp2(m - m_new);
+        m = m_new;
+        l *= alpha;
+    }
+    const float nm = -m;
+    float ps[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) ps[q] = 0.f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if (MASKED && h * 64 >= cols) break;
+        uint32_t u[32];
+#pragma unroll
+        for (int k = 0; k < 64; k += 2) {
+            float& a = x[h * 64 + k];
+            float& b = x[h * 64 + k + 1];
+            fma2_rn(a, b, c, c, nm, nm);
+            a = prompt_exp2(a);
+            b = prompt_exp2(b);
+            add2_rn(ps[k & 7], ps[(k & 7) + 1], a, b);
+            u[k >> 1] = pack_rn<T>(a, b);
+        }
+        tmem_st_x32_async(s_addr + h * 32, u);
+    }
+    l += ((ps[0] + ps[1]) + (ps[2] + ps[3])) + ((ps[4] + ps[5]) + (ps[6] + ps[7]));
+}
+
+template <typename T, class Shape>
+__device__ void prompt_softmax(const PromptParams& p, typename Shape::Smem& sm, uint32_t tmem, int i, int warp,
+                               int lane) {
+    constexpr int D = Shape::SLABS * 64;
+    const int r = warp * 32 + lane;
+    const int t = r / p.group;
+    const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+    const uint32_t s_addr = tmem + lanes + i * Shape::BN, o_addr = tmem + lanes + Shape::O_COL + i * D;
+    const float c = p.scale_log2;  // > 0
+    uint32_t ns = 0, used = 0;     // S_i and items so far
+    int n = 0;
+    PromptItem w;
+    while (prompt_next_item<Shape>(p, sm, lane, n, w)) {
+        const int end = w.end(i), nt = w.tiles(i);
+        if (!nt) continue;
+        const int token = w.t0 + i * p.tile_tokens + t;
+        // Rows past the tile's tokens compute something and are not stored.
+        const int last = t < p.tile_tokens && token < w.len ? token : end - 1;
+        float m = __int_as_float(0xff800000), l = 0.f;
+        bool ok = true;
+        for (int j = 0; j < nt && ok; ++j, ++ns) {
+            ok = prompt_wait_warp(p, sm, &sm.s_full[i], ns & 1u);
+            if (!ok) break;
+            tc_fence_after_sync();
+            float alpha;
+            bool grow;
+            if (j >= w.first_masked) {
+                const int kv0 = j * Shape::BN;
+                prompt_softmax_tile<T, true>(s_addr, c, last - kv0, end - kv0, m, l, alpha, grow);
+            } else {
+                prompt_softmax_tile<T, false>(s_addr, c, 0, 0, m, l, alpha, grow);
+            }
+            // A grown maximum rescales O_i, once P_i V of the previous tile has completed.
+            if (j > 0 && __any_sync(kFullMask, grow)) {
+                ok = prompt_wait_warp(p, sm, &sm.pv_done[i], (ns - 1) & 1u);
+                if (!ok) break;
+                tc_fence_after_sync();
+#pragma unroll 1
+                for (int c0 = 0; c0 < D; c0 += 32) {
+                    uint32_t u[32];
+                    tmem_ld_x32(o_addr + c0, u);
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) u[k] = __float_as_uint(__uint_as_float(u[k]) * alpha);
+                    tmem_st_x32(o_addr + c0, u);
+                }
+            }
+            tmem_wait_st();
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.p_full[i]);
+        }
+        if (!ok) break;
+        // The row sums, once the output warps have read the previous item's.
+        if (!prompt_wait_warp(p, sm, &sm.o_empty[i], (used & 1u) ^ 1u)) break;
+        ++used;
+        sm.row_sum[i][r] = l;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.l_full[i]);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// check warps: V tiles with masked positions
+// ---------------------------------------------------------------------------
+// 16-bit words whose exponent bits are all ones (infinities and NaN), as a
+// mask of their sign positions; exp_mask is the type's exponent field twice.
+template <typename T>
+__device__ __forceinline__ uint32_t nonfinite2(uint32_t w) {
+    if constexpr (std::is_same<T, __nv_bfloat16>::value)
+        return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+    else
+        return ((w & 0x7c007c00u) + 0x04000400u) & 0x80008000u;
+}
+
+template <typename T, class Shape>
+__device__ void prompt_check(const PromptParams& p, typename Shape::Smem& sm, int thread) {
+    constexpr int CHUNKS = Shape::SLABS * 8;  // 16-byte chunks of a row
+    const int lane = thread & 31;
+    uint32_t tiles = 0;   // ring tiles before the item
+    uint32_t parity = 0;  // per slot: of its next masked V tile
+    int n = 0;
+    PromptItem w;
+    while (prompt_next_item<Shape>(p, sm, lane, n, w)) {
+        const int end = w.last(), nt = (end + 127) >> 7;
+        bool ok = true;
+        for (int j = w.first_masked; j < nt && ok; ++j) {
+            const uint32_t tile = tiles + 2 * j + 1;  // K_0, V_0, K_1, ...
+            const uint32_t slot = tile % Shape::NSLOT;
+            // Issued first: before that the slot's barrier may still be two
+            // phases back, which its parity does not tell from complete.
+            ok = prompt_wait_warp(p, sm, &sm.check_go[slot], (parity >> slot) & 1u) &&
+                 prompt_wait_warp(p, sm, &sm.kv_full[slot], (tile / Shape::NSLOT) & 1u);
+            if (!ok) break;
+            parity ^= 1u << slot;
+            const int rows = min(Shape::BN, end - j * Shape::BN), rows16 = (rows + 15) & ~15;
+            for (int idx = thread; idx < rows16 * CHUNKS; idx += 64) {
+                const int row = idx / CHUNKS, chunk = idx % CHUNKS;
+                uint4* at = reinterpret_cast<uint4*>(sm.kv[slot][chunk >> 3] + row * 128) + (chunk & 7);
+                if (row >= rows) *at = make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.v_checked[slot]);
+        }
+        if (!ok) break;
+        tiles += 2 * nt;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// output warps
+// ---------------------------------------------------------------------------
+template <typename T, class Shape>
+__device__ void prompt_output(const PromptParams& p, typename Shape::Smem& sm, uint32_t tmem, int warp, int lane) {
+    constexpr int D = Shape::SLABS * 64;
+    const int r = warp * 32 + lane;
+    const int t = r / p.group, g = r - t * p.group;
+    const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+    uint32_t parity = 0;  // bit i: of the next O_i
+    int n = 0;
+    PromptItem w;
+    while (prompt_next_item<Shape>(p, sm, lane, n, w)) {
+        bool ok = true;
+#pragma unroll 1
+        for (int i = 0; i < 2; ++i) {
+            if (!w.end(i)) continue;
+            ok = prompt_wait_warp(p, sm, &sm.l_full[i], (parity >> i) & 1u) &&
+                 prompt_wait_warp(p, sm, &sm.o_full[i], (parity >> i) & 1u);
+            if (!ok) break;
+            parity ^= 1u << i;
+            tc_fence_after_sync();
+            const float l = sm.row_sum[i][r];
+            const float inv = 1.f / l;  // l > 0: every row attends its own position (NaN stays NaN)
+            const int token = w.t0 + i * p.tile_tokens + t;
+            const bool store = t < p.tile_tokens && token < w.len;
+            T* dst = static_cast<T*>(p.out) +
+                     ((int64_t)(w.row0 + token) * p.num_heads + (int64_t)w.kv_head * p.group + g) * D;
+#pragma unroll 1
+            for (int c0 = 0; c0 < D; c0 += 32) {
+                uint32_t u[32];
+                tmem_ld_x32(tmem + lanes + Shape::O_COL + i * D + c0, u);
+                if (c0 + 32 == D) {
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.o_empty[i]);
+                }
+                if (store) {
+#pragma unroll
+                    for (int k = 0; k < 32; k += 8) {
+                        uint4 q;
+                        q.x = pack_rn<T>(__uint_as_float(u[k]) * inv, __uint_as_float(u[k + 1]) * inv);
+                        q.y = pack_rn<T>(__uint_as_float(u[k + 2]) * inv, __uint_as_float(u[k + 3]) * inv);
+                        q.z = pack_rn<T>(__uint_as_float(u[k + 4]) * inv, __uint_as_float(u[k + 5]) * inv);
+                        q.w = pack_rn<T>(__uint_as_float(u[k + 6]) * inv, __uint_as_float(u[k + 7]) * inv);
+                        *reinterpret_cast<uint4*>(dst + c0 + k) = q;
+                    }
+                }
+            }
+        }
+        if (!ok) break;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// the kernel: one CTA per SM
+// ---------------------------------------------------------------------------
+template <typename T, int D>
+__global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
+    prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap tmap_q,
+                  const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v) {
+    using Shape = PromptShape<D>;
+    using Smem = typename Shape::Smem;
+    extern __shared__ uint8_t prompt_smem_raw[];
+    const uintptr_t a = reinterpret_cast<uintptr_t>(prompt_smem_raw);
+    Smem& sm = *reinterpret_cast<Smem*>((a + 1023) & ~uintptr_t(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        prefetch_tensormap(&tmap_q);
+        prefetch_tensormap(&tmap_k);
+        prefetch_tensormap(&tmap_v);
+        for (int s = 0; s < Shape::NITEM; ++s) {
+            mbar_init(&sm.item_full[s], 1);
+            mbar_init(&sm.item_empty[s], Shape::ITEM_READERS);
+        }
+        for (int s = 0; s < Shape::NSLOT; ++s) {
+            mbar_init(&sm.kv_full[s], 1);
+            mbar_init(&sm.kv_empty[s], 1);
+            mbar_init(&sm.check_go[s], 1);
+            mbar_init(&sm.v_checked[s], 2);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm.q_full[i], 1);
+            mbar_init(&sm.q_empty[i], 1);
+            mbar_init(&sm.s_full[i], 1);
+            mbar_init(&sm.p_full[i], Shape::SOFTMAX_WARPS);
+            mbar_init(&sm.pv_done[i], 1);
+            mbar_init(&sm.o_full[i], 1);
+            mbar_init(&sm.l_full[i], Shape::SOFTMAX_WARPS);
+            mbar_init(&sm.o_empty[i], 4);
+        }
+        mbar_init(&sm.mma_done, 1);
+        sm.abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == Shape::MMA_WARP) tmem_alloc(&sm.tmem_base, Shape::TMEM_COLS);
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = sm.tmem_base;
+    // The kernel that wrote the start rows, q, k and v may still be finishing.
+    pdl_wait_prerequisites();
+
+    if (warp < 8) {
+        regs_inc<Shape::REGS_SOFTMAX>();
+        prompt_softmax<T, Shape>(p, sm, tmem, warp >> 2, warp & 3, lane);
+    } else if (warp < Shape::MMA_WARP) {
+        regs_dec<Shape::REGS_OUT>();
+        prompt_output<T, Shape>(p, sm, tmem, warp - Shape::OUT_WARP, lane);
+    } else {
+        regs_dec<Shape::REGS_OTHER>();
+        if (warp == Shape::MMA_WARP)
+            prompt_mma<Shape, std::is_same<T, __nv_bfloat16>::value>(p, sm, tmem, lane);
+        else if (warp == Shape::LOAD_WARP)
+            prompt_load<Shape>(p, sm, lane, &tmap_q, &tmap_k, &tmap_v);
+        else
+            prompt_check<T, Shape>(p, sm, threadIdx.x - Shape::CHECK_WARP * 32);
+    }
+
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    if (warp == Shape::MMA_WARP) tmem_dealloc(tmem, Shape::TMEM_COLS);
+}
+
+}  // namespace pa

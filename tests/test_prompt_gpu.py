@@ -1,0 +1,122 @@
+"""Attention over whole packed prompts against its definition in 64 bits.
+
+Tolerance, per element, with u half a step of the type (bf16 2^-8, f16 2^-11)
+and A = sum_j p_j |v_j| the weighted sum of the values' magnitudes:
+  u A       the weights' rounding to the type
+  u |o|     the output's rounding
+  2 delta A relative error of a weight, and of their sum, from the scores: a dot
+            product in binary32 is off by at most d 2^-23 sum |q_e k_e| (each of
+            d additions rounded or truncated), the exponent's argument by 2^-23
+            of its magnitude, the hardware's 2^x by 2^-22
+  n 2^-25 max|v|  f16 only: weights below 2^-14 of the row's reference are
+            subnormal and off by up to 2^-25
+"""
+import pytest
+import torch
+
+from paged_kv_cache_132_gb300 import api, native
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _library():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    native.load()
+
+
+def starts(lens, first=0):
+    return torch.tensor([first] + lens).cumsum(0).to(torch.int32).cuda()
+
+
+def rows(tokens, h, hkv, d, dtype, seed, fused=False):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = torch.randn(tokens, (h + 2 * hkv) * d, generator=g, device="cuda").to(dtype)
+    q, k, v = (y.unflatten(1, (-1, d)) for y in x.split([h * d, hkv * d, hkv * d], dim=1))
+    return (q, k, v) if fused else (q.contiguous(), k.contiguous(), v.contiguous())
+
+
+def exact(q, k, v, scale):
+    """(out, tolerance) of one sequence, float64."""
+    n, h, d = q.shape
+    g = h // k.shape[1]
+    u = torch.finfo(q.dtype).eps / 2
+    q64 = q.double().transpose(0, 1)
+    k64 = k.double().transpose(0, 1).repeat_interleave(g, 0)
+    v64 = v.double().transpose(0, 1).repeat_interleave(g, 0)
+    z = q64 @ k64.transpose(1, 2) * scale
+    zabs = q64.abs() @ k64.abs().transpose(1, 2) * scale
+    future = torch.ones(n, n, dtype=torch.bool, device="cuda").triu(1)
+    p = torch.softmax(z.masked_fill(future, float("-inf")), -1)
+    out, a = p @ v64, p @ v64.abs()
+    spread = z.masked_fill(future, 0).abs().amax(-1, keepdim=True)
+    delta = (d * 2.0 ** -23 * zabs.masked_fill(future, 0)).amax(-1, keepdim=True) + 2.0 ** -22 + 3 * 2.0 ** -23 * spread
+    tol = u * (a + out.abs()) * 1.01 + 2 * delta * a
+    if q.dtype == torch.float16:
+        tol = tol + n * 2.0 ** -25 * v64.abs().amax() + 2.0 ** -25
+    return out.transpose(0, 1), tol.transpose(0, 1)
+
+
+def check(q, k, v, lens, scale, out, first=0):
+    at = first
+    for n in lens:
+        if n:
+            ref, tol = exact(q[at:at + n], k[at:at + n], v[at:at + n], scale)
+            off = (out[at:at + n].double() - ref).abs() - tol
+            assert not torch.isnan(out[at:at + n]).any(), f"NaN in a sequence of {n}"
+            assert float(off.max()) <= 0, f"sequence of {n}: {float(off.max())} over its tolerance"
+        at += n
+
+
+def run(lens, h, hkv, d, dtype, seed=1, fused=False, scale=None, extra=0, first=0):
+    tokens = first + sum(lens) + extra
+    q, k, v = rows(tokens, h, hkv, d, dtype, seed, fused)
+    scale = d ** -0.5 if scale is None else scale
+    out = torch.full((tokens, h, d), 7.0, dtype=dtype, device="cuda")
+    got = api.prompt_attention(q, k, v, starts(lens, first), scale, out=out)
+    assert got is out
+    assert api.get_device_error() == (0, 0)
+    check(q, k, v, lens, scale, out, first)
+    end = first + sum(lens)
+    assert bool((out[:first] == 7).all()) and bool((out[end:] == 7).all()), "rows outside the sequences were written"
+    return q, k, v, out
+
+
+@pytest.mark.parametrize("n", [1, 2, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129, 191, 192, 255, 256, 257, 500])
+@pytest.mark.parametrize("h,hkv,d,dtype", [(8, 2, 64, torch.bfloat16), (4, 4, 128, torch.float16)])
+def test_one_sequence(n, h, hkv, d, dtype):
+    run([n], h, hkv, d, dtype, seed=n)
+
+
+@pytest.mark.parametrize("h,hkv", [(1, 1), (8, 8), (4, 2), (6, 2), (8, 2), (5, 1), (14, 2), (8, 1), (16, 1), (32, 1),
+                                   (71, 1), (128, 1)])
+@pytest.mark.parametrize("d,dtype", [(64, torch.float16), (128, torch.bfloat16)])
+def test_groups(h, hkv, d, dtype):
+    run([77, 0, 1, 300, 129, 64], h, hkv, d, dtype, seed=h, fused=True, extra=3, first=2)
+
+
+def test_many_sequences_and_empty_ones():
+    g = torch.Generator().manual_seed(5)
+    lens = (torch.randint(0, 70, (300,), generator=g) * torch.randint(0, 2, (300,), generator=g)).tolist()
+    run(lens, 16, 8, 64, torch.bfloat16, fused=True, extra=200)
+
+
+def test_all_sequences_empty():
+    run([0] * 40, 8, 2, 64, torch.bfloat16, extra=9)
+
+
+@pytest.mark.parametrize("h,hkv,d,dtype", [(4, 1, 128, torch.bfloat16), (2, 2, 64, torch.float16)])
+def test_long(h, hkv, d, dtype):
+    run([2500, 4097], h, hkv, d, dtype)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_growing_scores(dtype):
+    """Later keys score higher and higher: the running maximum grows in every tile."""
+    n, h, d = 900, 4, 128
+    q, k, v = rows(n, h, h, d, dtype, 3)
+    ramp = torch.linspace(0.02, 6.0, n, device="cuda")[:, None, None]
+    q, k = q.abs().to(dtype), (k.abs() * ramp).to(dtype)
+    out = api.prompt_attention(q, k, v, starts([n]), d ** -0.5)
+    assert api.get_device_error() == (0, 0)
+    check(q, k, v, [n], d ** -0.5, out)
