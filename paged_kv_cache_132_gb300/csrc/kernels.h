@@ -161,6 +161,8 @@ cudaError_t launch_prefill(const PrefillParams& p, int dtype, int head_dim, cons
 // ---- attention over whole packed prompts (prompt*.cu) ---------------------------
 struct PromptParams {
     void* out;                    // [num_tokens][num_heads][head_dim], the inputs' type
+    const void* value;            // the values' rows (tmap_v), value_stride elements from token to token
+    int64_t value_stride;
     const int32_t* query_start;   // [num_seqs + 1] first row of each sequence
     int num_seqs;
     int num_tokens;               // rows of the query / key / value / output arrays

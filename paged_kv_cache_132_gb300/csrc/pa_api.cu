@@ -559,6 +559,8 @@ int pa_prompt_attention(void* out, const void* query, int64_t query_stride, cons
 
     pa::PromptParams p{};
     p.out = out;
+    p.value = value;
+    p.value_stride = value_stride;
     p.query_start = query_start_loc;
     p.num_seqs = num_seqs;
     p.num_tokens = num_tokens;

@@ -82,7 +82,7 @@ struct PromptShape {
         alignas(1024) uint8_t kv[NSLOT][SLABS][SLAB];
         float row_sum[2][BM];
         int4 item[NITEM];           // first row, length, item of the sequence, KV head; length 0: no more work
-        uint32_t dirty[2][4];       // V rows with non-finite elements, per masked tile of an item (128 bits each)
+        int last_dirty;             // latest item with non-finite values in its checked tiles
         uint64_t item_full[NITEM];  // announced (load warp)
         uint64_t item_empty[NITEM]; // read by every role
         uint64_t q_full[2];         // Q_i landed
@@ -579,8 +579,8 @@ __device__ void prompt_softmax(const PromptParams& p, typename Shape::Smem& sm, 
 // ---------------------------------------------------------------------------
 // check warps: V tiles with masked positions
 // ---------------------------------------------------------------------------
-// 16-bit words whose exponent bits are all ones (infinities and NaN), as a
-// mask of their sign positions; exp_mask is the type's exponent field twice.
+// Not 0 where a 16-bit half of w is infinite or NaN: an exponent of all ones
+// carries into the half's sign bit.
 template <typename T>
 __device__ __forceinline__ uint32_t nonfinite2(uint32_t w) {
     if constexpr (std::is_same<T, __nv_bfloat16>::value)
@@ -609,11 +609,29 @@ __device__ void prompt_check(const PromptParams& p, typename Shape::Smem& sm, in
                  prompt_wait_warp(p, sm, &sm.kv_full[slot], (tile / Shape::NSLOT) & 1u);
             if (!ok) break;
             parity ^= 1u << slot;
+            // Rows up to the item's first token are attended by all its rows.
+            const int first = max(w.t0 + 1 - j * Shape::BN, 0);
             const int rows = min(Shape::BN, end - j * Shape::BN), rows16 = (rows + 15) & ~15;
-            for (int idx = thread; idx < rows16 * CHUNKS; idx += 64) {
-                const int row = idx / CHUNKS, chunk = idx % CHUNKS;
-                uint4* at = reinterpret_cast<uint4*>(sm.kv[slot][chunk >> 3] + row * 128) + (chunk & 7);
-                if (row >= rows) *at = make_uint4(0u, 0u, 0u, 0u);
+            auto chunk_at = [&](int idx) {
+                return reinterpret_cast<uint4*>(sm.kv[slot][(idx % CHUNKS) >> 3] + idx / CHUNKS * 128) + (idx & 7);
+            };
+            for (int idx = rows * CHUNKS + thread; idx < rows16 * CHUNKS; idx += 64)
+                *chunk_at(idx) = make_uint4(0u, 0u, 0u, 0u);
+            uint32_t found = 0;
+#pragma unroll 8
+            for (int idx = first * CHUNKS + thread; idx < rows * CHUNKS; idx += 64) {
+                const uint4 v = *chunk_at(idx);
+                found |= nonfinite2<T>(v.x) | nonfinite2<T>(v.y) | nonfinite2<T>(v.z) | nonfinite2<T>(v.w);
+            }
+            if (found) {
+                for (int idx = first * CHUNKS + thread; idx < rows * CHUNKS; idx += 64) {
+                    uint32_t* v = reinterpret_cast<uint32_t*>(chunk_at(idx));
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t bad = nonfinite2<T>(v[e]);
+                        v[e] &= ~(((bad >> 31) * 0xffff0000u) | ((bad >> 15 & 1u) * 0xffffu));
+                    }
+                }
+                atomicMax(&sm.last_dirty, n - 1);  // n: items announced so far
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -627,6 +645,21 @@ __device__ void prompt_check(const PromptParams& p, typename Shape::Smem& sm, in
 // ---------------------------------------------------------------------------
 // output warps
 // ---------------------------------------------------------------------------
+// The non-finite values that the check warps took out of V tiles: each decides
+// its column of the rows that attend it.  Added to the stored output `dst` of
+// the row of `token` by the thread that stored it.
+template <typename T, int D>
+__device__ __noinline__ void prompt_add_nonfinite(const PromptParams& p, const PromptItem& w, int token, T* dst) {
+    const T* v = static_cast<const T*>(p.value) + (int64_t)w.kv_head * D;
+    for (int j = w.t0 + 1; j <= token; ++j) {
+        const T* row = v + (int64_t)(w.row0 + j) * p.value_stride;
+        for (int c = 0; c < D; ++c) {
+            const float x = (float)row[c];
+            if (!isfinite(x)) dst[c] = (T)((float)dst[c] + x);
+        }
+    }
+}
+
 template <typename T, class Shape>
 __device__ void prompt_output(const PromptParams& p, typename Shape::Smem& sm, uint32_t tmem, int warp, int lane) {
     constexpr int D = Shape::SLABS * 64;
@@ -650,6 +683,7 @@ __device__ void prompt_output(const PromptParams& p, typename Shape::Smem& sm, u
             const float inv = 1.f / l;  // l > 0: every row attends its own position (NaN stays NaN)
             const int token = w.t0 + i * p.tile_tokens + t;
             const bool store = t < p.tile_tokens && token < w.len;
+            const bool dirty = *reinterpret_cast<volatile int*>(&sm.last_dirty) >= n - 1;
             T* dst = static_cast<T*>(p.out) +
                      ((int64_t)(w.row0 + token) * p.num_heads + (int64_t)w.kv_head * p.group + g) * D;
 #pragma unroll 1
@@ -673,6 +707,7 @@ __device__ void prompt_output(const PromptParams& p, typename Shape::Smem& sm, u
                     }
                 }
             }
+            if (store && dirty) prompt_add_nonfinite<T, D>(p, w, token, dst);
         }
         if (!ok) break;
     }
@@ -718,6 +753,7 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
         }
         mbar_init(&sm.mma_done, 1);
         sm.abort_flag = 0;
+        sm.last_dirty = -1;
         fence_mbar_init();
     }
     if (warp == Shape::MMA_WARP) tmem_alloc(&sm.tmem_base, Shape::TMEM_COLS);

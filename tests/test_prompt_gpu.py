@@ -120,3 +120,133 @@ def test_growing_scores(dtype):
     out = api.prompt_attention(q, k, v, starts([n]), d ** -0.5)
     assert api.get_device_error() == (0, 0)
     check(q, k, v, [n], d ** -0.5, out)
+
+
+@pytest.mark.parametrize("what", ["nan", "inf", "lowest"])
+@pytest.mark.parametrize("h,hkv,d,dtype", [(8, 2, 128, torch.bfloat16), (4, 4, 64, torch.float16),
+                                           (6, 2, 64, torch.bfloat16)])
+def test_unattended_rows_may_hold_anything(what, h, hkv, d, dtype):
+    """Rows outside the sequences, and later tokens of a sequence, change nothing
+    of what does not attend them, to the bit."""
+    lens, first, extra = [70, 300, 5, 513], 7, 150
+    tokens = first + sum(lens) + extra
+    q, k, v = rows(tokens, h, hkv, d, dtype, 11)
+    loc = starts(lens, first)
+    clean = api.prompt_attention(q, k, v, loc, d ** -0.5)
+    fill = {"nan": float("nan"), "inf": float("inf"), "lowest": torch.finfo(dtype).min}[what]
+    q2, k2, v2 = q.clone(), k.clone(), v.clone()
+    end = first + sum(lens)
+    for x in (q2, k2, v2):
+        x[:first] = fill
+        x[end:] = fill
+    poisoned = [(first + 70 + 211, 1), (first + 70 + 300 + 5 + 500, 0), (first + 69, 0)]  # (row, column)
+    for row, col in poisoned:
+        k2[row] = fill
+        v2[row, :, col::3] = fill
+    out = api.prompt_attention(q2, k2, v2, loc, d ** -0.5)
+    assert api.get_device_error() == (0, 0)
+    at = first
+    for n in lens:
+        bad = [r for r, _ in poisoned if at <= r < at + n]
+        upto = min(bad) if bad else at + n
+        assert torch.equal(out[at:upto], clean[at:upto])
+        if bad and what != "lowest":
+            assert not torch.isfinite(out[upto:at + n, :, :]).all(-1).any()  # each later row attends it
+        at += n
+
+
+def test_non_finite_values_reach_what_attends_them():
+    """An infinite or NaN value decides its column of every row from its own on,
+    and no other column."""
+    n, h, hkv, d = 400, 4, 2, 128
+    q, k, v = rows(n, h, hkv, d, torch.bfloat16, 12)
+    loc = starts([n])
+    clean = api.prompt_attention(q, k, v, loc, d ** -0.5)
+    v2 = v.clone()
+    v2[150, 0, 5] = float("inf")
+    v2[390, 1, 100] = float("nan")
+    v2[395, 0, 5] = float("-inf")
+    v2[20, 1, 0] = float("-inf")
+    out = api.prompt_attention(q, k, v2, loc, d ** -0.5)
+    want = clean.clone()
+    want[150:, :2, 5] = float("inf")
+    want[395:, :2, 5] = float("nan")
+    want[390:, 2:, 100] = float("nan")
+    want[20:, 2:, 0] = float("-inf")
+    assert torch.equal(out.isnan(), want.isnan())
+    assert torch.equal(out[~out.isnan()], want[~want.isnan()])
+
+
+def test_bad_start_rows_are_reported():
+    """Start rows out of order or out of range: the sequences they spoil are
+    skipped, the others computed."""
+    q, k, v = rows(300, 4, 2, 64, torch.float16, 13)
+    loc = torch.tensor([0, 90, 50, 300, 301], dtype=torch.int32, device="cuda")
+    out = torch.full_like(q, 7.0)
+    api.prompt_attention(q, k, v, loc, 0.125, out=out)
+    assert api.get_device_error() == (-5, native.DEVERR_CONTEXT_LEN)
+    # rows 50 .. 89 belong to two sequences here: either may write them last
+    check(q[:50], k[:50], v[:50], [50], 0.125, out[:50])
+    ref, tol = exact(q[50:], k[50:], v[50:], 0.125)
+    assert float(((out[90:].double() - ref[40:]).abs() - tol[40:]).max()) <= 0
+    loc = torch.tensor([-3, 100], dtype=torch.int32, device="cuda")
+    out.fill_(7.0)
+    api.prompt_attention(q, k, v, loc, 0.125, out=out)
+    assert api.get_device_error() == (-5, native.DEVERR_CONTEXT_LEN)
+    assert bool((out == 7).all())
+
+
+def test_captured_and_replayed_with_other_lengths():
+    q, k, v = rows(400, 8, 2, 64, torch.bfloat16, 14)
+    loc = starts([150, 250])
+    out = torch.empty_like(q)
+    api.prompt_attention(q, k, v, loc, 0.125, out=out)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        api.prompt_attention(q, k, v, loc, 0.125, out=out)
+    for lens in ([150, 250], [399, 1], [0, 128]):
+        loc.copy_(starts(lens))
+        out.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        check(q, k, v, lens, 0.125, out)
+        assert bool((out[sum(lens):] == 7).all())
+
+
+def test_another_stream_and_two_calls_at_once():
+    a = rows(600, 8, 2, 128, torch.bfloat16, 15)
+    b = rows(600, 8, 8, 128, torch.bfloat16, 16)
+    loc = starts([600])
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    outs = [(api.prompt_attention(*a, loc, 0.1, stream=s1), api.prompt_attention(*b, loc, 0.1, stream=s2))
+            for _ in range(4)]
+    torch.cuda.synchronize()
+    assert api.get_device_error() == (0, 0)
+    for x, y in outs:
+        check(*a, [600], 0.1, x)
+        check(*b, [600], 0.1, y)
+
+
+def test_refusals():
+    q, k, v = rows(20, 4, 2, 64, torch.float16, 17)
+    loc = starts([20])
+    with pytest.raises(ValueError):
+        api.prompt_attention(q, k, v.bfloat16(), loc, 0.1)
+    with pytest.raises(ValueError):
+        api.prompt_attention(q, k[:19], v[:19], loc, 0.1)
+    with pytest.raises(ValueError):
+        api.prompt_attention(q, k, v, loc.long(), 0.1)
+    with pytest.raises(ValueError):
+        api.prompt_attention(q.transpose(0, 1).contiguous().transpose(0, 1), k, v, loc, 0.1)  # heads outermost
+    with pytest.raises(ValueError):
+        api.prompt_attention(q, k[:1].expand(20, 2, 64), v, loc, 0.1)  # rows that overlap
+    with pytest.raises(ValueError):
+        api.prompt_attention(q, k, v, loc, 0.1, out=torch.empty(20, 4, 64, device="cuda"))
+    with pytest.raises(ValueError):
+        api.prompt_attention(q.cpu(), k.cpu(), v.cpu(), loc.cpu(), 0.1)
+    with pytest.raises(native.PaError):
+        api.prompt_attention(q.float(), k.float(), v.float(), loc, 0.1)
+    with pytest.raises(native.PaError):
+        api.prompt_attention(q, k, v, loc, 0.0)
