@@ -265,6 +265,14 @@ int pa_prefill(void *out, int32_t out_dtype, const void *query, const int32_t *q
                int32_t num_kv_heads, float scale, void *stream);
 
 /*
+ * Bytes of device workspace pa_prompt_attention needs for num_seqs sequences in
+ * num_tokens rows: the list of its work items.  Reset by every call; two calls
+ * in flight at once must not share one.  Returns 0 for invalid arguments.
+ */
+size_t pa_prompt_attention_workspace_size(int32_t num_seqs, int32_t num_tokens, int32_t num_heads,
+                                          int32_t num_kv_heads);
+
+/*
  * Attention over whole prompts ("PagedAttention 论文精读笔记", §2.1 attention
  * equation, §5.3 prompt step): causal attention of the tokens of num_seqs
  * packed sequences over themselves, keys and values taken from the
@@ -289,14 +297,17 @@ int pa_prefill(void *out, int32_t out_dtype, const void *query, const int32_t *q
  * sequences, rows outside every sequence -- may hold anything, NaN included.
  * Supported: f16 or bf16, head_dim 64 or 128, G <= 128; else
  * PA_ERR_UNSUPPORTED.  A sequence whose start rows break the rules above sets
- * PA_DEVERR_CONTEXT_LEN and is skipped.  No workspace.
+ * PA_DEVERR_CONTEXT_LEN and is skipped; start rows that overlap may set it too,
+ * and what the workspace's list has no room for is then not computed.
+ *   workspace         device, 256-byte aligned, at least
+ *                     pa_prompt_attention_workspace_size(...) bytes
  */
 int pa_prompt_attention(void *out, const void *query, int64_t query_stride,
                         const void *key, int64_t key_stride,
                         const void *value, int64_t value_stride,
                         const int32_t *query_start_loc, int32_t num_seqs, int32_t num_tokens,
                         int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, int32_t dtype,
-                        float scale, void *stream);
+                        float scale, void *workspace, size_t workspace_bytes, void *stream);
 
 /*
  * Copy-on-write block copy, one launch for all pairs and layers.  For every

@@ -247,8 +247,13 @@ def _token_stride(t: torch.Tensor, name: str) -> int:
     return by_token
 
 
+def prompt_attention_workspace_size(num_seqs: int, num_tokens: int, num_heads: int, num_kv_heads: int) -> int:
+    return int(native.load().pa_prompt_attention_workspace_size(num_seqs, num_tokens, num_heads, num_kv_heads))
+
+
 def prompt_attention(query: torch.Tensor, key: torch.Tensor, value: torch.Tensor, query_start_loc: torch.Tensor,
                      scale: float, *, out: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None,
                      stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """Causal attention of whole packed prompts over themselves; returns
     out [T][H][d] in the inputs' type (f16 or bf16).
@@ -272,11 +277,16 @@ def prompt_attention(query: torch.Tensor, key: torch.Tensor, value: torch.Tensor
         out = _empty((t, h, d), query.dtype, query.device, stream)
     _require(out.shape == query.shape and out.dtype == query.dtype and out.is_contiguous(),
              "out is contiguous [num_tokens][num_heads][head_dim] of the inputs' dtype")
-    _require_here(query, key, value, query_start_loc, out)
+    if workspace is None:
+        need = lib.pa_prompt_attention_workspace_size(query_start_loc.numel() - 1, t, h, hkv)
+        workspace = _empty((max(need, 256),), torch.uint8, query.device, stream)
+    _require(workspace.dtype == torch.uint8 and workspace.is_contiguous(), "workspace is bytes")
+    _require_here(query, key, value, query_start_loc, out, workspace)
     _raise(lib.pa_prompt_attention(out.data_ptr(), query.data_ptr(), _token_stride(query, "query"), key.data_ptr(),
                                    _token_stride(key, "key"), value.data_ptr(), _token_stride(value, "value"),
                                    query_start_loc.data_ptr(), query_start_loc.numel() - 1, t, h, hkv, d,
-                                   DTYPE_CODE[query.dtype], float(scale), _stream_ptr(stream)),
+                                   DTYPE_CODE[query.dtype], float(scale), workspace.data_ptr(), workspace.numel(),
+                                   _stream_ptr(stream)),
            "pa_prompt_attention")
     return out
 

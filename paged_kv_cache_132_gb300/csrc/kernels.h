@@ -171,9 +171,22 @@ struct PromptParams {
     int group;                    // num_heads / num_kv_heads, 1..128
     int tile_tokens;              // tokens per query tile: 128 / group
     float scale_log2;             // scale * log2(e), > 0
+    // Work list (workspace views), or nullptr: at most one item per CTA and no
+    // planning kernel.
+    int4* items;                  // (first row, length, pair of query tiles, 0) of each unit, longest sequences first
+    int* num_units;               // units listed; an item is a unit and a KV head
+    int* next_item;               // items taken beyond the first one of each CTA
+    int max_units;                // entries of the list
     int* err;
     unsigned long long wait_limit_ns;
 };
+
+// Units (pairs of query tiles of a sequence) of a call, at most: every sequence
+// has at most one more than its share of the rows.
+inline int64_t prompt_max_units(int64_t num_tokens, int64_t num_seqs, int tile_tokens) {
+    return num_tokens / (2 * tile_tokens) + num_seqs;
+}
+constexpr size_t kPromptHeaderBytes = 256;  // num_units and next_item, before the list
 
 // tmap_q, tmap_k, tmap_v: the rows as 3-D tensors {head_dim, heads, tokens} with
 // the 128-byte swizzle, box {64, group, tile_tokens} for q and {64, 1, 64} for k

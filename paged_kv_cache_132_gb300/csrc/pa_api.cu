@@ -528,10 +528,19 @@ int pa_prefill(void* out, int32_t out_dtype, const void* query, const int32_t* q
                                         static_cast<cudaStream_t>(stream)));
 }
 
+size_t pa_prompt_attention_workspace_size(int32_t num_seqs, int32_t num_tokens, int32_t num_heads,
+                                          int32_t num_kv_heads) {
+    if (num_seqs < 0 || num_tokens < 0 || num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads != 0 ||
+        num_heads / num_kv_heads > 128)
+        return 0;
+    return pa::kPromptHeaderBytes +
+           pa::prompt_max_units(num_tokens, num_seqs, 128 / (num_heads / num_kv_heads)) * sizeof(int4);
+}
+
 int pa_prompt_attention(void* out, const void* query, int64_t query_stride, const void* key, int64_t key_stride,
                         const void* value, int64_t value_stride, const int32_t* query_start_loc, int32_t num_seqs,
                         int32_t num_tokens, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, int32_t dtype,
-                        float scale, void* stream) {
+                        float scale, void* workspace, size_t workspace_bytes, void* stream) {
     NvtxRange range("pa_prompt_attention");
     if (elem_bytes(dtype) == 0 || num_seqs < 0 || num_tokens < 0 || num_heads <= 0 || num_kv_heads <= 0 ||
         num_heads % num_kv_heads != 0 || head_dim <= 0 || !std::isfinite(scale) || !(scale > 0.f))
@@ -571,6 +580,19 @@ int pa_prompt_attention(void* out, const void* query, int64_t query_stride, cons
     p.scale_log2 = scale * 1.4426950408889634f;
     p.err = err;
     p.wait_limit_ns = wait_limit_ns();
+    if (!aligned(workspace, 256) ||
+        workspace_bytes < pa_prompt_attention_workspace_size(num_seqs, num_tokens, num_heads, num_kv_heads))
+        return PA_ERR_WORKSPACE;
+    const int64_t units = pa::prompt_max_units(num_tokens, num_seqs, p.tile_tokens);
+    if (units * num_kv_heads > 0x40000000LL) return PA_ERR_UNSUPPORTED;  // item numbers stay 32-bit
+    if (units * num_kv_heads > sms) {
+        // More items than CTAs: a planning kernel lists them.
+        char* ws = static_cast<char*>(workspace);
+        p.num_units = reinterpret_cast<int*>(ws);
+        p.next_item = p.num_units + 1;
+        p.items = reinterpret_cast<int4*>(ws + pa::kPromptHeaderBytes);
+        p.max_units = (int)units;
+    }
 
     CUtensorMap tmap_q, tmap_k, tmap_v;  // copies: later lookups may reuse a cache slot
     const CUtensorMap* m = rows_map(query, dtype, num_tokens, num_heads, head_dim, query_stride, group, p.tile_tokens);

@@ -35,7 +35,7 @@
 // Warp roles (512 threads, registers moved between the groups by setmaxnreg):
 //   warps 0-3, 4-7   softmax of query tile 0 / 1
 //   warps 8-11       outputs: O_i / row sum, rounded once, written to memory
-//   warp 12          MMA issuer (one thread), owner of the TMEM allocation
+//   warp 12          MMA issuer, owner of the TMEM allocation
 //   warp 13          work items, Q, K and V copies (TMA)
 //   warps 14, 15     the V tiles with masked positions (above)
 // Every wait is bounded; a wait that runs out sets PA_DEVERR_TIMEOUT and makes
@@ -68,9 +68,9 @@ struct PromptShape {
     static constexpr int CHECK_WARP = 14;        // first of two
     static constexpr int THREADS = 512;
     static constexpr int ITEM_READERS = 8 + 4 + 1 + 2;  // softmax, output, MMA and check warps
-    // Registers per thread after the split: 256 * 192 + 128 * 64 + 128 * 64
+    // Registers per thread after the split: 256 * 176 + 128 * 64 + 128 * 96
     // = 512 * 128, the launch's total.
-    static constexpr int REGS_SOFTMAX = 192, REGS_OUT = 64, REGS_OTHER = 64;
+    static constexpr int REGS_SOFTMAX = 176, REGS_OUT = 64, REGS_OTHER = 96;
     static_assert(256 * REGS_SOFTMAX + 128 * REGS_OUT + 128 * REGS_OTHER <= THREADS * 128, "register split");
     // TMEM columns: S_i (and P_i over it, two per column) at 128 i, O_i after both.
     static constexpr uint32_t TMEM_COLS = 512;
@@ -111,8 +111,6 @@ __device__ __forceinline__ float prompt_exp2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-
-__device__ __forceinline__ uint64_t desc_of(uint32_t lo, uint32_t hi) { return ((uint64_t)hi << 32) | lo; }
 
 template <uint32_t REGS>
 __device__ __forceinline__ void regs_inc() {
@@ -193,11 +191,11 @@ __device__ __forceinline__ bool prompt_next_item(const PromptParams& p, typename
 // ---------------------------------------------------------------------------
 // load warp: work items and copies
 // ---------------------------------------------------------------------------
-// Items are numbered sequence after sequence, the last query tiles (the
-// longest key ranges) of a sequence first, KV heads innermost, so that CTAs at
-// work together share keys and values in L2.  CTA c takes items c, c + grid,
-// ...; a warp finds an item's sequence by walking the start rows forward, 32
-// sequences at a time.
+// With a list (prompt_plan_kernel) CTA c takes item c first and then whatever
+// a device counter gives it; KV heads are innermost, so CTAs at work together
+// share a sequence's rows in L2.  A call with no more items than CTAs needs no
+// list: CTA c finds item c itself, walking the start rows 32 sequences at a
+// time.
 struct PromptWalk {
     int base;    // sequences [base, base + 32) are in the lanes
     int64_t before;  // (sequence, query tile pair) units before them
@@ -250,6 +248,7 @@ __device__ void prompt_load(const PromptParams& p, typename Shape::Smem& sm, int
     const uint32_t q_bytes = (uint32_t)(Shape::SLABS * p.tile_tokens * p.group * 128);
     uint32_t q_used[2] = {0, 0};  // items that loaded Q_i
     uint32_t slot = 0, round = 0, filled = 0;
+    const int total = p.items ? __ldg(p.num_units) * p.num_kv_heads : 0;
     bool ok = true;
     // One K or V tile of `rows` positions (rounded up to whole halves).
     auto load_tile = [&](const CUtensorMap* map, const PromptItem& w, int j, int end, bool check) {
@@ -282,11 +281,28 @@ __device__ void prompt_load(const PromptParams& p, typename Shape::Smem& sm, int
         ++q_used[i];
     };
 
-    PromptWalk walk{};
-    prompt_walk_load(p, walk, lane);
-    int64_t index = blockIdx.x;
-    for (int n = 0;; ++n, index += gridDim.x) {
-        const int4 it = prompt_walk_to(p, walk, lane, index);
+    auto listed = [&](int index) {
+        int4 e = make_int4(0, 0, 0, 0);
+        if (index < total) {
+            const int unit = index / p.num_kv_heads;
+            e = __ldg(p.items + unit);
+            e.w = index - unit * p.num_kv_heads;
+        }
+        return e;
+    };
+    int4 next;
+    if (p.items) {
+        next = listed(blockIdx.x);
+    } else {
+        PromptWalk walk{};
+        prompt_walk_load(p, walk, lane);
+        next = prompt_walk_to(p, walk, lane, blockIdx.x);
+    }
+    for (int n = 0;; ++n) {
+        const int4 it = next;
+        // The next item's number arrives while this one's copies are issued.
+        int taken = 0;
+        if (p.items && lane == 0) taken = (int)gridDim.x + atomicAdd(p.next_item, 1);
         const int st = n % Shape::NITEM;
         if (!prompt_wait_warp(p, sm, &sm.item_empty[st], ((uint32_t)(n / Shape::NITEM) & 1u) ^ 1u)) break;
         if (lane == 0) {
@@ -307,6 +323,8 @@ __device__ void prompt_load(const PromptParams& p, typename Shape::Smem& sm, int
             }
         }
         if (!__shfl_sync(kFullMask, ok, 0)) break;
+        next = make_int4(0, 0, 0, 0);
+        if (p.items) next = listed(__shfl_sync(kFullMask, taken, 0));
     }
     pdl_launch_dependents();
     // Every copy this warp issued lands before the CTA exits (bounded).
@@ -324,127 +342,160 @@ __device__ void prompt_load(const PromptParams& p, typename Shape::Smem& sm, int
 }
 
 // ---------------------------------------------------------------------------
-// MMA issuer (one warp; lane 0 issues)
+// MMA issuer (one warp)
 // ---------------------------------------------------------------------------
+// The whole warp runs the issue loop and one elected lane issues: descriptors
+// then stay in uniform registers.  With the loop inside `if (lane == 0)` every
+// MMA waited for its operands to be moved there, about 115 cycles an MMA
+// against the 64 that it runs for (measured: 4500 against 2300 cycles per
+// tile of both query tiles).
+__device__ __forceinline__ void prompt_mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                              uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred lead, acc;\n\t"
+        "elect.sync _|lead, 0xffffffff;\n\t"
+        "setp.ne.b32 acc, %4, 0;\n\t"
+        "@lead tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, acc;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void prompt_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                              uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred lead, acc;\n\t"
+        "elect.sync _|lead, 0xffffffff;\n\t"
+        "setp.ne.b32 acc, %4, 0;\n\t"
+        "@lead tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, acc;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void prompt_commit(uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred lead;\n\t"
+        "elect.sync _|lead, 0xffffffff;\n\t"
+        "@lead tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_addr(bar))
+        : "memory");
+}
+
 template <class Shape, bool BF16>
 __device__ void prompt_mma(const PromptParams& p, typename Shape::Smem& sm, uint32_t tmem, int lane) {
     constexpr int D = Shape::SLABS * 64;
     constexpr uint32_t IDESC_S = mma_idesc_f16(BF16, false, Shape::BM, 0);  // N is added per tile
     constexpr uint32_t IDESC_O = mma_idesc_f16(BF16, true, Shape::BM, D);
-    // All operands share the upper half of their descriptors; the lower half
-    // (address / 16, leading offset) fits 32-bit arithmetic: every address is
-    // below 2^18, so a step of it never carries out of its 14 bits.
     constexpr uint32_t SLOT16 = sizeof(sm.kv[0]) >> 4, Q16 = sizeof(sm.q[0]) >> 4;
     const uint64_t dq = smem_desc_sw128(smem_addr(sm.q[0][0]), 16, 1024);
     const uint64_t dk = smem_desc_sw128(smem_addr(sm.kv[0][0]), 16, 1024);
     const uint64_t dv = smem_desc_sw128(smem_addr(sm.kv[0][0]), Shape::SLAB, 1024);
-    const uint32_t hi = (uint32_t)(dq >> 32);
 
     // S_i = Q_i K^T over the first `cols` (a multiple of 16) positions of the tile.
     auto issue_s = [&](int i, uint32_t slot, int cols) {
-        const uint32_t idesc = IDESC_S | ((uint32_t)(cols >> 3) << 17);
-        uint32_t a = (uint32_t)dq + i * Q16, b = (uint32_t)dk + slot * SLOT16;
-        asm volatile("" : "+r"(a), "+r"(b));  // the 2 * 8 sums stay out of the registers of the loop
+        const uint32_t idesc = IDESC_S | ((uint32_t)(cols >> 3) << 17), d = tmem + i * Shape::BN;
+        const uint64_t a = dq + i * Q16, b = dk + slot * SLOT16;
 #pragma unroll
         for (int ks = 0; ks < Shape::SLABS * 4; ++ks) {
             const uint32_t off = (uint32_t)((ks >> 2) * (Shape::SLAB >> 4) + (ks & 3) * 2);
-            mma_f16_ss(tmem + i * Shape::BN, desc_of(a + off, hi), desc_of(b + off, hi), idesc, ks > 0 ? 1u : 0u);
+            prompt_mma_ss(d, a + off, b + off, idesc, ks > 0 ? 1u : 0u);
         }
-        mma_commit(&sm.s_full[i]);
+        prompt_commit(&sm.s_full[i]);
     };
     // O_i (+)= P_i V over the same positions.
     auto issue_pv = [&](int i, uint32_t slot, int cols, bool first) {
-        uint32_t a = tmem + i * Shape::BN, b = (uint32_t)dv + slot * SLOT16;
-        const uint32_t o = tmem + Shape::O_COL + i * D;
-        asm volatile("" : "+r"(a), "+r"(b));
+        const uint32_t a = tmem + i * Shape::BN, o = tmem + Shape::O_COL + i * D;
+        const uint64_t b = dv + slot * SLOT16;
+        if (cols == Shape::BN) {
 #pragma unroll
-        for (int ks = 0; ks < Shape::BN / 16; ++ks)
-            if (ks * 16 < cols)
-                mma_f16_ts(o, a + ks * 8, desc_of(b + ks * 128, hi), IDESC_O, (ks > 0 || !first) ? 1u : 0u);
-        mma_commit(&sm.pv_done[i]);
+            for (int ks = 0; ks < Shape::BN / 16; ++ks)
+                prompt_mma_ts(o, a + ks * 8, b + ks * 128, IDESC_O, (ks > 0 || !first) ? 1u : 0u);
+        } else {
+#pragma unroll 1
+            for (int ks = 0; ks < cols / 16; ++ks)
+                prompt_mma_ts(o, a + ks * 8, b + ks * 128, IDESC_O, (ks > 0 || !first) ? 1u : 0u);
+        }
+        prompt_commit(&sm.pv_done[i]);
     };
     auto cols_of = [](int end, int j) { return min(Shape::BN, (end - j * Shape::BN + 15) & ~15); };
 
     uint32_t slot = 0, round = 0;    // ring position of the next tile
-    uint32_t used[2] = {0, 0};       // items of tile i so far
-    uint32_t np[2] = {0, 0};         // P_i so far
-    uint32_t checked = 0;            // per slot: parity of its next checked V tile
+    uint32_t used = 0;               // bit i: parity of tile i's items so far
+    uint32_t np = 0;                 // bit i: of its P so far
+    uint32_t checked = 0;            // bit slot: of the slot's checked V tiles so far
     auto advance = [&] {
         if (++slot == Shape::NSLOT) {
             slot = 0;
-            ++round;
+            round ^= 1u;
         }
     };
     int n = 0;
     PromptItem w;
-    while (prompt_next_item<Shape>(p, sm, lane, n, w)) {
-        bool ok = true;
-        if (lane == 0) {
-            const int nt = (w.last() + 127) >> 7;
-            ok = prompt_wait(p, sm, &sm.kv_full[slot], round & 1u);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                if (!ok || !w.end(i)) continue;
-                ok = prompt_wait(p, sm, &sm.q_full[i], used[i] & 1u);
-                if (!ok) continue;
-                tc_fence_after_sync();
-                issue_s(i, slot, cols_of(w.end(i), 0));
-                if (w.tiles(i) == 1) mma_commit(&sm.q_empty[i]);
+    bool ok = true;
+    while (ok && prompt_next_item<Shape>(p, sm, lane, n, w)) {
+        const int tiles0 = w.tiles(0), tiles1 = w.tiles(1), nt = max(tiles0, tiles1);
+        const int both = w.end1 ? 2 : 1;
+        // Tiles V_j and K_j+1, waited for before they are due: at the end of a
+        // step only P is, so that the tensor cores do not run dry meanwhile.
+        uint32_t vslot = 0, kslot = 0;
+        auto ready = [&](int j) {
+            vslot = slot;
+            if (j >= w.first_masked) {
+                ok = prompt_wait_warp(p, sm, &sm.v_checked[vslot], (checked >> vslot) & 1u);
+                checked ^= 1u << vslot;
+            } else {
+                ok = prompt_wait_warp(p, sm, &sm.kv_full[vslot], round);
             }
-            if (ok) mma_commit(&sm.kv_empty[slot]);
             advance();
-            for (int j = 0; j < nt && ok; ++j) {
-                const uint32_t vslot = slot, vround = round;
+            if (j + 1 < nt) {
+                kslot = slot;
+                if (ok) ok = prompt_wait_warp(p, sm, &sm.kv_full[kslot], round);
                 advance();
-                const uint32_t kslot = slot, kround = round;
-                const bool more = j + 1 < nt;
-                if (more) advance();
-                if (j >= w.first_masked) {
-                    ok = prompt_wait(p, sm, &sm.v_checked[vslot], (checked >> vslot) & 1u);
-                    checked ^= 1u << vslot;
-                } else {
-                    ok = prompt_wait(p, sm, &sm.kv_full[vslot], vround & 1u);
-                }
-                bool k_ready = false;
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int nti = w.tiles(i);
-                    if (!ok || j >= nti) continue;
-                    if (j == 0) ok = prompt_wait(p, sm, &sm.o_empty[i], (used[i] & 1u) ^ 1u);
-                    if (ok) ok = prompt_wait(p, sm, &sm.p_full[i], np[i] & 1u);
-                    if (!ok) continue;
-                    ++np[i];
+            }
+            tc_fence_after_sync();
+        };
+        ok = prompt_wait_warp(p, sm, &sm.kv_full[slot], round);
+#pragma unroll 1
+        for (int i = 0; i < both && ok; ++i) {
+            ok = prompt_wait_warp(p, sm, &sm.q_full[i], (used >> i) & 1u);
+            tc_fence_after_sync();
+            if (ok) issue_s(i, slot, cols_of(w.end(i), 0));
+            if (w.tiles(i) == 1) prompt_commit(&sm.q_empty[i]);
+        }
+        prompt_commit(&sm.kv_empty[slot]);
+        advance();
+        // The accumulators: free once the output warps have read the item before.
+#pragma unroll 1
+        for (int i = 0; i < both && ok; ++i) ok = prompt_wait_warp(p, sm, &sm.o_empty[i], ((used >> i) & 1u) ^ 1u);
+        if (ok) ready(0);
+#pragma unroll 1
+        for (int j = 0; j < nt && ok; ++j) {
+            const uint32_t vnow = vslot, know = kslot;
+#pragma unroll 1
+            for (int i = 0; i < both && ok; ++i) {
+                const int nti = i ? tiles1 : tiles0;
+                const bool last = i + 1 == both;
+                if (j < nti) {
+                    ok = prompt_wait_warp(p, sm, &sm.p_full[i], (np >> i) & 1u);
+                    if (!ok) break;
+                    np ^= 1u << i;
                     tc_fence_after_sync();
-                    issue_pv(i, vslot, cols_of(w.end(i), j), j == 0);
-                    if (j + 1 == nti) {
-                        mma_commit(&sm.o_full[i]);
-                    } else {
-                        if (!k_ready) {
-                            ok = prompt_wait(p, sm, &sm.kv_full[kslot], kround & 1u);
-                            k_ready = true;
-                            if (!ok) continue;
-                            tc_fence_after_sync();
-                        }
-                        issue_s(i, kslot, cols_of(w.end(i), j + 1));
-                        if (j + 2 == nti) mma_commit(&sm.q_empty[i]);
-                    }
+                    issue_pv(i, vnow, cols_of(w.end(i), j), j == 0);
                 }
-                if (ok) {
-                    mma_commit(&sm.kv_empty[vslot]);
-                    if (more) mma_commit(&sm.kv_empty[kslot]);
+                if (last) {
+                    prompt_commit(&sm.kv_empty[vnow]);
+                    if (j + 1 < nt) ready(j + 1);
+                }
+                if (j + 1 < nti) {
+                    if (ok) issue_s(i, know, cols_of(w.end(i), j + 1));
+                    if (j + 2 == nti) prompt_commit(&sm.q_empty[i]);
+                } else if (j + 1 == nti) {
+                    prompt_commit(&sm.o_full[i]);
                 }
             }
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                if (w.end(i)) ++used[i];
+            if (j + 1 < nt) prompt_commit(&sm.kv_empty[know]);
         }
-        if (!__shfl_sync(kFullMask, ok, 0)) break;
+        used ^= both == 2 ? 3u : 1u;
     }
-    // Nothing this thread issued may still be running when TMEM is released.
-    if (lane == 0) {
-        mma_commit(&sm.mma_done);
-        if (!mbar_wait_bounded(&sm.mma_done, 0, p.wait_limit_ns)) set_error(p.err, PA_DEVERR_TIMEOUT);
-    }
+    // Nothing this warp issued may still be running when TMEM is released.
+    prompt_commit(&sm.mma_done);
+    if (lane == 0 && !mbar_wait_bounded(&sm.mma_done, 0, p.wait_limit_ns)) set_error(p.err, PA_DEVERR_TIMEOUT);
     __syncwarp();
 }
 

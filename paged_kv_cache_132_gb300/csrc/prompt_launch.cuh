@@ -23,8 +23,7 @@ cudaError_t launch_prompt_t(const PromptParams& p, int sms, const CUtensorMap* t
         if (e != cudaSuccess) return e;
         __atomic_store_n(&configured[dev], 1, __ATOMIC_RELEASE);
     }
-    // Every sequence has at most one item per KV head more than its share of the rows.
-    const int64_t items = ((int64_t)p.num_tokens / (2 * p.tile_tokens) + p.num_seqs) * p.num_kv_heads;
+    const int64_t items = prompt_max_units(p.num_tokens, p.num_seqs, p.tile_tokens) * p.num_kv_heads;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(items < sms ? items : sms));
     cfg.blockDim = dim3(Shape::THREADS);

@@ -72,7 +72,9 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.pa_prefill.argtypes = [vp, i32, vp, vp, i32, i32, vp, vp, desc, vp, i32, vp, i32, i32, i32,
                                    ctypes.c_float, vp]
         lib.pa_prompt_attention.argtypes = [vp, vp, i64, vp, i64, vp, i64, vp, i32, i32, i32, i32, i32, i32,
-                                            ctypes.c_float, vp]
+                                            ctypes.c_float, vp, sz, vp]
+        lib.pa_prompt_attention_workspace_size.argtypes = [i32, i32, i32, i32]
+        lib.pa_prompt_attention_workspace_size.restype = sz
         lib.pa_get_device_error.argtypes = [vp, ctypes.POINTER(i32)]
         lib.pa_status_string.argtypes = [ctypes.c_int]
         lib.pa_status_string.restype = ctypes.c_char_p

@@ -15,11 +15,12 @@ def lib():
 
 def _call(lib, **over):
     a = dict(out=FAKE, q=FAKE, qs=256, k=FAKE, ks=128, v=FAKE, vs=128, qsl=FAKE, seqs=2, tokens=40, heads=4, kv_heads=2,
-             d=64, dtype=native.PA_BF16, scale=0.125, stream=None)
+             d=64, dtype=native.PA_BF16, scale=0.125, ws=FAKE,
+             ws_bytes=1 << 30, stream=None)
     a.update(over)
     return lib.pa_prompt_attention(a["out"], a["q"], a["qs"], a["k"], a["ks"], a["v"], a["vs"], a["qsl"], a["seqs"],
                                    a["tokens"], a["heads"], a["kv_heads"], a["d"], a["dtype"], a["scale"],
-                                   a["stream"])
+                                   a["ws"], a["ws_bytes"], a["stream"])
 
 
 @pytest.mark.parametrize("over,status", [
@@ -58,3 +59,14 @@ def test_rejects_on_host(lib, over, status):
 def test_nothing_to_do_is_noop(lib):
     assert _call(lib, seqs=0) == 0
     assert _call(lib, tokens=0, out=0) == 0
+
+
+def test_workspace_size(lib):
+    size = lib.pa_prompt_attention_workspace_size
+    assert size(0, 0, 8, 8) > 0
+    # at least an entry per pair of query tiles: 256 tokens of 1 head, 64 of a group of 4
+    assert size(1, 25600, 8, 8) >= 100 * 16
+    assert size(1, 6400, 32, 8) >= 100 * 16
+    assert size(500, 500, 32, 8) >= 500 * 16
+    for bad in ((-1, 5, 8, 8), (1, -5, 8, 8), (1, 5, 0, 8), (1, 5, 8, 0), (1, 5, 9, 8), (1, 5, 258, 2)):
+        assert size(*bad) == 0

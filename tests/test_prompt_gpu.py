@@ -250,3 +250,19 @@ def test_refusals():
         api.prompt_attention(q.float(), k.float(), v.float(), loc, 0.1)
     with pytest.raises(native.PaError):
         api.prompt_attention(q, k, v, loc, 0.0)
+    with pytest.raises(native.PaError):
+        api.prompt_attention(q, k, v, loc, 0.1, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("h,hkv", [(8, 1), (8, 8)])
+def test_overlapping_start_rows_stay_inside_the_workspace(h, hkv):
+    """Start rows that go back and forth claim more work than the rows hold: the
+    call reports it, and writes nothing outside its buffers."""
+    n = 4000
+    q, k, v = rows(n, h, hkv, 64, torch.float16, 18)
+    loc = torch.tensor([0, n] * 20, dtype=torch.int32, device="cuda")
+    need = api.prompt_attention_workspace_size(39, n, h, hkv)
+    room = torch.full((need + 4096,), 0x5a, dtype=torch.uint8, device="cuda")
+    api.prompt_attention(q, k, v, loc, 0.1, workspace=room[:need])
+    assert api.get_device_error() == (-5, native.DEVERR_CONTEXT_LEN)
+    assert bool((room[need:] == 0x5a).all())
