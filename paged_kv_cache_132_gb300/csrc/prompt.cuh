@@ -33,11 +33,11 @@
 // whatever its weight is).  Keys need no such care: masked scores are replaced.
 //
 // Warp roles (512 threads, registers moved between the groups by setmaxnreg):
-//   warps 0-3, 4-7   softmax of query tile 0 / 1
-//   warps 8-11       outputs: O_i / row sum, rounded once, written to memory
-//   warp 12          MMA issuer, owner of the TMEM allocation
-//   warp 13          work items, Q, K and V copies (TMA)
-//   warps 14, 15     the V tiles with masked positions (above)
+//   warp 0           MMA issuer, owner of the TMEM allocation
+//   warp 1           work items, Q, K and V copies (TMA)
+//   warps 2, 3       the V tiles with masked positions (above)
+//   warps 4-7, 8-11  softmax of query tile 0 / 1
+//   warps 12-15      outputs: O_i / row sum, rounded once, written to memory
 // Every wait is bounded; a wait that runs out sets PA_DEVERR_TIMEOUT and makes
 // every role of the CTA leave, after what it issued has landed.
 #pragma once
@@ -62,10 +62,11 @@ struct PromptShape {
     static constexpr int NSLOT = D == 128 ? 5 : 8;  // K/V ring: K_0, V_0, K_1, V_1, ... one tile per slot
     static constexpr int NITEM = 4;              // work items announced ahead of their last reader
     static constexpr int SOFTMAX_WARPS = 4;      // per query tile
-    static constexpr int OUT_WARP = 8;           // first of four
-    static constexpr int MMA_WARP = 12;
-    static constexpr int LOAD_WARP = 13;
-    static constexpr int CHECK_WARP = 14;        // first of two
+    static constexpr int MMA_WARP = 0;
+    static constexpr int LOAD_WARP = 1;
+    static constexpr int CHECK_WARP = 2;         // first of two
+    static constexpr int SOFTMAX_WARP = 4;       // first of eight
+    static constexpr int OUT_WARP = 12;          // first of four
     static constexpr int THREADS = 512;
     static constexpr int ITEM_READERS = 8 + 4 + 1 + 2;  // softmax, output, MMA and check warps
     // Registers per thread after the split: 256 * 176 + 128 * 64 + 128 * 96
@@ -92,8 +93,7 @@ struct PromptShape {
         uint64_t check_go[NSLOT];   // the copy of a V tile with masked positions was issued (load warp)
         uint64_t v_checked[NSLOT];  // ... and the tile is fit for P.V (check warps)
         uint64_t s_full[2];         // S_i complete
-        uint64_t p_full[2];         // P_i written (softmax warps)
-        uint64_t pv_done[2];        // P_i V_j complete
+        uint64_t p_full[2][2];      // each half of P_i written (softmax warps)
         uint64_t o_full[2];         // last P_i V_j of the item complete
         uint64_t l_full[2];         // row sums written (softmax warps)
         uint64_t o_empty[2];        // O_i and the row sums read (output warps)
@@ -121,30 +121,27 @@ __device__ __forceinline__ void regs_dec() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
 }
 
-// A wait that also ends when another role of the CTA gave up.
-__device__ __forceinline__ bool prompt_wait_slow(uint64_t* bar, uint32_t parity, int* abort_flag, uint64_t lim,
+__device__ __forceinline__ bool prompt_aborted(int* abort_flag) { return *reinterpret_cast<volatile int*>(abort_flag); }
+
+// Waits for a phase of a barrier.  When the limit runs out, here or in another
+// role, every wait of the CTA ends: the roles run on to the end of their item
+// without data (nothing they write leaves their buffers; the load warp issues
+// nothing more) and then leave.
+__device__ __forceinline__ void prompt_wait_slow(uint64_t* bar, uint32_t parity, int* abort_flag, uint64_t lim,
                                                  int* err) {
     const uint64_t start = global_timer_ns();
-    while (true) {
-        for (int i = 0; i < 64; ++i)
-            if (mbar_try_wait(bar, parity)) return true;
-        if (*reinterpret_cast<volatile int*>(abort_flag)) return false;
+    while (!prompt_aborted(abort_flag)) {
+        for (int i = 0; i < 16; ++i)
+            if (mbar_try_wait(bar, parity)) return;
         if (global_timer_ns() - start > lim) {
             set_error(err, PA_DEVERR_TIMEOUT);
             atomicExch(abort_flag, 1);
-            return false;
         }
     }
 }
 template <class Smem>
-__device__ __forceinline__ bool prompt_wait(const PromptParams& p, Smem& sm, uint64_t* bar, uint32_t parity) {
-    if (mbar_try_wait(bar, parity)) return true;
-    return prompt_wait_slow(bar, parity, &sm.abort_flag, p.wait_limit_ns, p.err);
-}
-// The same for a whole warp: every lane observes the barrier, all leave together.
-template <class Smem>
-__device__ __forceinline__ bool prompt_wait_warp(const PromptParams& p, Smem& sm, uint64_t* bar, uint32_t parity) {
-    return __all_sync(kFullMask, prompt_wait(p, sm, bar, parity));
+__device__ __forceinline__ void prompt_wait(const PromptParams& p, Smem& sm, uint64_t* bar, uint32_t parity) {
+    if (!mbar_try_wait(bar, parity)) prompt_wait_slow(bar, parity, &sm.abort_flag, p.wait_limit_ns, p.err);
 }
 
 // What an item is made of, for every role alike.
@@ -178,7 +175,8 @@ template <class Shape>
 __device__ __forceinline__ bool prompt_next_item(const PromptParams& p, typename Shape::Smem& sm, int lane, int& n,
                                                  PromptItem& w) {
     const int st = n % Shape::NITEM;
-    if (!prompt_wait_warp(p, sm, &sm.item_full[st], (uint32_t)(n / Shape::NITEM) & 1u)) return false;
+    prompt_wait(p, sm, &sm.item_full[st], (uint32_t)(n / Shape::NITEM) & 1u);
+    if (__any_sync(kFullMask, prompt_aborted(&sm.abort_flag))) return false;
     const int4 it = sm.item[st];
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.item_empty[st]);
@@ -253,7 +251,8 @@ __device__ void prompt_load(const PromptParams& p, typename Shape::Smem& sm, int
     // One K or V tile of `rows` positions (rounded up to whole halves).
     auto load_tile = [&](const CUtensorMap* map, const PromptItem& w, int j, int end, bool check) {
         if (!ok) return;
-        ok = prompt_wait(p, sm, &sm.kv_empty[slot], (round & 1u) ^ 1u);
+        prompt_wait(p, sm, &sm.kv_empty[slot], (round & 1u) ^ 1u);
+        ok = !prompt_aborted(&sm.abort_flag);
         if (!ok) return;
         const int halves = end - j * Shape::BN > Shape::HALF ? 2 : 1;
         mbar_arrive_expect_tx(&sm.kv_full[slot], (uint32_t)(halves * Shape::SLABS * HALF_BYTES));
@@ -271,7 +270,8 @@ __device__ void prompt_load(const PromptParams& p, typename Shape::Smem& sm, int
     };
     auto load_q = [&](const PromptItem& w, int i) {
         if (!ok) return;
-        ok = prompt_wait(p, sm, &sm.q_empty[i], (q_used[i] & 1u) ^ 1u);
+        prompt_wait(p, sm, &sm.q_empty[i], (q_used[i] & 1u) ^ 1u);
+        ok = !prompt_aborted(&sm.abort_flag);
         if (!ok) return;
         mbar_arrive_expect_tx(&sm.q_full[i], q_bytes);
 #pragma unroll
@@ -304,7 +304,8 @@ __device__ void prompt_load(const PromptParams& p, typename Shape::Smem& sm, int
         int taken = 0;
         if (p.items && lane == 0) taken = (int)gridDim.x + atomicAdd(p.next_item, 1);
         const int st = n % Shape::NITEM;
-        if (!prompt_wait_warp(p, sm, &sm.item_empty[st], ((uint32_t)(n / Shape::NITEM) & 1u) ^ 1u)) break;
+        prompt_wait(p, sm, &sm.item_empty[st], ((uint32_t)(n / Shape::NITEM) & 1u) ^ 1u);
+        if (__any_sync(kFullMask, prompt_aborted(&sm.abort_flag))) break;
         if (lane == 0) {
             sm.item[st] = it;
             mbar_arrive(&sm.item_full[st]);
@@ -398,27 +399,25 @@ __device__ void prompt_mma(const PromptParams& p, typename Shape::Smem& sm, uint
         }
         prompt_commit(&sm.s_full[i]);
     };
-    // O_i (+)= P_i V over the same positions.
-    auto issue_pv = [&](int i, uint32_t slot, int cols, bool first) {
-        const uint32_t a = tmem + i * Shape::BN, o = tmem + Shape::O_COL + i * D;
-        const uint64_t b = dv + slot * SLOT16;
-        if (cols == Shape::BN) {
+    // O_i (+)= P_i V over one half (64) of the same positions.
+    auto issue_pv = [&](int i, uint32_t slot, int cols, int half, bool first) {
+        const uint32_t a = tmem + i * Shape::BN + half * 32, o = tmem + Shape::O_COL + i * D;
+        const uint64_t b = dv + slot * SLOT16 + half * 512;
+        if (cols >= half * 64 + 64) {
 #pragma unroll
-            for (int ks = 0; ks < Shape::BN / 16; ++ks)
+            for (int ks = 0; ks < 4; ++ks)
                 prompt_mma_ts(o, a + ks * 8, b + ks * 128, IDESC_O, (ks > 0 || !first) ? 1u : 0u);
         } else {
 #pragma unroll 1
-            for (int ks = 0; ks < cols / 16; ++ks)
+            for (int ks = 0; ks < (cols - half * 64) / 16; ++ks)
                 prompt_mma_ts(o, a + ks * 8, b + ks * 128, IDESC_O, (ks > 0 || !first) ? 1u : 0u);
         }
-        prompt_commit(&sm.pv_done[i]);
     };
     auto cols_of = [](int end, int j) { return min(Shape::BN, (end - j * Shape::BN + 15) & ~15); };
 
-    uint32_t slot = 0, round = 0;    // ring position of the next tile
-    uint32_t used = 0;               // bit i: parity of tile i's items so far
-    uint32_t np = 0;                 // bit i: of its P so far
-    uint32_t checked = 0;            // bit slot: of the slot's checked V tiles so far
+    uint32_t slot = 0, round = 0;  // ring position of the next tile, parity of its round
+    uint32_t used = 0, np = 0;     // bit i: parities of tile i's items and P so far
+    uint32_t checked = 0;          // bit slot: of the slot's checked V tiles so far
     auto advance = [&] {
         if (++slot == Shape::NSLOT) {
             slot = 0;
@@ -427,69 +426,59 @@ __device__ void prompt_mma(const PromptParams& p, typename Shape::Smem& sm, uint
     };
     int n = 0;
     PromptItem w;
-    bool ok = true;
-    while (ok && prompt_next_item<Shape>(p, sm, lane, n, w)) {
+    while (prompt_next_item<Shape>(p, sm, lane, n, w)) {
         const int tiles0 = w.tiles(0), tiles1 = w.tiles(1), nt = max(tiles0, tiles1);
         const int both = w.end1 ? 2 : 1;
-        // Tiles V_j and K_j+1, waited for before they are due: at the end of a
-        // step only P is, so that the tensor cores do not run dry meanwhile.
-        uint32_t vslot = 0, kslot = 0;
-        auto ready = [&](int j) {
-            vslot = slot;
-            if (j >= w.first_masked) {
-                ok = prompt_wait_warp(p, sm, &sm.v_checked[vslot], (checked >> vslot) & 1u);
-                checked ^= 1u << vslot;
-            } else {
-                ok = prompt_wait_warp(p, sm, &sm.kv_full[vslot], round);
-            }
-            advance();
-            if (j + 1 < nt) {
-                kslot = slot;
-                if (ok) ok = prompt_wait_warp(p, sm, &sm.kv_full[kslot], round);
-                advance();
-            }
-            tc_fence_after_sync();
-        };
-        ok = prompt_wait_warp(p, sm, &sm.kv_full[slot], round);
+        prompt_wait(p, sm, &sm.kv_full[slot], round);
 #pragma unroll 1
-        for (int i = 0; i < both && ok; ++i) {
-            ok = prompt_wait_warp(p, sm, &sm.q_full[i], (used >> i) & 1u);
-            tc_fence_after_sync();
-            if (ok) issue_s(i, slot, cols_of(w.end(i), 0));
+        for (int i = 0; i < both; ++i) {
+            prompt_wait(p, sm, &sm.q_full[i], (used >> i) & 1u);
+            issue_s(i, slot, cols_of(w.end(i), 0));
             if (w.tiles(i) == 1) prompt_commit(&sm.q_empty[i]);
         }
         prompt_commit(&sm.kv_empty[slot]);
         advance();
         // The accumulators: free once the output warps have read the item before.
 #pragma unroll 1
-        for (int i = 0; i < both && ok; ++i) ok = prompt_wait_warp(p, sm, &sm.o_empty[i], ((used >> i) & 1u) ^ 1u);
-        if (ok) ready(0);
+        for (int i = 0; i < both; ++i) prompt_wait(p, sm, &sm.o_empty[i], ((used >> i) & 1u) ^ 1u);
 #pragma unroll 1
-        for (int j = 0; j < nt && ok; ++j) {
-            const uint32_t vnow = vslot, know = kslot;
+        for (int j = 0; j < nt; ++j) {
+            // V_j and K_j+1 are waited for here, before the P that takes longest,
+            // so that between the MMAs of a step there is no wait but for P.
+            const uint32_t vslot = slot;
+            if (j >= w.first_masked) {
+                prompt_wait(p, sm, &sm.v_checked[vslot], (checked >> vslot) & 1u);
+                checked ^= 1u << vslot;
+            } else {
+                prompt_wait(p, sm, &sm.kv_full[vslot], round);
+            }
+            advance();
+            const uint32_t kslot = slot;
+            if (j + 1 < nt) {
+                prompt_wait(p, sm, &sm.kv_full[kslot], round);
+                advance();
+            }
 #pragma unroll 1
-            for (int i = 0; i < both && ok; ++i) {
+            for (int i = 0; i < both; ++i) {
                 const int nti = i ? tiles1 : tiles0;
-                const bool last = i + 1 == both;
-                if (j < nti) {
-                    ok = prompt_wait_warp(p, sm, &sm.p_full[i], (np >> i) & 1u);
-                    if (!ok) break;
-                    np ^= 1u << i;
-                    tc_fence_after_sync();
-                    issue_pv(i, vnow, cols_of(w.end(i), j), j == 0);
-                }
-                if (last) {
-                    prompt_commit(&sm.kv_empty[vnow]);
-                    if (j + 1 < nt) ready(j + 1);
-                }
+                if (j >= nti) continue;
+                const int cols = cols_of(w.end(i), j);
+                prompt_wait(p, sm, &sm.p_full[i][0], (np >> i) & 1u);
+                tc_fence_after_sync();
+                issue_pv(i, vslot, cols, 0, j == 0);
+                prompt_wait(p, sm, &sm.p_full[i][1], (np >> i) & 1u);
+                tc_fence_after_sync();
+                np ^= 1u << i;
+                issue_pv(i, vslot, cols, 1, false);
                 if (j + 1 < nti) {
-                    if (ok) issue_s(i, know, cols_of(w.end(i), j + 1));
+                    issue_s(i, kslot, cols_of(w.end(i), j + 1));
                     if (j + 2 == nti) prompt_commit(&sm.q_empty[i]);
-                } else if (j + 1 == nti) {
+                } else {
                     prompt_commit(&sm.o_full[i]);
                 }
             }
-            if (j + 1 < nt) prompt_commit(&sm.kv_empty[know]);
+            prompt_commit(&sm.kv_empty[vslot]);
+            if (j + 1 < nt) prompt_commit(&sm.kv_empty[kslot]);
         }
         used ^= both == 2 ? 3u : 1u;
     }
@@ -502,68 +491,53 @@ __device__ void prompt_mma(const PromptParams& p, typename Shape::Smem& sm, uint
 // ---------------------------------------------------------------------------
 // softmax warps of query tile i (thread r = row r = TMEM lane r)
 // ---------------------------------------------------------------------------
-// One K/V tile: P over S, the running maximum and sum.  MASKED: the tile holds
-// positions after some row's own, or fewer than 128 of the item's.
-template <typename T, bool MASKED>
-__device__ __forceinline__ void prompt_softmax_tile(uint32_t s_addr, float c, int last, int cols, float& m, float& l,
-                                                    float& alpha, bool& grow) {
-    constexpr int BN = 128;
-    const float NEG_INF = __int_as_float(0xff800000);
-    float x[BN];
+// 64 columns of this thread's TMEM lane, not waited for.  The registers hold
+// nothing before tmem_wait_ld(r), which names them so that no use moves ahead.
+__device__ __forceinline__ void tmem_ld_x64_async(uint32_t taddr, float (&r)[64]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];"
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]), "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]), "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31]), "=f"(r[32]), "=f"(r[33]), "=f"(r[34]), "=f"(r[35]), "=f"(r[36]), "=f"(r[37]), "=f"(r[38]), "=f"(r[39]), "=f"(r[40]), "=f"(r[41]), "=f"(r[42]), "=f"(r[43]), "=f"(r[44]), "=f"(r[45]), "=f"(r[46]), "=f"(r[47]), "=f"(r[48]), "=f"(r[49]), "=f"(r[50]), "=f"(r[51]), "=f"(r[52]), "=f"(r[53]), "=f"(r[54]), "=f"(r[55]), "=f"(r[56]), "=f"(r[57]), "=f"(r[58]), "=f"(r[59]), "=f"(r[60]), "=f"(r[61]), "=f"(r[62]), "=f"(r[63])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld(float (&r)[64]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]), "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15]), "+f"(r[16]), "+f"(r[17]), "+f"(r[18]), "+f"(r[19]), "+f"(r[20]), "+f"(r[21]), "+f"(r[22]), "+f"(r[23]), "+f"(r[24]), "+f"(r[25]), "+f"(r[26]), "+f"(r[27]), "+f"(r[28]), "+f"(r[29]), "+f"(r[30]), "+f"(r[31]), "+f"(r[32]), "+f"(r[33]), "+f"(r[34]), "+f"(r[35]), "+f"(r[36]), "+f"(r[37]), "+f"(r[38]), "+f"(r[39]), "+f"(r[40]), "+f"(r[41]), "+f"(r[42]), "+f"(r[43]), "+f"(r[44]), "+f"(r[45]), "+f"(r[46]), "+f"(r[47]), "+f"(r[48]), "+f"(r[49]), "+f"(r[50]), "+f"(r[51]), "+f"(r[52]), "+f"(r[53]), "+f"(r[54]), "+f"(r[55]), "+f"(r[56]), "+f"(r[57]), "+f"(r[58]), "+f"(r[59]), "+f"(r[60]), "+f"(r[61]), "+f"(r[62]), "+f"(r[63])
+                 :
+                 : "memory");
+}
+// Issue a store of 16 columns; tmem_wait_st() waits for all stores issued.
+__device__ __forceinline__ void tmem_st_x16_async(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
+                 :
+                 : "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+                 : "memory");
+}
+// The largest of three.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// 16 columns of this thread's accumulator lane, times a.
+__device__ __forceinline__ void prompt_scale16(uint32_t addr, float a) {
+    uint32_t u[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
+        : "r"(addr)
+        : "memory");
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        if (!MASKED || h * 64 < cols) {
-            uint32_t u[64];
-            tmem_ld_x64(s_addr + h * 64, u);
+    for (int k = 0; k < 16; ++k) u[k] = __float_as_uint(__uint_as_float(u[k]) * a);
+    tmem_st_x16_async(addr, u);
+}
+
+// Positions after `own` (-inf: no weight).
+__device__ __forceinline__ void mask64(float (&x)[64], int own) {
 #pragma unroll
-            for (int k = 0; k < 64; ++k) x[h * 64 + k] = __uint_as_float(u[k]);
-        } else {
-#pragma unroll
-            for (int k = 0; k < 64; ++k) x[h * 64 + k] = NEG_INF;
-        }
-    }
-    if (MASKED) {
-#pragma unroll
-        for (int k = 0; k < BN; ++k) x[k] = k <= last ? x[k] : NEG_INF;
-    }
-    float pm[8];
-#pragma unroll
-    for (int q = 0; q < 8; ++q) pm[q] = fmaxf(x[q], x[q + 8]);
-#pragma unroll
-    for (int k = 16; k < BN; k += 16)
-#pragma unroll
-        for (int q = 0; q < 8; ++q) pm[q] = fmaxf(fmaxf(pm[q], x[k + q]), x[k + 8 + q]);
-    const float mx =
-        fmaxf(fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])), fmaxf(fmaxf(pm[4], pm[5]), fmaxf(pm[6], pm[7])));
-    const float m_new = fmaxf(m, mx * c);
-    grow = m_new > m + 8.f;  // always on the first tile (m = -inf)
-    alpha = 1.f;
-    if (grow) {
-        alpha = prompt_exp2(m - m_new);
-        m = m_new;
-        l *= alpha;
-    }
-    const float nm = -m;
-    float ps[8];
-#pragma unroll
-    for (int q = 0; q < 8; ++q) ps[q] = 0.f;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        if (MASKED && h * 64 >= cols) break;
-        uint32_t u[32];
-#pragma unroll
-        for (int k = 0; k < 64; k += 2) {
-            float& a = x[h * 64 + k];
-            float& b = x[h * 64 + k + 1];
-            fma2_rn(a, b, c, c, nm, nm);
-            a = prompt_exp2(a);
-            b = prompt_exp2(b);
-            add2_rn(ps[k & 7], ps[(k & 7) + 1], a, b);
-            u[k >> 1] = pack_rn<T>(a, b);
-        }
-        tmem_st_x32_async(s_addr + h * 32, u);
-    }
-    l += ((ps[0] + ps[1]) + (ps[2] + ps[3])) + ((ps[4] + ps[5]) + (ps[6] + ps[7]));
+    for (int k = 0; k < 64; ++k) x[k] = k <= own ? x[k] : __int_as_float(0xff800000);
 }
 
 template <typename T, class Shape>
@@ -575,6 +549,7 @@ __device__ void prompt_softmax(const PromptParams& p, typename Shape::Smem& sm, 
     const uint32_t lanes = (uint32_t)(warp * 32) << 16;
     const uint32_t s_addr = tmem + lanes + i * Shape::BN, o_addr = tmem + lanes + Shape::O_COL + i * D;
     const float c = p.scale_log2;  // > 0
+    const float NEG_INF = __int_as_float(0xff800000);
     uint32_t ns = 0, used = 0;     // S_i and items so far
     int n = 0;
     PromptItem w;
@@ -584,42 +559,80 @@ __device__ void prompt_softmax(const PromptParams& p, typename Shape::Smem& sm, 
         const int token = w.t0 + i * p.tile_tokens + t;
         // Rows past the tile's tokens compute something and are not stored.
         const int last = t < p.tile_tokens && token < w.len ? token : end - 1;
-        float m = __int_as_float(0xff800000), l = 0.f;
-        bool ok = true;
-        for (int j = 0; j < nt && ok; ++j, ++ns) {
-            ok = prompt_wait_warp(p, sm, &sm.s_full[i], ns & 1u);
-            if (!ok) break;
+        float m = NEG_INF, l = 0.f;
+        for (int j = 0; j < nt; ++j, ++ns) {
+            prompt_wait(p, sm, &sm.s_full[i], ns & 1u);
             tc_fence_after_sync();
-            float alpha;
-            bool grow;
-            if (j >= w.first_masked) {
-                const int kv0 = j * Shape::BN;
-                prompt_softmax_tile<T, true>(s_addr, c, last - kv0, end - kv0, m, l, alpha, grow);
-            } else {
-                prompt_softmax_tile<T, false>(s_addr, c, 0, 0, m, l, alpha, grow);
-            }
-            // A grown maximum rescales O_i, once P_i V of the previous tile has completed.
-            if (j > 0 && __any_sync(kFullMask, grow)) {
-                ok = prompt_wait_warp(p, sm, &sm.pv_done[i], (ns - 1) & 1u);
-                if (!ok) break;
-                tc_fence_after_sync();
-#pragma unroll 1
-                for (int c0 = 0; c0 < D; c0 += 32) {
-                    uint32_t u[32];
-                    tmem_ld_x32(o_addr + c0, u);
+            float x0[64], x1[64];  // scores of positions kv0 .. kv0 + 63, kv0 + 64 .. kv0 + 127
+            const int kv0 = j * Shape::BN;
+            const int cols = min(Shape::BN, end - kv0);
+            // The second half loads while the first one's maximum is taken.
+            tmem_ld_x64_async(s_addr, x0);
+            tmem_wait_ld(x0);
+            tmem_ld_x64_async(s_addr + 64, x1);
+            const int own = j >= w.first_masked ? last - kv0 : Shape::BN;
+            float pm[8];
+            if (own < 63) mask64(x0, own);
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) u[k] = __float_as_uint(__uint_as_float(u[k]) * alpha);
-                    tmem_st_x32(o_addr + c0, u);
-                }
+            for (int q = 0; q < 8; ++q) pm[q] = fmaxf(x0[q], x0[q + 8]);
+#pragma unroll
+            for (int k = 16; k < 64; k += 16)
+#pragma unroll
+                for (int q = 0; q < 8; ++q) pm[q] = max3(pm[q], x0[k + q], x0[k + q + 8]);
+            tmem_wait_ld(x1);
+            if (own < 127) mask64(x1, own - 64);
+#pragma unroll
+            for (int k = 0; k < 64; k += 16)
+#pragma unroll
+                for (int q = 0; q < 8; ++q) pm[q] = max3(pm[q], x1[k + q], x1[k + q + 8]);
+            const float mx = max3(max3(pm[0], pm[1], pm[2]), max3(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7]));
+            const float m_new = fmaxf(m, mx * c);
+            const bool grow = m_new > m + 8.f;  // always on the first tile (m = -inf)
+            float alpha = 1.f;
+            if (grow) {
+                alpha = prompt_exp2(m - m_new);
+                m = m_new;
+                l *= alpha;
             }
-            tmem_wait_st();
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.p_full[i]);
+            // A grown maximum rescales O_i: S_i was issued after P_i V of the tile
+            // before, by the same thread, so that has completed too.
+            if (j > 0 && __any_sync(kFullMask, grow)) {
+#pragma unroll 1
+                for (int c0 = 0; c0 < D; c0 += 16) prompt_scale16(o_addr + c0, alpha);
+                tmem_wait_st();
+            }
+            // P in four pieces of 32 positions; P.V starts on the first half
+            // while the second is made.
+            const float nm = -m;
+            float ps[4] = {0.f, 0.f, 0.f, 0.f};
+            auto piece = [&](float* x, uint32_t addr) {
+                uint32_t u[16];
+#pragma unroll
+                for (int k = 0; k < 32; k += 2) {
+                    fma2_rn(x[k], x[k + 1], c, c, nm, nm);
+                    x[k] = prompt_exp2(x[k]);
+                    x[k + 1] = prompt_exp2(x[k + 1]);
+                    add2_rn(ps[k & 2], ps[(k & 2) + 1], x[k], x[k + 1]);
+                    u[k >> 1] = pack_rn<T>(x[k], x[k + 1]);
+                }
+                tmem_st_x16_async(addr, u);
+            };
+            auto written = [&](int half) {
+                tmem_wait_st();
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.p_full[i][half]);
+            };
+            piece(x0, s_addr);
+            piece(x0 + 32, s_addr + 16);
+            if (cols > 64) piece(x1, s_addr + 32);
+            written(0);
+            if (cols > 64) piece(x1 + 32, s_addr + 48);
+            written(1);
+            l += (ps[0] + ps[1]) + (ps[2] + ps[3]);
         }
-        if (!ok) break;
         // The row sums, once the output warps have read the previous item's.
-        if (!prompt_wait_warp(p, sm, &sm.o_empty[i], (used & 1u) ^ 1u)) break;
+        prompt_wait(p, sm, &sm.o_empty[i], (used & 1u) ^ 1u);
         ++used;
         sm.row_sum[i][r] = l;
         __syncwarp();
@@ -650,15 +663,13 @@ __device__ void prompt_check(const PromptParams& p, typename Shape::Smem& sm, in
     PromptItem w;
     while (prompt_next_item<Shape>(p, sm, lane, n, w)) {
         const int end = w.last(), nt = (end + 127) >> 7;
-        bool ok = true;
-        for (int j = w.first_masked; j < nt && ok; ++j) {
+        for (int j = w.first_masked; j < nt; ++j) {
             const uint32_t tile = tiles + 2 * j + 1;  // K_0, V_0, K_1, ...
             const uint32_t slot = tile % Shape::NSLOT;
             // Issued first: before that the slot's barrier may still be two
             // phases back, which its parity does not tell from complete.
-            ok = prompt_wait_warp(p, sm, &sm.check_go[slot], (parity >> slot) & 1u) &&
-                 prompt_wait_warp(p, sm, &sm.kv_full[slot], (tile / Shape::NSLOT) & 1u);
-            if (!ok) break;
+            prompt_wait(p, sm, &sm.check_go[slot], (parity >> slot) & 1u);
+            prompt_wait(p, sm, &sm.kv_full[slot], (tile / Shape::NSLOT) & 1u);
             parity ^= 1u << slot;
             // Rows up to the item's first token are attended by all its rows.
             const int first = max(w.t0 + 1 - j * Shape::BN, 0);
@@ -688,7 +699,6 @@ __device__ void prompt_check(const PromptParams& p, typename Shape::Smem& sm, in
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.v_checked[slot]);
         }
-        if (!ok) break;
         tiles += 2 * nt;
     }
 }
@@ -721,13 +731,11 @@ __device__ void prompt_output(const PromptParams& p, typename Shape::Smem& sm, u
     int n = 0;
     PromptItem w;
     while (prompt_next_item<Shape>(p, sm, lane, n, w)) {
-        bool ok = true;
 #pragma unroll 1
         for (int i = 0; i < 2; ++i) {
             if (!w.end(i)) continue;
-            ok = prompt_wait_warp(p, sm, &sm.l_full[i], (parity >> i) & 1u) &&
-                 prompt_wait_warp(p, sm, &sm.o_full[i], (parity >> i) & 1u);
-            if (!ok) break;
+            prompt_wait(p, sm, &sm.l_full[i], (parity >> i) & 1u);
+            prompt_wait(p, sm, &sm.o_full[i], (parity >> i) & 1u);
             parity ^= 1u << i;
             tc_fence_after_sync();
             const float l = sm.row_sum[i][r];
@@ -760,7 +768,6 @@ __device__ void prompt_output(const PromptParams& p, typename Shape::Smem& sm, u
             }
             if (store && dirty) prompt_add_nonfinite<T, D>(p, w, token, dst);
         }
-        if (!ok) break;
     }
 }
 
@@ -796,8 +803,8 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
             mbar_init(&sm.q_full[i], 1);
             mbar_init(&sm.q_empty[i], 1);
             mbar_init(&sm.s_full[i], 1);
-            mbar_init(&sm.p_full[i], Shape::SOFTMAX_WARPS);
-            mbar_init(&sm.pv_done[i], 1);
+            mbar_init(&sm.p_full[i][0], Shape::SOFTMAX_WARPS);
+            mbar_init(&sm.p_full[i][1], Shape::SOFTMAX_WARPS);
             mbar_init(&sm.o_full[i], 1);
             mbar_init(&sm.l_full[i], Shape::SOFTMAX_WARPS);
             mbar_init(&sm.o_empty[i], 4);
@@ -815,13 +822,7 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
     // The kernel that wrote the start rows, q, k and v may still be finishing.
     pdl_wait_prerequisites();
 
-    if (warp < 8) {
-        regs_inc<Shape::REGS_SOFTMAX>();
-        prompt_softmax<T, Shape>(p, sm, tmem, warp >> 2, warp & 3, lane);
-    } else if (warp < Shape::MMA_WARP) {
-        regs_dec<Shape::REGS_OUT>();
-        prompt_output<T, Shape>(p, sm, tmem, warp - Shape::OUT_WARP, lane);
-    } else {
+    if (warp < Shape::SOFTMAX_WARP) {
         regs_dec<Shape::REGS_OTHER>();
         if (warp == Shape::MMA_WARP)
             prompt_mma<Shape, std::is_same<T, __nv_bfloat16>::value>(p, sm, tmem, lane);
@@ -829,6 +830,13 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
             prompt_load<Shape>(p, sm, lane, &tmap_q, &tmap_k, &tmap_v);
         else
             prompt_check<T, Shape>(p, sm, threadIdx.x - Shape::CHECK_WARP * 32);
+    } else if (warp < Shape::OUT_WARP) {
+        regs_inc<Shape::REGS_SOFTMAX>();
+        const int v = warp - Shape::SOFTMAX_WARP;
+        prompt_softmax<T, Shape>(p, sm, tmem, v >> 2, v & 3, lane);
+    } else {
+        regs_dec<Shape::REGS_OUT>();
+        prompt_output<T, Shape>(p, sm, tmem, warp - Shape::OUT_WARP, lane);
     }
 
     tc_fence_before_sync();
