@@ -131,6 +131,7 @@ __device__ __forceinline__ void prompt_wait_slow(uint64_t* bar, uint32_t parity,
                                                  int* err) {
     const uint64_t start = global_timer_ns();
     while (!prompt_aborted(abort_flag)) {
+#pragma unroll 1
         for (int i = 0; i < 16; ++i)
             if (mbar_try_wait(bar, parity)) return;
         if (global_timer_ns() - start > lim) {
@@ -348,34 +349,18 @@ __device__ void prompt_load(const PromptParams& p, typename Shape::Smem& sm, int
 // The whole warp runs the issue loop and one elected lane issues: descriptors
 // then stay in uniform registers.  With the loop inside `if (lane == 0)` every
 // MMA waited for its operands to be moved there, about 115 cycles an MMA
-// against the 64 that it runs for (measured: 4500 against 2300 cycles per
-// tile of both query tiles).
-__device__ __forceinline__ void prompt_mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                              uint32_t accumulate) {
+// against the 64 that it runs for.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t lead;
     asm volatile(
-        "{\n\t.reg .pred lead, acc;\n\t"
-        "elect.sync _|lead, 0xffffffff;\n\t"
-        "setp.ne.b32 acc, %4, 0;\n\t"
-        "@lead tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, acc;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-__device__ __forceinline__ void prompt_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                              uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred lead, acc;\n\t"
-        "elect.sync _|lead, 0xffffffff;\n\t"
-        "setp.ne.b32 acc, %4, 0;\n\t"
-        "@lead tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, acc;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-        : "memory");
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(lead));
+    return lead != 0;
 }
 __device__ __forceinline__ void prompt_commit(uint64_t* bar) {
-    asm volatile(
-        "{\n\t.reg .pred lead;\n\t"
-        "elect.sync _|lead, 0xffffffff;\n\t"
-        "@lead tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_addr(bar))
-        : "memory");
+    if (elect_one()) mma_commit(bar);
 }
 
 template <class Shape, bool BF16>
@@ -392,26 +377,27 @@ __device__ void prompt_mma(const PromptParams& p, typename Shape::Smem& sm, uint
     auto issue_s = [&](int i, uint32_t slot, int cols) {
         const uint32_t idesc = IDESC_S | ((uint32_t)(cols >> 3) << 17), d = tmem + i * Shape::BN;
         const uint64_t a = dq + i * Q16, b = dk + slot * SLOT16;
+        if (elect_one()) {
 #pragma unroll
-        for (int ks = 0; ks < Shape::SLABS * 4; ++ks) {
-            const uint32_t off = (uint32_t)((ks >> 2) * (Shape::SLAB >> 4) + (ks & 3) * 2);
-            prompt_mma_ss(d, a + off, b + off, idesc, ks > 0 ? 1u : 0u);
+            for (int ks = 0; ks < Shape::SLABS * 4; ++ks) {
+                const uint32_t off = (uint32_t)((ks >> 2) * (Shape::SLAB >> 4) + (ks & 3) * 2);
+                mma_f16_ss(d, a + off, b + off, idesc, ks > 0 ? 1u : 0u);
+            }
+            mma_commit(&sm.s_full[i]);
         }
-        prompt_commit(&sm.s_full[i]);
+        __syncwarp();
     };
     // O_i (+)= P_i V over one half (64) of the same positions.
     auto issue_pv = [&](int i, uint32_t slot, int cols, int half, bool first) {
         const uint32_t a = tmem + i * Shape::BN + half * 32, o = tmem + Shape::O_COL + i * D;
         const uint64_t b = dv + slot * SLOT16 + half * 512;
-        if (cols >= half * 64 + 64) {
+        if (elect_one()) {
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
-                prompt_mma_ts(o, a + ks * 8, b + ks * 128, IDESC_O, (ks > 0 || !first) ? 1u : 0u);
-        } else {
-#pragma unroll 1
-            for (int ks = 0; ks < (cols - half * 64) / 16; ++ks)
-                prompt_mma_ts(o, a + ks * 8, b + ks * 128, IDESC_O, (ks > 0 || !first) ? 1u : 0u);
+                if (half * 64 + ks * 16 < cols)
+                    mma_f16_ts(o, a + ks * 8, b + ks * 128, IDESC_O, (ks > 0 || !first) ? 1u : 0u);
         }
+        __syncwarp();
     };
     auto cols_of = [](int end, int j) { return min(Shape::BN, (end - j * Shape::BN + 15) & ~15); };
 
