@@ -70,6 +70,10 @@ typedef enum {
                                        or > the max_context_len the call was sized for    */
 #define PA_DEVERR_COPY_PAIR    0x8  /* copy or swap pair id outside its pool                */
 #define PA_DEVERR_TIMEOUT      0x10 /* a bounded wait inside a kernel ran out              */
+#define PA_DEVERR_POSITION     0x80 /* position >= the rows of the rotary table             */
+#define PA_DEVERR_STEP         0x100 /* a step needs more blocks than are free, more ring
+                                        entries or more token rows than there are, or its
+                                        free_state is out of range                         */
 /* Reported only in checked mode (PA_OPT_DEBUG_CHECKS, below): */
 #define PA_DEVERR_DUP_SLOT     0x20 /* two tokens of one cache write share a slot          */
 #define PA_DEVERR_PAIR_CONFLICT 0x40 /* copy/swap pairs: a destination repeated, or (same
@@ -141,6 +145,81 @@ typedef struct {
 int pa_reshape_and_cache(const void *key, const void *value, void *k_cache, void *v_cache,
                          const int64_t *slot_mapping, int64_t num_tokens,
                          const pa_cache_desc *cache, void *stream);
+
+/*
+ * Rotary embedding of new query and key rows, fused with the cache write
+ * ("Efficient Memory Management ... PagedAttention Review", §3-2 "fused reshape
+ * and block write").  For every token t with position i = positions[t] >= 0,
+ * pair number j of the first rotary_dim elements (a, b) of every query and key
+ * head becomes
+ *     a cos[i][j] - b sin[i][j],  b cos[i][j] + a sin[i][j],
+ * computed in binary32 and rounded once; elements from rotary_dim on stay.  The
+ * rotated query goes to query_out, the rotated key to key_out (unless NULL) and,
+ * with the value, to slot slot_mapping[t] of the pools as pa_reshape_and_cache
+ * writes it.
+ *   interleaved   0: pair j is elements j and j + rotary_dim / 2; 1: 2j and 2j + 1
+ *   cos_sin       device, float [num_positions][rotary_dim]: row i holds its
+ *                 rotary_dim / 2 cosines, then the sines
+ *   positions     device, int32 [num_tokens]; a negative one marks a padding row:
+ *                 nothing of it is written
+ *   slot_mapping  device, int64 [num_tokens], entries >= 0 distinct; a negative
+ *                 one is not cached (its row is still rotated)
+ *   query, key, value, query_out, key_out   device, of the cache dtype: rows of
+ *                 num_heads (query) or cache->num_kv_heads heads of head_dim
+ *                 contiguous elements; *_stride elements from one token's row to
+ *                 the next, at least the row, a multiple of 16 bytes.  query_out
+ *                 may be query and key_out key (same stride); no other overlap.
+ * A position >= num_positions sets PA_DEVERR_POSITION and the token is skipped;
+ * a slot >= num_blocks * B sets PA_DEVERR_SLOT and the token is not cached.
+ * Checked mode: as pa_reshape_and_cache.  Supported: any cache dtype, rotary_dim
+ * elements a multiple of 32 bytes; else PA_ERR_UNSUPPORTED.
+ */
+int pa_rotary_and_cache(void *query_out, int64_t query_out_stride, void *key_out, int64_t key_out_stride,
+                        const void *query, int64_t query_stride, const void *key, int64_t key_stride,
+                        const void *value, int64_t value_stride, const int32_t *positions,
+                        const float *cos_sin, int32_t num_positions, int32_t rotary_dim,
+                        int32_t interleaved, void *k_cache, void *v_cache,
+                        const int64_t *slot_mapping, int64_t num_tokens, int32_t num_heads,
+                        const pa_cache_desc *cache, void *stream);
+
+/*
+ * Plan of a serving step on the GPU: block tables, slots and positions from
+ * request lengths ("paged-attention은 도대체 뭘 최적화 하는 것일까", §6, §17,
+ * §18 step 8), as a host block manager that visits the sequences in order would
+ * make them.  The free blocks are a ring of block ids, free_state = {index of
+ * the first one, how many}.  First, every finished sequence (new_lens[s] = -1)
+ * appends its ceil(context_lens[s] / B) blocks to the ring's end, in order; then
+ * every growing one (new_lens[s] = n > 0) takes
+ * ceil((context_lens[s] + n) / B) - ceil(context_lens[s] / B) blocks from its
+ * head into its table row; new_lens[s] = 0 leaves a sequence as it is.
+ *   new_lens, context_lens  device, int32 [num_seqs]
+ *   context_lens_out  device, int32 [num_seqs]: 0, or context_lens[s] + n.  May
+ *                     be context_lens
+ *   free_ring         device, int32 [ring_size]; only entries behind the last
+ *                     free one are written
+ *   free_state, free_state_out  device, int32 [2].  May be the same
+ *   block_tables      device, int32 [num_seqs][max_blocks_per_seq]; only the
+ *                     entries of blocks taken are written
+ *   query_start_loc   device, int32 [num_seqs + 1]: prefix sums of the new tokens
+ *   slot_mapping, positions   device, int64 and int32 [max_tokens]: where each
+ *                     new token goes, sequence after sequence; -1 behind the last
+ *                     one, which pa_reshape_and_cache and pa_rotary_and_cache skip
+ *   max_tokens        host, >= the new tokens (a captured graph's largest step)
+ * Blocks belong to one sequence each: shared ones are the host manager's.
+ * A sequence whose lengths are negative (but -1) or beyond its table row sets
+ * PA_DEVERR_CONTEXT_LEN and stays as it is.  A step that does not fit -- blocks,
+ * ring entries, token rows -- sets PA_DEVERR_STEP and is refused whole: lengths,
+ * tables and free blocks stay, query_start_loc is 0 and slots are -1.  A block id
+ * outside [0, num_blocks) in the ring or a table sets PA_DEVERR_BLOCK_ID, and
+ * tokens in it get slot -1.  num_seqs <= 16384, else PA_ERR_UNSUPPORTED.
+ */
+int pa_plan_step(const int32_t *new_lens, const int32_t *context_lens, int32_t *context_lens_out,
+                 int32_t num_seqs, int32_t *free_ring, int32_t ring_size,
+                 const int32_t *free_state, int32_t *free_state_out,
+                 int64_t num_blocks, int32_t block_size,
+                 int32_t *block_tables, int32_t max_blocks_per_seq,
+                 int32_t *query_start_loc, int64_t *slot_mapping, int32_t *positions,
+                 int32_t max_tokens, void *stream);
 
 /*
  * Bytes of device workspace pa_decode needs for a batch of at most num_seqs

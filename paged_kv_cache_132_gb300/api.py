@@ -9,7 +9,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
-from typing import Iterator, Optional, Sequence, Tuple
+from typing import Iterator, NamedTuple, Optional, Sequence, Tuple
 
 import torch
 
@@ -245,6 +245,105 @@ def _token_stride(t: torch.Tensor, name: str) -> int:
     if by_token < heads * d:
         raise ValueError(f"{name}: rows of tokens must not overlap")
     return by_token
+
+
+def rotary_and_cache(query: torch.Tensor, key: torch.Tensor, value: torch.Tensor, positions: torch.Tensor,
+                     cos_sin: torch.Tensor, slot_mapping: torch.Tensor, k_cache: torch.Tensor,
+                     v_cache: torch.Tensor, *, interleaved: bool = False, query_out: Optional[torch.Tensor] = None,
+                     key_out: Optional[torch.Tensor] = None,
+                     stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Rotate the first rotary_dim elements of every query and key head by the
+    angles of positions[t], write the keys and values to slot_mapping[t] (< 0:
+    not cached) and return the rotated query [T][H][d]; the rotated keys too go
+    to ``key_out`` where that is given.  ``cos_sin`` is float32
+    [positions][rotary_dim], cosines then sines.  A token at a negative position
+    is padding: nothing of it is written (a new query_out is undefined there).
+    The rows may be slices of a fused projection's rows, and query_out / key_out
+    the query / key themselves."""
+    lib = native.load()
+    _require(query.dim() == 3 and key.dim() == 3 and k_cache.dim() == 4, "rows are [tokens][heads][head_dim]")
+    t, h, d = query.shape
+    desc = cache_desc(k_cache)
+    _require(k_cache.shape == v_cache.shape and k_cache.dtype == v_cache.dtype and k_cache.is_contiguous()
+             and v_cache.is_contiguous(), "K and V pools must match and be contiguous")
+    _require(key.shape == value.shape and tuple(key.shape) == (t, desc.num_kv_heads, d) and d == desc.head_dim,
+             "key/value are [num_tokens][num_kv_heads][head_dim] of the pools")
+    _require(query.dtype == k_cache.dtype and key.dtype == k_cache.dtype and value.dtype == k_cache.dtype,
+             "query, key and value share the pools' dtype")
+    _require(positions.dtype == torch.int32 and positions.dim() == 1 and positions.numel() == t
+             and positions.is_contiguous(), "positions is int32 [T]")
+    _require(slot_mapping.dtype == torch.int64 and slot_mapping.dim() == 1 and slot_mapping.numel() == t
+             and slot_mapping.is_contiguous(), "slot_mapping is int64 [T]")
+    _require(cos_sin.dtype == torch.float32 and cos_sin.dim() == 2 and cos_sin.is_contiguous(),
+             "cos_sin is float32 [positions][rotary_dim]")
+    if query_out is None:
+        query_out = _empty((t, h, d), query.dtype, query.device, stream)
+    _require(query_out.shape == query.shape and query_out.dtype == query.dtype, "query_out is like query")
+    _require_here(query, key, value, positions, cos_sin, slot_mapping, k_cache, v_cache, query_out)
+    key_ptr, key_stride = None, 0
+    if key_out is not None:
+        _require(key_out.shape == key.shape and key_out.dtype == key.dtype, "key_out is like key")
+        _require_here(key_out)
+        key_ptr, key_stride = key_out.data_ptr(), _token_stride(key_out, "key_out")
+    _raise(lib.pa_rotary_and_cache(query_out.data_ptr(), _token_stride(query_out, "query_out"), key_ptr, key_stride,
+                                   query.data_ptr(), _token_stride(query, "query"), key.data_ptr(),
+                                   _token_stride(key, "key"), value.data_ptr(), _token_stride(value, "value"),
+                                   positions.data_ptr(), cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1],
+                                   1 if interleaved else 0, k_cache.data_ptr(), v_cache.data_ptr(),
+                                   slot_mapping.data_ptr(), t, h, ctypes.byref(desc), _stream_ptr(stream)),
+           "pa_rotary_and_cache")
+    return query_out
+
+
+class StepPlan(NamedTuple):
+    """What plan_step makes (device tensors)."""
+    context_lens: torch.Tensor      # int32 [S] after the step
+    free_state: torch.Tensor        # int32 [2] first free entry of the ring, free blocks
+    query_start_loc: torch.Tensor   # int32 [S + 1]
+    slot_mapping: torch.Tensor      # int64 [max_tokens], -1 behind the last token
+    positions: torch.Tensor         # int32 [max_tokens], -1 behind the last token
+
+
+def plan_step(new_lens: torch.Tensor, context_lens: torch.Tensor, free_ring: torch.Tensor, free_state: torch.Tensor,
+              block_tables: torch.Tensor, block_size: int, max_tokens: int, num_blocks: int, *,
+              out: Optional[StepPlan] = None, stream: Optional[torch.cuda.Stream] = None) -> StepPlan:
+    """Plan a step on the GPU: take blocks for the new_lens[s] tokens that each
+    sequence gains (-1: finished, its blocks go back; 0: idle), write them into
+    block_tables, and return the lengths after the step, the free blocks left,
+    the start rows and every new token's slot and position.
+
+    ``free_ring`` int32 holds the free block ids from entry free_state[0] on,
+    free_state[1] of them, wrapping around.  ``out`` may reuse buffers, the
+    inputs context_lens and free_state among them (a captured step that advances
+    in place).  A step that does not fit is refused whole (get_device_error)."""
+    lib = native.load()
+    s = new_lens.numel()
+    _require(max_tokens >= 0, "max_tokens must not be negative")
+    for t, n in ((new_lens, s), (context_lens, s), (free_state, 2)):
+        _require(t.dtype == torch.int32 and t.dim() == 1 and t.numel() == n and t.is_contiguous(),
+                 "new_lens and context_lens are int32 [num_seqs], free_state int32 [2]")
+    _require(free_ring.dtype == torch.int32 and free_ring.dim() == 1 and free_ring.is_contiguous(),
+             "free_ring is int32 [ring_size]")
+    _require(block_tables.dtype == torch.int32 and block_tables.dim() == 2 and block_tables.shape[0] == s
+             and block_tables.is_contiguous(), "block_tables is int32 [num_seqs][max_blocks]")
+    if out is None:
+        dev, i32 = new_lens.device, torch.int32
+        out = StepPlan(_empty((s,), i32, dev, stream), _empty((2,), i32, dev, stream),
+                       _empty((s + 1,), i32, dev, stream), _empty((max_tokens,), torch.int64, dev, stream),
+                       _empty((max_tokens,), i32, dev, stream))
+    else:
+        for t, n, dt in zip(out, (s, 2, s + 1, max_tokens, max_tokens),
+                            (torch.int32, torch.int32, torch.int32, torch.int64, torch.int32)):
+            _require(t.dtype == dt and t.dim() == 1 and t.numel() == n and t.is_contiguous(),
+                     "out is (context_lens [S], free_state [2], query_start_loc [S + 1], slot_mapping int64 [T], "
+                     "positions [T])")
+    _require_here(new_lens, context_lens, free_ring, free_state, block_tables, *out)
+    _raise(lib.pa_plan_step(new_lens.data_ptr(), context_lens.data_ptr(), out[0].data_ptr(), s, free_ring.data_ptr(),
+                            free_ring.numel(), free_state.data_ptr(), out[1].data_ptr(), int(num_blocks),
+                            int(block_size), block_tables.data_ptr(), block_tables.shape[1], out[2].data_ptr(),
+                            out[3].data_ptr(), out[4].data_ptr(), int(max_tokens), _stream_ptr(stream)),
+           "pa_plan_step")
+    return out
 
 
 def prompt_attention_workspace_size(num_seqs: int, num_tokens: int, num_heads: int, num_kv_heads: int) -> int:

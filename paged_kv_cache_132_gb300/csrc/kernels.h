@@ -30,6 +30,64 @@ cudaError_t launch_swap_blocks(void* const* src_k, void* const* src_v, int64_t s
                                void* const* dst_v, int64_t dst_num_blocks, int num_layers, const int64_t* pairs,
                                int64_t num_pairs, const PoolShape& shape, int* err, cudaStream_t stream);
 
+// ---- rotary embedding fused with the cache write (rotary.cu) ------------------
+struct RotaryParams {
+    // rows of `chunks` 16-byte chunks per head; strides from token to token, in
+    // elements as given to launch_rotary, in chunks inside the kernel
+    const void* query;
+    const void* key;
+    const void* value;
+    void* query_out;
+    void* key_out;               // or nullptr: the rotated keys only go to the pool
+    int64_t query_stride, key_stride, value_stride, query_out_stride, key_out_stride;
+    const int32_t* positions;    // [num_tokens]; < 0: padding row
+    const int64_t* slot_mapping; // [num_tokens]; < 0: not cached
+    const float* cos_sin;        // [num_positions][rotary_dim]: cosines, then sines
+    int num_positions;
+    int rotary_dim;
+    void* k_cache;
+    void* v_cache;
+    int num_heads;
+    int num_kv_heads;
+    int block_size;
+    int64_t num_slots;
+    int* err;
+    // set by launch_rotary
+    int chunks;     // 16-byte chunks of a head row
+    int lanes;      // lanes of a head row, two chunks each
+    int rot_lanes;  // the first of them, whose chunks rotate
+};
+
+bool rotary_supported(int head_dim, int rotary_dim, int elem_bytes);
+cudaError_t launch_rotary(RotaryParams p, int dtype, int head_dim, int elem_bytes, bool interleaved,
+                          int64_t num_tokens, cudaStream_t stream);
+
+// ---- plan of a step (step_plan.cu) ---------------------------------------------
+struct StepPlanParams {
+    const int32_t* new_lens;      // [num_seqs] tokens the step adds; -1: finished
+    const int32_t* context_lens;  // [num_seqs]
+    int32_t* context_lens_out;    // may be context_lens
+    int num_seqs;
+    int32_t* free_ring;           // [ring_size]
+    int ring_size;
+    const int32_t* free_state;    // {head, count}
+    int32_t* free_state_out;      // may be free_state
+    int64_t num_blocks;
+    int block_size;
+    int32_t* block_tables;        // [num_seqs][max_blocks]
+    int max_blocks;
+    int ctx_cap;                  // max_blocks * block_size, at most INT_MAX
+    int32_t* query_start_loc;     // [num_seqs + 1]
+    int64_t* slot_mapping;        // [max_tokens]
+    int32_t* positions;           // [max_tokens]
+    int max_tokens;
+    int* err;
+    bool place_tokens;            // set by launch_step_plan: slots and positions in the planning CTA
+};
+
+constexpr int kMaxStepSeqs = 16384;  // two prefix sums of so many sequences in shared memory
+cudaError_t launch_step_plan(StepPlanParams p, cudaStream_t stream);
+
 // ---- checked mode (checks.cu): precondition pre-passes -----------------------
 // Each reports violations through the error word and never traps; see the
 // PA_OPT_DEBUG_CHECKS paragraph of include/pa.h.

@@ -356,6 +356,114 @@ int pa_reshape_and_cache(const void* key, const void* value, void* k_cache, void
                                                   err, static_cast<cudaStream_t>(stream)));
 }
 
+int pa_rotary_and_cache(void* query_out, int64_t query_out_stride, void* key_out, int64_t key_out_stride,
+                        const void* query, int64_t query_stride, const void* key, int64_t key_stride,
+                        const void* value, int64_t value_stride, const int32_t* positions, const float* cos_sin,
+                        int32_t num_positions, int32_t rotary_dim, int32_t interleaved, void* k_cache, void* v_cache,
+                        const int64_t* slot_mapping, int64_t num_tokens, int32_t num_heads,
+                        const pa_cache_desc* cache, void* stream) {
+    NvtxRange range("pa_rotary_and_cache");
+    pa::PoolShape shape;
+    int rc = check_cache(cache, &shape);
+    if (rc != PA_OK) return rc;
+    if (num_tokens < 0 || num_heads <= 0 || num_heads % shape.num_kv_heads != 0 || num_positions <= 0 ||
+        rotary_dim <= 0 || rotary_dim > shape.head_dim || rotary_dim % 2 != 0 || (interleaved != 0 && interleaved != 1))
+        return PA_ERR_INVALID_ARG;
+    const int64_t q_row = (int64_t)num_heads * shape.head_dim, kv_row = (int64_t)shape.num_kv_heads * shape.head_dim;
+    const int per_chunk = 16 / shape.elem_bytes;
+    if (query_stride < q_row || query_out_stride < q_row || key_stride < kv_row || value_stride < kv_row ||
+        (key_out && key_out_stride < kv_row) || query_stride % per_chunk || query_out_stride % per_chunk ||
+        key_stride % per_chunk || value_stride % per_chunk || (key_out && key_out_stride % per_chunk))
+        return PA_ERR_INVALID_ARG;
+    if (num_tokens == 0) return PA_OK;
+    if (!aligned(query_out, 16) || (key_out && !aligned(key_out, 16)) || !aligned(query, 16) || !aligned(key, 16) ||
+        !aligned(value, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(cos_sin, 16) ||
+        !aligned(positions, 4) || !aligned(slot_mapping, 8))
+        return PA_ERR_INVALID_ARG;
+    // A row that is written where another is still to be read: only whole arrays in place.
+    if ((query_out == query && query_out_stride != query_stride) ||
+        (key_out && key_out == key && key_out_stride != key_stride))
+        return PA_ERR_INVALID_ARG;
+    if (!pa::rotary_supported(shape.head_dim, rotary_dim, shape.elem_bytes)) return PA_ERR_UNSUPPORTED;
+
+    const int dev = current_device();
+    if (dev < 0) return PA_ERR_CUDA;
+    int* err = error_word(dev);
+    if (!err) return PA_ERR_CUDA;
+    if (option(PA_OPT_DEBUG_CHECKS)) {
+        rc = status_of(pa::launch_check_unique_slots(slot_mapping, num_tokens, err, static_cast<cudaStream_t>(stream)));
+        if (rc != PA_OK) return rc;
+    }
+    pa::RotaryParams p{};
+    p.query = query;
+    p.key = key;
+    p.value = value;
+    p.query_out = query_out;
+    p.key_out = key_out;
+    p.query_stride = query_stride;
+    p.key_stride = key_stride;
+    p.value_stride = value_stride;
+    p.query_out_stride = query_out_stride;
+    p.key_out_stride = key_out_stride;
+    p.positions = positions;
+    p.slot_mapping = slot_mapping;
+    p.cos_sin = cos_sin;
+    p.num_positions = num_positions;
+    p.rotary_dim = rotary_dim;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.num_heads = num_heads;
+    p.num_kv_heads = shape.num_kv_heads;
+    p.block_size = shape.block_size;
+    p.num_slots = shape.num_blocks * shape.block_size;
+    p.err = err;
+    return status_of(pa::launch_rotary(p, cache->dtype, shape.head_dim, shape.elem_bytes, interleaved != 0, num_tokens,
+                                       static_cast<cudaStream_t>(stream)));
+}
+
+int pa_plan_step(const int32_t* new_lens, const int32_t* context_lens, int32_t* context_lens_out, int32_t num_seqs,
+                 int32_t* free_ring, int32_t ring_size, const int32_t* free_state, int32_t* free_state_out,
+                 int64_t num_blocks, int32_t block_size, int32_t* block_tables, int32_t max_blocks_per_seq,
+                 int32_t* query_start_loc, int64_t* slot_mapping, int32_t* positions, int32_t max_tokens,
+                 void* stream) {
+    NvtxRange range("pa_plan_step");
+    if (num_seqs < 0 || ring_size <= 0 || num_blocks <= 0 || block_size <= 0 || max_blocks_per_seq <= 0 ||
+        max_tokens < 0)
+        return PA_ERR_INVALID_ARG;
+    if (!aligned(query_start_loc, 4) || !aligned(free_ring, 4) || !aligned(free_state, 4) || !aligned(free_state_out, 4))
+        return PA_ERR_INVALID_ARG;
+    if (num_seqs > 0 && (!aligned(new_lens, 4) || !aligned(context_lens, 4) || !aligned(context_lens_out, 4) ||
+                         !aligned(block_tables, 4)))
+        return PA_ERR_INVALID_ARG;
+    if (max_tokens > 0 && (!aligned(slot_mapping, 8) || !aligned(positions, 4))) return PA_ERR_INVALID_ARG;
+    if (num_seqs > pa::kMaxStepSeqs) return PA_ERR_UNSUPPORTED;
+    const int dev = current_device();
+    if (dev < 0) return PA_ERR_CUDA;
+    int* err = error_word(dev);
+    if (!err) return PA_ERR_CUDA;
+    pa::StepPlanParams p{};
+    p.new_lens = new_lens;
+    p.context_lens = context_lens;
+    p.context_lens_out = context_lens_out;
+    p.num_seqs = num_seqs;
+    p.free_ring = free_ring;
+    p.ring_size = ring_size;
+    p.free_state = free_state;
+    p.free_state_out = free_state_out;
+    p.num_blocks = num_blocks;
+    p.block_size = block_size;
+    p.block_tables = block_tables;
+    p.max_blocks = max_blocks_per_seq;
+    const int64_t cap = (int64_t)max_blocks_per_seq * block_size;
+    p.ctx_cap = (int)(cap < 0x7fffffffLL ? cap : 0x7fffffffLL);
+    p.query_start_loc = query_start_loc;
+    p.slot_mapping = slot_mapping;
+    p.positions = positions;
+    p.max_tokens = max_tokens;
+    p.err = err;
+    return status_of(pa::launch_step_plan(p, static_cast<cudaStream_t>(stream)));
+}
+
 size_t pa_decode_workspace_size(int32_t num_seqs, int32_t num_heads, int32_t max_context_len,
                                 int32_t partition_size, int32_t head_dim) {
     if (num_seqs < 0 || num_heads <= 0 || max_context_len < 0 || head_dim <= 0 || !partition_ok(partition_size))

@@ -19,6 +19,7 @@ STATUS_NAMES = {0: "PA_OK", -1: "PA_ERR_INVALID_ARG", -2: "PA_ERR_UNSUPPORTED", 
 PA_F32, PA_F16, PA_BF16 = 0, 1, 2
 DEVERR_BLOCK_ID, DEVERR_SLOT, DEVERR_CONTEXT_LEN, DEVERR_COPY_PAIR, DEVERR_TIMEOUT = 0x1, 0x2, 0x4, 0x8, 0x10
 DEVERR_DUP_SLOT, DEVERR_PAIR_CONFLICT = 0x20, 0x40  # checked mode only
+DEVERR_POSITION, DEVERR_STEP = 0x80, 0x100
 OPT_DEBUG_CHECKS, OPT_DECODE_KERNEL, OPT_DROP_FIRST_FILL = 0, 1, 2  # pa_option
 NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024  # PA_NOALLOC_SCRATCH_BYTES
 
@@ -71,6 +72,9 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                                        ctypes.POINTER(vp), i64, i32, vp, i64, desc, vp]
         lib.pa_prefill.argtypes = [vp, i32, vp, vp, i32, i32, vp, vp, desc, vp, i32, vp, i32, i32, i32,
                                    ctypes.c_float, vp]
+        lib.pa_rotary_and_cache.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, i32, i32, i32, vp, vp,
+                                            vp, i64, i32, desc, vp]
+        lib.pa_plan_step.argtypes = [vp, vp, vp, i32, vp, i32, vp, vp, i64, i32, vp, i32, vp, vp, vp, i32, vp]
         lib.pa_prompt_attention.argtypes = [vp, vp, i64, vp, i64, vp, i64, vp, i32, i32, i32, i32, i32, i32,
                                             ctypes.c_float, vp, sz, vp]
         lib.pa_prompt_attention_workspace_size.argtypes = [i32, i32, i32, i32]
@@ -82,7 +86,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.pa_set_option.argtypes = [ctypes.c_int, ctypes.c_int]
         lib.pa_get_option.argtypes = [ctypes.c_int]
         for name in ("pa_reshape_and_cache", "pa_decode", "pa_decode_noalloc", "pa_copy_blocks",
-                     "pa_swap_blocks", "pa_prefill", "pa_prompt_attention", "pa_get_device_error", "pa_abi_version", "pa_set_option",
+                     "pa_swap_blocks", "pa_prefill", "pa_prompt_attention", "pa_rotary_and_cache", "pa_plan_step", "pa_get_device_error", "pa_abi_version", "pa_set_option",
                      "pa_get_option"):
             getattr(lib, name).restype = ctypes.c_int
         _lib = lib
