@@ -211,7 +211,8 @@ int pa_rotary_and_cache(void *query_out, int64_t query_out_stride, void *key_out
  * ring entries, token rows -- sets PA_DEVERR_STEP and is refused whole: lengths,
  * tables and free blocks stay, query_start_loc is 0 and slots are -1.  A block id
  * outside [0, num_blocks) in the ring or a table sets PA_DEVERR_BLOCK_ID, and
- * tokens in it get slot -1.  num_seqs <= 16384, else PA_ERR_UNSUPPORTED.
+ * tokens in it get slot -1.  num_seqs <= 16384, max_tokens and ring_size below
+ * 2^30 - 1, else PA_ERR_UNSUPPORTED.
  */
 int pa_plan_step(const int32_t *new_lens, const int32_t *context_lens, int32_t *context_lens_out,
                  int32_t num_seqs, int32_t *free_ring, int32_t ring_size,

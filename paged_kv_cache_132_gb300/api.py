@@ -318,19 +318,22 @@ def plan_step(new_lens: torch.Tensor, context_lens: torch.Tensor, free_ring: tor
     in place).  A step that does not fit is refused whole (get_device_error)."""
     lib = native.load()
     s = new_lens.numel()
+    i32 = torch.int32
     _require(max_tokens >= 0, "max_tokens must not be negative")
-    for t, n in ((new_lens, s), (context_lens, s), (free_state, 2)):
-        _require(t.dtype == torch.int32 and t.dim() == 1 and t.numel() == n and t.is_contiguous(),
-                 "new_lens and context_lens are int32 [num_seqs], free_state int32 [2]")
-    _require(free_ring.dtype == torch.int32 and free_ring.dim() == 1 and free_ring.is_contiguous(),
-             "free_ring is int32 [ring_size]")
-    _require(block_tables.dtype == torch.int32 and block_tables.dim() == 2 and block_tables.shape[0] == s
-             and block_tables.is_contiguous(), "block_tables is int32 [num_seqs][max_blocks]")
+    _require(new_lens.dtype is i32 and context_lens.dtype is i32 and free_state.dtype is i32
+             and free_ring.dtype is i32 and block_tables.dtype is i32, "lengths, blocks and tables are int32")
+    _require(new_lens.shape == (s,) and context_lens.shape == (s,) and free_state.shape == (2,)
+             and free_ring.dim() == 1 and block_tables.dim() == 2 and block_tables.shape[0] == s,
+             "new_lens and context_lens are [num_seqs], free_state [2], free_ring [ring_size], block_tables "
+             "[num_seqs][max_blocks]")
+    _require(new_lens.is_contiguous() and context_lens.is_contiguous() and free_state.is_contiguous()
+             and free_ring.is_contiguous() and block_tables.is_contiguous(), "tensors must be contiguous")
     if out is None:
-        dev, i32 = new_lens.device, torch.int32
-        out = StepPlan(_empty((s,), i32, dev, stream), _empty((2,), i32, dev, stream),
-                       _empty((s + 1,), i32, dev, stream), _empty((max_tokens,), torch.int64, dev, stream),
-                       _empty((max_tokens,), i32, dev, stream))
+        dev, empty = new_lens.device, torch.empty
+        with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+            out = StepPlan(empty((s,), dtype=i32, device=dev), empty((2,), dtype=i32, device=dev),
+                           empty((s + 1,), dtype=i32, device=dev), empty((max_tokens,), dtype=torch.int64, device=dev),
+                           empty((max_tokens,), dtype=i32, device=dev))
     else:
         for t, n, dt in zip(out, (s, 2, s + 1, max_tokens, max_tokens),
                             (torch.int32, torch.int32, torch.int32, torch.int64, torch.int32)):

@@ -436,7 +436,8 @@ int pa_plan_step(const int32_t* new_lens, const int32_t* context_lens, int32_t* 
                          !aligned(block_tables, 4)))
         return PA_ERR_INVALID_ARG;
     if (max_tokens > 0 && (!aligned(slot_mapping, 8) || !aligned(positions, 4))) return PA_ERR_INVALID_ARG;
-    if (num_seqs > pa::kMaxStepSeqs) return PA_ERR_UNSUPPORTED;
+    if (num_seqs > pa::kMaxStepSeqs || max_tokens >= pa::kMaxStepCount || ring_size >= pa::kMaxStepCount)
+        return PA_ERR_UNSUPPORTED;
     const int dev = current_device();
     if (dev < 0) return PA_ERR_CUDA;
     int* err = error_word(dev);

@@ -14,10 +14,14 @@
 // one of thousands of single tokens cost alike.
 //
 // Bound: latency.  A step's data are a few bytes per sequence and 12 per token
-// (a megabyte at most), but its loads depend on one another.  One CTA does the
-// sums and the tables, with the sums in shared memory; slots and positions
-// follow in the same CTA up to kTokensInPlan tokens, and in a second kernel
-// over the whole GPU above that.
+// (a megabyte at most), but its loads depend on one another.  So the step is one
+// launch: one CTA, or for large steps one cluster of kStepCluster CTAs, each of
+// which makes the sums for itself in shared memory.  Nothing that a thread
+// writes is read by another one -- a block that is given back and taken again in
+// the same step is looked up in the table that gives it -- and the outputs that
+// may be inputs (lengths, free state) are written after a barrier of them all.
+#include <cooperative_groups.h>
+
 #include "common.cuh"
 #include "kernels.h"
 
@@ -25,239 +29,282 @@ namespace pa {
 namespace {
 
 constexpr int kStepThreads = 1024;
-constexpr int kSlotThreads = 256;
-constexpr int kSlotTokens = 4;  // consecutive tokens of a thread
+constexpr int kStepCluster = 8;  // the largest cluster every GPU of the family schedules
+// Steps of more token rows or sequences than these run on the cluster.
+constexpr int kStepSmallTokens = 2048;
+constexpr int kStepSmallSeqs = 1024;
+constexpr int kStepUnroll = 4;   // entries of a thread whose loads are in flight together
 
-// Last index i in [0, n) with start[i] <= x; start[0] <= x, non-decreasing.
-__device__ inline int find_sequence(const int* start, int n, int x) {
-    int lo = 0, hi = n;  // start[lo] <= x < start[hi]
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (start[mid] <= x)
-            lo = mid;
-        else
-            hi = mid;
-    }
-    return lo;
+// For each x: the last index i in [0, n) with start[i] <= x (start[0] = 0 <= x,
+// non-decreasing), n <= 2^steps.  The searches go step by step together, so
+// that their loads overlap.
+template <int N>
+__device__ inline void find_sequences(const int* start, int n, int steps, const int (&x)[N], int (&found)[N]) {
+#pragma unroll
+    for (int u = 0; u < N; ++u) found[u] = 0;
+    for (int bit = steps > 0 ? 1 << (steps - 1) : 0; bit; bit >>= 1)
+#pragma unroll
+        for (int u = 0; u < N; ++u) {
+            const int mid = found[u] + bit;
+            if (mid < n && start[mid] <= x[u]) found[u] = mid;
+        }
 }
 
 __device__ inline int blocks_of(int tokens, int block_size) {
     return (int)(((unsigned)tokens + (unsigned)block_size - 1u) / (unsigned)block_size);
 }
 
-// Position and slot of one token; -1 where its block id is out of range.
-__device__ inline void place_token(const StepPlanParams& p, int t, int seq, int position) {
-    const int32_t id = p.block_tables[(int64_t)seq * p.max_blocks + (unsigned)position / (unsigned)p.block_size];
-    const bool good = id >= 0 && id < p.num_blocks;
-    if (!good) set_error(p.err, PA_DEVERR_BLOCK_ID);
-    p.positions[t] = position;
-    p.slot_mapping[t] =
-        good ? (int64_t)id * p.block_size + (int)((unsigned)position % (unsigned)p.block_size) : -1;
-}
-
+// Counts saturate at kMaxStepCount: what reaches it fits no step.
 struct Sums {
-    long long tokens, given, taken;
+    int tokens, given, taken;
 };
 
 __device__ inline Sums add(const Sums& a, const Sums& b) {
-    return {a.tokens + b.tokens, a.given + b.given, a.taken + b.taken};
-}
-__device__ inline Sums shuffle_up(const Sums& a, int d) {
-    return {__shfl_up_sync(0xffffffffu, a.tokens, d), __shfl_up_sync(0xffffffffu, a.given, d),
-            __shfl_up_sync(0xffffffffu, a.taken, d)};
+    return {min(a.tokens + b.tokens, kMaxStepCount), min(a.given + b.given, kMaxStepCount),
+            min(a.taken + b.taken, kMaxStepCount)};
 }
 __device__ inline Sums inclusive_in_warp(Sums a, int lane) {
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const Sums up = shuffle_up(a, d);
+        const Sums up{__shfl_up_sync(0xffffffffu, a.tokens, d), __shfl_up_sync(0xffffffffu, a.given, d),
+                      __shfl_up_sync(0xffffffffu, a.taken, d)};
         if (lane >= d) a = add(a, up);
     }
     return a;
 }
 
-// One CTA.  Every input is read before the outputs that may alias it
-// (context_lens, free_state) are written.
+// One sequence's step; invalid lengths leave it as it is.
+struct Change {
+    int ctx, grow;
+    bool done, bad;
+};
+__device__ inline Change change_of(const StepPlanParams& p, int s) {
+    const int n = p.new_lens[s];
+    Change c{p.context_lens[s], n > 0 ? n : 0, n == -1, false};
+    c.bad = c.ctx < 0 || c.ctx > p.ctx_cap || n < -1 || c.grow > p.ctx_cap - c.ctx;
+    if (c.bad) {
+        c.grow = 0;
+        c.done = false;
+    }
+    return c;
+}
+__device__ inline Sums sums_of(const StepPlanParams& p, const Change& c) {
+    Sums a{min(c.grow, kMaxStepCount), 0, 0};
+    if (c.done) a.given = min(blocks_of(c.ctx, p.block_size), kMaxStepCount);
+    if (c.grow) a.taken = min(blocks_of(c.ctx + c.grow, p.block_size) - blocks_of(c.ctx, p.block_size), kMaxStepCount);
+    return a;
+}
+
+template <bool CLUSTER>
 __global__ void __launch_bounds__(kStepThreads) step_plan_kernel(const StepPlanParams p) {
-    extern __shared__ int starts[];  // [num_seqs + 1] first token, [num_seqs + 1] first block given or taken
+    extern __shared__ int starts[];  // three prefix sums of num_seqs entries
     __shared__ Sums warp_sums[32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rank = CLUSTER ? (int)blockIdx.x : 0;
+    const int first = rank * kStepThreads + tid;             // this thread's entries of each kind
+    const int stride = (CLUSTER ? kStepCluster : 1) * kStepThreads;
     int* token_start = starts;
-    int* block_start = starts + p.num_seqs + 1;
+    int* given_start = starts + p.num_seqs;
+    int* taken_start = starts + 2 * p.num_seqs;
     pdl_launch_dependents();
     pdl_wait_prerequisites();
 
     // A thread's consecutive sequences.
     const int each = (p.num_seqs + kStepThreads - 1) / kStepThreads;
     const int s0 = min(tid * each, p.num_seqs), s1 = min(s0 + each, p.num_seqs);
-    auto counts = [&](int s, int& ctx, int& grow, bool& done) {
-        ctx = p.context_lens[s];
-        const int n = p.new_lens[s];
-        done = n == -1;
-        grow = n > 0 ? n : 0;
-        if (ctx < 0 || ctx > p.ctx_cap || n < -1 || grow > p.ctx_cap - ctx) {
-            set_error(p.err, PA_DEVERR_CONTEXT_LEN);
-            grow = 0;  // the sequence stays as it is
-            done = false;
-            return false;
-        }
-        return true;
-    };
-    auto count = [&](int s) {
-        int ctx, grow;
-        bool done;
-        Sums a{0, 0, 0};
-        if (!counts(s, ctx, grow, done)) return a;
-        const int held = blocks_of(ctx, p.block_size);
-        a.tokens = grow;
-        a.given = done ? held : 0;
-        a.taken = grow ? blocks_of(ctx + grow, p.block_size) - held : 0;
-        return a;
-    };
+    const int head = p.free_state[0], free_count = p.free_state[1];
     Sums mine{0, 0, 0};
-    for (int s = s0; s < s1; ++s) mine = add(mine, count(s));
+    bool bad = false;
+#pragma unroll 4
+    for (int s = s0; s < s1; ++s) {
+        const Change c = change_of(p, s);
+        bad |= c.bad;
+        mine = add(mine, sums_of(p, c));
+    }
+    if (bad && rank == 0) set_error(p.err, PA_DEVERR_CONTEXT_LEN);
     const Sums incl = inclusive_in_warp(mine, lane);
     if (lane == 31) warp_sums[warp] = incl;
-    const int head = p.free_state[0], free_count = p.free_state[1];
     __syncthreads();
     if (warp == 0) warp_sums[lane] = inclusive_in_warp(warp_sums[lane], lane);
     __syncthreads();
     const Sums total = warp_sums[31];
-    Sums at = warp ? add(warp_sums[warp - 1], incl) : incl;  // the sums before this thread's sequences
-    at.tokens -= mine.tokens;
-    at.given -= mine.given;
-    at.taken -= mine.taken;
-
     const bool fits = head >= 0 && head < p.ring_size && free_count >= 0 &&
-                      free_count + total.given <= p.ring_size && total.taken <= free_count + total.given &&
-                      total.tokens <= p.max_tokens;
-    if (!fits && tid == 0) set_error(p.err, PA_DEVERR_STEP);
-    const int tokens = fits ? (int)total.tokens : 0;
+                      (long long)free_count + total.given <= p.ring_size &&
+                      total.taken <= (long long)free_count + total.given && total.tokens <= p.max_tokens &&
+                      total.tokens < kMaxStepCount && total.given < kMaxStepCount && total.taken < kMaxStepCount;
+    if (!fits && first == 0) set_error(p.err, PA_DEVERR_STEP);
+    const int tokens = fits ? total.tokens : 0, given = fits ? total.given : 0, taken = fits ? total.taken : 0;
 
-    {
-        Sums run = at;
-        for (int s = s0; s < s1; ++s) {
-            const int first = fits ? (int)run.tokens : 0;
-            token_start[s] = first;
-            block_start[s] = fits ? (int)run.given : 0;
-            p.query_start_loc[s] = first;
-            run = add(run, count(s));
-        }
-        if (tid == 0) {
-            token_start[p.num_seqs] = tokens;
-            p.query_start_loc[p.num_seqs] = tokens;
-        }
-    }
-    // Position of entry k of the ring.
-    auto ring_at = [&](long long k) {
-        const long long i = head + k;  // < 2 * ring_size
-        return (int)(i >= p.ring_size ? i - p.ring_size : i);
-    };
-    if (fits && total.given > 0) {
-        __syncthreads();
-        for (int k = tid; k < (int)total.given; k += kStepThreads) {
-            const int s = find_sequence(block_start, p.num_seqs, k);
-            const int32_t id = p.block_tables[(int64_t)s * p.max_blocks + (k - block_start[s])];
-            if (id < 0 || id >= p.num_blocks) set_error(p.err, PA_DEVERR_BLOCK_ID);
-            p.free_ring[ring_at((long long)free_count + k)] = id;
-        }
-    }
-    if (fits && total.taken > 0) {
-        __syncthreads();
-        Sums run = at;
-        for (int s = s0; s < s1; ++s) {
-            block_start[s] = (int)run.taken;
-            run = add(run, count(s));
-        }
-        __syncthreads();
-        for (int k = tid; k < (int)total.taken; k += kStepThreads) {
-            const int s = find_sequence(block_start, p.num_seqs, k);
-            const int32_t id = p.free_ring[ring_at(k)];
-            if (id < 0 || id >= p.num_blocks) set_error(p.err, PA_DEVERR_BLOCK_ID);
-            const int held = blocks_of(p.context_lens[s], p.block_size);
-            p.block_tables[(int64_t)s * p.max_blocks + held + (k - block_start[s])] = id;
-        }
-    }
-    __syncthreads();
-    if (p.place_tokens)
-        for (int t = tid; t < p.max_tokens; t += kStepThreads) {
-            if (t < tokens) {
-                const int s = find_sequence(token_start, p.num_seqs, t);
-                place_token(p, t, s, p.context_lens[s] + (t - token_start[s]));
-            } else {
-                p.positions[t] = -1;
-                p.slot_mapping[t] = -1;
-            }
-        }
-    __syncthreads();  // the inputs were read: the outputs may be the same memory
+    // The sums before each sequence.
+    Sums run = {incl.tokens - mine.tokens, incl.given - mine.given, incl.taken - mine.taken};
+    if (warp) run = add(run, warp_sums[warp - 1]);
     for (int s = s0; s < s1; ++s) {
-        int ctx, grow;
-        bool done;
-        counts(s, ctx, grow, done);
-        p.context_lens_out[s] = !fits ? ctx : done ? 0 : ctx + grow;
+        token_start[s] = run.tokens;
+        given_start[s] = run.given;
+        taken_start[s] = run.taken;
+        if (rank == 0) p.query_start_loc[s] = fits ? run.tokens : 0;
+        if (s + 1 < s1) run = add(run, sums_of(p, change_of(p, s)));
     }
-    if (tid == 0) {
-        p.free_state_out[0] = fits ? ring_at(total.taken) : head;
-        p.free_state_out[1] = fits ? (int)(free_count + total.given - total.taken) : free_count;
-    }
-}
+    if (first == 0) p.query_start_loc[p.num_seqs] = tokens;
+    __syncthreads();
 
-// Slots and positions of many tokens, from the plan's start rows and lengths.
-__global__ void __launch_bounds__(kSlotThreads) step_slots_kernel(const StepPlanParams p) {
-    pdl_launch_dependents();
-    pdl_wait_prerequisites();
-    const int tokens = p.query_start_loc[p.num_seqs];
-    const int64_t first = ((int64_t)blockIdx.x * kSlotThreads + threadIdx.x) * kSlotTokens;
-    int s = -1, end = 0, ctx = 0;
-    for (int i = 0; i < kSlotTokens; ++i) {
-        if (first + i >= p.max_tokens) return;
-        const int t = (int)(first + i);
-        if (t >= tokens) {
-            p.positions[t] = -1;
-            p.slot_mapping[t] = -1;
-            continue;
+    const int steps = p.num_seqs > 1 ? 32 - __clz(p.num_seqs - 1) : 0;
+    auto ring_at = [&](int k) {  // entry k from the head on; head + k < 2 * ring_size
+        const unsigned i = (unsigned)head + (unsigned)k;
+        return (int)(i >= (unsigned)p.ring_size ? i - (unsigned)p.ring_size : i);
+    };
+    auto table_at = [&](int s, int block) { return (int64_t)s * p.max_blocks + block; };
+    // Where block k of those given back stands, and where block k of those taken
+    // comes from: the ring, or the table of the sequence that gives it back.
+    auto given_at = [&](const int (&k)[kStepUnroll], const int32_t* (&from)[kStepUnroll]) {
+        int seq[kStepUnroll];
+        find_sequences(given_start, p.num_seqs, steps, k, seq);
+#pragma unroll
+        for (int u = 0; u < kStepUnroll; ++u)
+            from[u] = p.block_tables + table_at(seq[u], k[u] - given_start[seq[u]]);
+    };
+    auto taken_from = [&](const int (&k)[kStepUnroll], const int32_t* (&from)[kStepUnroll]) {
+        bool beyond = false;
+#pragma unroll
+        for (int u = 0; u < kStepUnroll; ++u) beyond |= k[u] >= free_count;
+        if (beyond) {
+            int back[kStepUnroll];
+#pragma unroll
+            for (int u = 0; u < kStepUnroll; ++u) back[u] = max(k[u] - free_count, 0);
+            given_at(back, from);
         }
-        if (s < 0 || t >= end) {
-            s = find_sequence(p.query_start_loc, p.num_seqs, t);
-            end = p.query_start_loc[s + 1];
-            ctx = p.context_lens_out[s];
+#pragma unroll
+        for (int u = 0; u < kStepUnroll; ++u)
+            if (k[u] < free_count) from[u] = p.free_ring + ring_at(k[u]);
+    };
+    bool wrong = false;  // a block id out of range
+    auto good_id = [&](int32_t id) {
+        const bool good = id >= 0 && id < p.num_blocks;
+        wrong |= !good;
+        return good;
+    };
+
+    // Blocks of finished sequences, behind the ring's last free entry.
+    for (int k0 = first; k0 < given; k0 += kStepUnroll * stride) {
+        int k[kStepUnroll];
+        const int32_t* from[kStepUnroll];
+        int32_t id[kStepUnroll];
+#pragma unroll
+        for (int u = 0; u < kStepUnroll; ++u) k[u] = min(k0 + u * stride, given - 1);
+        given_at(k, from);
+#pragma unroll
+        for (int u = 0; u < kStepUnroll; ++u) id[u] = *from[u];
+#pragma unroll
+        for (int u = 0; u < kStepUnroll; ++u) {  // the last entry again where there is none
+            good_id(id[u]);
+            p.free_ring[ring_at(free_count + k[u])] = id[u];
         }
-        place_token(p, t, s, ctx - (end - t));
+    }
+    // Blocks of growing sequences, from its head.
+    for (int k0 = first; k0 < taken; k0 += kStepUnroll * stride) {
+        int k[kStepUnroll], seq[kStepUnroll], held[kStepUnroll];
+        const int32_t* from[kStepUnroll];
+        int32_t id[kStepUnroll];
+#pragma unroll
+        for (int u = 0; u < kStepUnroll; ++u) k[u] = min(k0 + u * stride, taken - 1);
+        find_sequences(taken_start, p.num_seqs, steps, k, seq);
+        taken_from(k, from);
+#pragma unroll
+        for (int u = 0; u < kStepUnroll; ++u) {
+            id[u] = *from[u];
+            held[u] = blocks_of(p.context_lens[seq[u]], p.block_size);
+        }
+#pragma unroll
+        for (int u = 0; u < kStepUnroll; ++u) {
+            good_id(id[u]);
+            p.block_tables[table_at(seq[u], held[u] + k[u] - taken_start[seq[u]])] = id[u];
+        }
+    }
+    // Positions and slots.
+    for (int t0 = first; t0 < p.max_tokens; t0 += kStepUnroll * stride) {
+        int32_t id[kStepUnroll];
+        int position[kStepUnroll];
+        if (t0 < tokens) {
+            int t[kStepUnroll], seq[kStepUnroll], ctx[kStepUnroll], k[kStepUnroll];
+            const int32_t* from[kStepUnroll];
+#pragma unroll
+            for (int u = 0; u < kStepUnroll; ++u) t[u] = min(t0 + u * stride, tokens - 1);
+            find_sequences(token_start, p.num_seqs, steps, t, seq);
+#pragma unroll
+            for (int u = 0; u < kStepUnroll; ++u) ctx[u] = p.context_lens[seq[u]];
+#pragma unroll
+            for (int u = 0; u < kStepUnroll; ++u) {
+                position[u] = ctx[u] + (t[u] - token_start[seq[u]]);
+                const int block = (int)((unsigned)position[u] / (unsigned)p.block_size);
+                const int held = blocks_of(ctx[u], p.block_size);
+                k[u] = block < held ? -1 : taken_start[seq[u]] + block - held;
+            }
+            taken_from(k, from);
+#pragma unroll
+            for (int u = 0; u < kStepUnroll; ++u)  // the last block held, not yet full
+                if (k[u] < 0)
+                    from[u] = p.block_tables +
+                              table_at(seq[u], (int)((unsigned)position[u] / (unsigned)p.block_size));
+#pragma unroll
+            for (int u = 0; u < kStepUnroll; ++u) id[u] = *from[u];
+        }
+#pragma unroll
+        for (int u = 0; u < kStepUnroll; ++u) {
+            const int t = t0 + u * stride;
+            if (t >= p.max_tokens) continue;
+            int64_t slot = -1;
+            int place = -1;
+            if (t < tokens) {
+                place = position[u];
+                if (good_id(id[u]))
+                    slot = (int64_t)id[u] * p.block_size + (int)((unsigned)place % (unsigned)p.block_size);
+            }
+            p.positions[t] = place;
+            p.slot_mapping[t] = slot;
+        }
+    }
+    if (wrong) set_error(p.err, PA_DEVERR_BLOCK_ID);
+
+    // Every input was read: the outputs may be the same memory.
+    if (CLUSTER)
+        cooperative_groups::this_cluster().sync();
+    else
+        __syncthreads();
+    for (int s = first; s < p.num_seqs; s += stride) {
+        const Change c = change_of(p, s);
+        p.context_lens_out[s] = !fits ? c.ctx : c.done ? 0 : c.ctx + c.grow;
+    }
+    if (first == 0) {
+        p.free_state_out[0] = fits ? ring_at(taken) : head;
+        p.free_state_out[1] = fits ? free_count + given - taken : free_count;
     }
 }
-
-cudaError_t launch_dependent(void (*kernel)(const StepPlanParams), unsigned grid, unsigned threads, size_t smem,
-                             const StepPlanParams& p, cudaStream_t stream) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, p);
-}
-
-// Up to here the planning CTA places the tokens itself; above it a second
-// kernel does.
-constexpr int kTokensInPlan = 4096;
 
 }  // namespace
 
-cudaError_t launch_step_plan(StepPlanParams p, cudaStream_t stream) {
-    const size_t smem = 2 * ((size_t)p.num_seqs + 1) * sizeof(int);
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(step_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   2 * (kMaxStepSeqs + 1) * (int)sizeof(int));
+cudaError_t launch_step_plan(const StepPlanParams& p, cudaStream_t stream) {
+    const bool large = p.max_tokens > kStepSmallTokens || p.num_seqs > kStepSmallSeqs;
+    const auto kernel = large ? step_plan_kernel<true> : step_plan_kernel<false>;
+    const size_t smem = 3 * (size_t)p.num_seqs * sizeof(int);
+    if (smem > 40 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   3 * kMaxStepSeqs * (int)sizeof(int));
         if (e != cudaSuccess) return e;
     }
-    p.place_tokens = p.max_tokens <= kTokensInPlan;
-    cudaError_t e = launch_dependent(step_plan_kernel, 1, kStepThreads, smem, p, stream);
-    if (e != cudaSuccess || p.place_tokens) return e;
-    const unsigned ctas = (unsigned)(((int64_t)p.max_tokens + kSlotThreads * kSlotTokens - 1) / (kSlotThreads * kSlotTokens));
-    return launch_dependent(step_slots_kernel, ctas, kSlotThreads, 0, p, stream);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(large ? kStepCluster : 1);
+    cfg.blockDim = dim3(kStepThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = kStepCluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = large ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 }  // namespace pa

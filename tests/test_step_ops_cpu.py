@@ -99,6 +99,8 @@ def _plan(lib, **over):
     (dict(slots=FAKE + 4), -1),
     (dict(pos=0), -1),
     (dict(seqs=16385), -2),
+    (dict(tokens=(1 << 30) - 1), -2),
+    (dict(ring_size=(1 << 30) - 1), -2),
 ])
 def test_plan_rejects_on_host(lib, over, status):
     assert _plan(lib, **over) == status
