@@ -82,11 +82,12 @@ struct StepPlanParams {
     int32_t* positions;           // [max_tokens]
     int max_tokens;
     int* err;
+    int block_shift;              // set by launch_step_plan: log2(block_size), or -1
 };
 
 constexpr int kMaxStepSeqs = 16384;          // three prefix sums of so many sequences in shared memory
 constexpr int kMaxStepCount = (1 << 30) - 1; // tokens or blocks of a step stay below it
-cudaError_t launch_step_plan(const StepPlanParams& p, cudaStream_t stream);
+cudaError_t launch_step_plan(StepPlanParams p, cudaStream_t stream);
 
 // ---- checked mode (checks.cu): precondition pre-passes -----------------------
 // Each reports violations through the error word and never traps; see the

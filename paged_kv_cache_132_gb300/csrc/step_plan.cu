@@ -14,12 +14,13 @@
 // one of thousands of single tokens cost alike.
 //
 // Bound: latency.  A step's data are a few bytes per sequence and 12 per token
-// (a megabyte at most), but its loads depend on one another.  So the step is one
-// launch: one CTA, or for large steps one cluster of kStepCluster CTAs, each of
-// which makes the sums for itself in shared memory.  Nothing that a thread
-// writes is read by another one -- a block that is given back and taken again in
-// the same step is looked up in the table that gives it -- and the outputs that
-// may be inputs (lengths, free state) are written after a barrier of them all.
+// (a megabyte at most), but its loads depend on one another.  So a step is one
+// CTA, or for large steps one cluster of kStepCluster CTAs, each of which makes
+// the sums for itself in shared memory, and then a second kernel that places the
+// tokens on the whole GPU.  Nothing that a thread writes is read by another one
+// of the same kernel -- a block that is given back and taken again in the same
+// step is looked up in the table that gives it -- and the outputs that may be
+// inputs (lengths, free state) are written after a barrier of them all.
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -29,6 +30,7 @@ namespace pa {
 namespace {
 
 constexpr int kStepThreads = 1024;
+constexpr int kSlotThreads = 256;
 constexpr int kStepCluster = 8;  // the largest cluster every GPU of the family schedules
 // Steps of more token rows or sequences than these run on the cluster.
 constexpr int kStepSmallTokens = 2048;
@@ -50,8 +52,17 @@ __device__ inline void find_sequences(const int* start, int n, int steps, const 
         }
 }
 
-__device__ inline int blocks_of(int tokens, int block_size) {
-    return (int)(((unsigned)tokens + (unsigned)block_size - 1u) / (unsigned)block_size);
+// Block of a position and blocks of a number of tokens; block sizes are powers
+// of two as a rule (block_shift >= 0), and a division costs some 20 instructions.
+__device__ inline int block_of(const StepPlanParams& p, unsigned position) {
+    return (int)(p.block_shift >= 0 ? position >> p.block_shift : position / (unsigned)p.block_size);
+}
+__device__ inline int blocks_of(const StepPlanParams& p, int tokens) {
+    return block_of(p, (unsigned)tokens + (unsigned)p.block_size - 1u);
+}
+
+__device__ inline int64_t slot_of(const StepPlanParams& p, int32_t id, int position) {
+    return (int64_t)id * p.block_size + (position - block_of(p, (unsigned)position) * p.block_size);
 }
 
 // Counts saturate at kMaxStepCount: what reaches it fits no step.
@@ -90,63 +101,76 @@ __device__ inline Change change_of(const StepPlanParams& p, int s) {
 }
 __device__ inline Sums sums_of(const StepPlanParams& p, const Change& c) {
     Sums a{min(c.grow, kMaxStepCount), 0, 0};
-    if (c.done) a.given = min(blocks_of(c.ctx, p.block_size), kMaxStepCount);
-    if (c.grow) a.taken = min(blocks_of(c.ctx + c.grow, p.block_size) - blocks_of(c.ctx, p.block_size), kMaxStepCount);
+    if (c.done) a.given = min(blocks_of(p, c.ctx), kMaxStepCount);
+    if (c.grow) a.taken = min(blocks_of(p, c.ctx + c.grow) - blocks_of(p, c.ctx), kMaxStepCount);
     return a;
 }
 
-template <bool CLUSTER>
+// LARGE: a cluster, and the tokens are left to step_slots_kernel.
+template <bool LARGE>
 __global__ void __launch_bounds__(kStepThreads) step_plan_kernel(const StepPlanParams p) {
     extern __shared__ int starts[];  // three prefix sums of num_seqs entries
     __shared__ Sums warp_sums[32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int rank = CLUSTER ? (int)blockIdx.x : 0;
+    const int rank = LARGE ? (int)blockIdx.x : 0;
     const int first = rank * kStepThreads + tid;             // this thread's entries of each kind
-    const int stride = (CLUSTER ? kStepCluster : 1) * kStepThreads;
+    const int stride = (LARGE ? kStepCluster : 1) * kStepThreads;
     int* token_start = starts;
     int* given_start = starts + p.num_seqs;
     int* taken_start = starts + 2 * p.num_seqs;
     pdl_launch_dependents();
     pdl_wait_prerequisites();
 
-    // A thread's consecutive sequences.
-    const int each = (p.num_seqs + kStepThreads - 1) / kStepThreads;
-    const int s0 = min(tid * each, p.num_seqs), s1 = min(s0 + each, p.num_seqs);
+    // The sums, EACH sequences of a thread at a time; the next ones load meanwhile.
+    constexpr int EACH = LARGE ? 4 : 1;
     const int head = p.free_state[0], free_count = p.free_state[1];
-    Sums mine{0, 0, 0};
+    Sums total{0, 0, 0};
     bool bad = false;
-#pragma unroll 4
-    for (int s = s0; s < s1; ++s) {
-        const Change c = change_of(p, s);
-        bad |= c.bad;
-        mine = add(mine, sums_of(p, c));
+    Change next[EACH];
+    auto load = [&](int s) {
+#pragma unroll
+        for (int e = 0; e < EACH; ++e)
+            next[e] = s + e < p.num_seqs ? change_of(p, s + e) : Change{0, 0, false, false};
+    };
+    load(tid * EACH);
+    for (int base = 0; base < p.num_seqs; base += kStepThreads * EACH) {
+        const int s = base + tid * EACH;
+        Sums each[EACH], mine{0, 0, 0};
+#pragma unroll
+        for (int e = 0; e < EACH; ++e) {
+            bad |= next[e].bad;
+            each[e] = sums_of(p, next[e]);
+            mine = add(mine, each[e]);
+        }
+        load(s + kStepThreads * EACH);
+        const Sums incl = inclusive_in_warp(mine, lane);
+        if (lane == 31) warp_sums[warp] = incl;
+        __syncthreads();
+        if (warp == 0) warp_sums[lane] = inclusive_in_warp(warp_sums[lane], lane);
+        __syncthreads();
+        Sums before = {incl.tokens - mine.tokens, incl.given - mine.given, incl.taken - mine.taken};
+        if (warp) before = add(before, warp_sums[warp - 1]);
+        before = add(before, total);
+#pragma unroll
+        for (int e = 0; e < EACH; ++e)
+            if (s + e < p.num_seqs) {
+                token_start[s + e] = before.tokens;
+                given_start[s + e] = before.given;
+                taken_start[s + e] = before.taken;
+                before = add(before, each[e]);
+            }
+        total = add(total, warp_sums[31]);
+        __syncthreads();
     }
     if (bad && rank == 0) set_error(p.err, PA_DEVERR_CONTEXT_LEN);
-    const Sums incl = inclusive_in_warp(mine, lane);
-    if (lane == 31) warp_sums[warp] = incl;
-    __syncthreads();
-    if (warp == 0) warp_sums[lane] = inclusive_in_warp(warp_sums[lane], lane);
-    __syncthreads();
-    const Sums total = warp_sums[31];
     const bool fits = head >= 0 && head < p.ring_size && free_count >= 0 &&
                       (long long)free_count + total.given <= p.ring_size &&
                       total.taken <= (long long)free_count + total.given && total.tokens <= p.max_tokens &&
                       total.tokens < kMaxStepCount && total.given < kMaxStepCount && total.taken < kMaxStepCount;
     if (!fits && first == 0) set_error(p.err, PA_DEVERR_STEP);
     const int tokens = fits ? total.tokens : 0, given = fits ? total.given : 0, taken = fits ? total.taken : 0;
-
-    // The sums before each sequence.
-    Sums run = {incl.tokens - mine.tokens, incl.given - mine.given, incl.taken - mine.taken};
-    if (warp) run = add(run, warp_sums[warp - 1]);
-    for (int s = s0; s < s1; ++s) {
-        token_start[s] = run.tokens;
-        given_start[s] = run.given;
-        taken_start[s] = run.taken;
-        if (rank == 0) p.query_start_loc[s] = fits ? run.tokens : 0;
-        if (s + 1 < s1) run = add(run, sums_of(p, change_of(p, s)));
-    }
+    for (int s = first; s < p.num_seqs; s += stride) p.query_start_loc[s] = fits ? token_start[s] : 0;
     if (first == 0) p.query_start_loc[p.num_seqs] = tokens;
-    __syncthreads();
 
     const int steps = p.num_seqs > 1 ? 32 - __clz(p.num_seqs - 1) : 0;
     auto ring_at = [&](int k) {  // entry k from the head on; head + k < 2 * ring_size
@@ -212,7 +236,7 @@ __global__ void __launch_bounds__(kStepThreads) step_plan_kernel(const StepPlanP
 #pragma unroll
         for (int u = 0; u < kStepUnroll; ++u) {
             id[u] = *from[u];
-            held[u] = blocks_of(p.context_lens[seq[u]], p.block_size);
+            held[u] = blocks_of(p, p.context_lens[seq[u]]);
         }
 #pragma unroll
         for (int u = 0; u < kStepUnroll; ++u) {
@@ -221,7 +245,7 @@ __global__ void __launch_bounds__(kStepThreads) step_plan_kernel(const StepPlanP
         }
     }
     // Positions and slots.
-    for (int t0 = first; t0 < p.max_tokens; t0 += kStepUnroll * stride) {
+    for (int t0 = first; !LARGE && t0 < p.max_tokens; t0 += kStepUnroll * stride) {
         int32_t id[kStepUnroll];
         int position[kStepUnroll];
         if (t0 < tokens) {
@@ -235,16 +259,15 @@ __global__ void __launch_bounds__(kStepThreads) step_plan_kernel(const StepPlanP
 #pragma unroll
             for (int u = 0; u < kStepUnroll; ++u) {
                 position[u] = ctx[u] + (t[u] - token_start[seq[u]]);
-                const int block = (int)((unsigned)position[u] / (unsigned)p.block_size);
-                const int held = blocks_of(ctx[u], p.block_size);
+                const int block = block_of(p, (unsigned)position[u]);
+                const int held = blocks_of(p, ctx[u]);
                 k[u] = block < held ? -1 : taken_start[seq[u]] + block - held;
             }
             taken_from(k, from);
 #pragma unroll
             for (int u = 0; u < kStepUnroll; ++u)  // the last block held, not yet full
                 if (k[u] < 0)
-                    from[u] = p.block_tables +
-                              table_at(seq[u], (int)((unsigned)position[u] / (unsigned)p.block_size));
+                    from[u] = p.block_tables + table_at(seq[u], block_of(p, (unsigned)position[u]));
 #pragma unroll
             for (int u = 0; u < kStepUnroll; ++u) id[u] = *from[u];
         }
@@ -257,7 +280,7 @@ __global__ void __launch_bounds__(kStepThreads) step_plan_kernel(const StepPlanP
             if (t < tokens) {
                 place = position[u];
                 if (good_id(id[u]))
-                    slot = (int64_t)id[u] * p.block_size + (int)((unsigned)place % (unsigned)p.block_size);
+                    slot = slot_of(p, id[u], place);
             }
             p.positions[t] = place;
             p.slot_mapping[t] = slot;
@@ -266,7 +289,7 @@ __global__ void __launch_bounds__(kStepThreads) step_plan_kernel(const StepPlanP
     if (wrong) set_error(p.err, PA_DEVERR_BLOCK_ID);
 
     // Every input was read: the outputs may be the same memory.
-    if (CLUSTER)
+    if (LARGE)
         cooperative_groups::this_cluster().sync();
     else
         __syncthreads();
@@ -280,31 +303,99 @@ __global__ void __launch_bounds__(kStepThreads) step_plan_kernel(const StepPlanP
     }
 }
 
-}  // namespace
-
-cudaError_t launch_step_plan(const StepPlanParams& p, cudaStream_t stream) {
-    const bool large = p.max_tokens > kStepSmallTokens || p.num_seqs > kStepSmallSeqs;
-    const auto kernel = large ? step_plan_kernel<true> : step_plan_kernel<false>;
-    const size_t smem = 3 * (size_t)p.num_seqs * sizeof(int);
-    if (smem > 40 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   3 * kMaxStepSeqs * (int)sizeof(int));
-        if (e != cudaSuccess) return e;
+// Positions and slots of a large step, from the plan's start rows, lengths and
+// tables.  The start rows are searched in shared memory.
+__global__ void __launch_bounds__(kSlotThreads) step_slots_kernel(const StepPlanParams p) {
+    extern __shared__ int starts[];
+    pdl_launch_dependents();
+    pdl_wait_prerequisites();
+    const int64_t base = (int64_t)blockIdx.x * (kSlotThreads * kStepUnroll) + threadIdx.x;
+    const int tokens = p.query_start_loc[p.num_seqs];
+    const int steps = p.num_seqs > 1 ? 32 - __clz(p.num_seqs - 1) : 0;
+    if ((int64_t)blockIdx.x * (kSlotThreads * kStepUnroll) < tokens) {
+        for (int s = threadIdx.x; s < p.num_seqs; s += kSlotThreads) starts[s] = p.query_start_loc[s];
+        __syncthreads();
     }
+    int t[kStepUnroll], seq[kStepUnroll], position[kStepUnroll];
+    int32_t id[kStepUnroll];
+    if (base < tokens) {
+#pragma unroll
+        for (int u = 0; u < kStepUnroll; ++u) t[u] = (int)min(base + u * kSlotThreads, (int64_t)tokens - 1);
+        find_sequences(starts, p.num_seqs, steps, t, seq);
+#pragma unroll
+        for (int u = 0; u < kStepUnroll; ++u) {
+            const int end = seq[u] + 1 < p.num_seqs ? starts[seq[u] + 1] : tokens;
+            position[u] = p.context_lens_out[seq[u]] - (end - t[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < kStepUnroll; ++u)
+            id[u] = p.block_tables[(int64_t)seq[u] * p.max_blocks + block_of(p, (unsigned)position[u])];
+    }
+    bool wrong = false;
+#pragma unroll
+    for (int u = 0; u < kStepUnroll; ++u) {
+        const int64_t at = base + u * kSlotThreads;
+        if (at >= p.max_tokens) continue;
+        int64_t slot = -1;
+        int place = -1;
+        if (at < tokens) {
+            place = position[u];
+            const bool good = id[u] >= 0 && id[u] < p.num_blocks;
+            wrong |= !good;
+            if (good) slot = slot_of(p, id[u], place);
+        }
+        p.positions[at] = place;
+        p.slot_mapping[at] = slot;
+    }
+    if (wrong) set_error(p.err, PA_DEVERR_BLOCK_ID);
+}
+
+cudaError_t launch(void (*kernel)(const StepPlanParams), unsigned ctas, unsigned cluster, int threads, size_t smem,
+                   const StepPlanParams& p, cudaStream_t stream) {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(large ? kStepCluster : 1);
-    cfg.blockDim = dim3(kStepThreads);
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = kStepCluster;
+    attr[1].val.clusterDim.x = cluster;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = large ? 2 : 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+}  // namespace
+
+cudaError_t launch_step_plan(StepPlanParams p, cudaStream_t stream) {
+    p.block_shift = -1;
+    if ((p.block_size & (p.block_size - 1)) == 0)
+        for (p.block_shift = 0; (1 << p.block_shift) < p.block_size;) ++p.block_shift;
+    const bool large = p.max_tokens > kStepSmallTokens || p.num_seqs > kStepSmallSeqs;
+    const size_t smem = 3 * (size_t)p.num_seqs * sizeof(int);
+    if (!large) return launch(step_plan_kernel<false>, 1, 1, kStepThreads, smem, p, stream);
+    constexpr int kMaxDevices = 64;
+    static int configured[kMaxDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    if (!__atomic_load_n(&configured[dev], __ATOMIC_ACQUIRE)) {
+        e = cudaFuncSetAttribute(step_plan_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 3 * kMaxStepSeqs * (int)sizeof(int));
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(step_slots_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     kMaxStepSeqs * (int)sizeof(int));
+        if (e != cudaSuccess) return e;
+        __atomic_store_n(&configured[dev], 1, __ATOMIC_RELEASE);
+    }
+    e = launch(step_plan_kernel<true>, kStepCluster, kStepCluster, kStepThreads, smem, p, stream);
+    if (e != cudaSuccess || p.max_tokens == 0) return e;
+    const unsigned ctas = (unsigned)(((int64_t)p.max_tokens + kSlotThreads * kStepUnroll - 1) / (kSlotThreads * kStepUnroll));
+    return launch(step_slots_kernel, ctas, 1, kSlotThreads, smem / 3, p, stream);
 }
 
 }  // namespace pa
