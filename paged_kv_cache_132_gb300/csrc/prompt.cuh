@@ -126,23 +126,17 @@ __device__ __forceinline__ bool prompt_aborted(int* abort_flag) { return *reinte
 // Waits for a phase of a barrier.  When the limit runs out, here or in another
 // role, every wait of the CTA ends: the roles run on to the end of their item
 // without data (nothing they write leaves their buffers; the load warp issues
-// nothing more) and then leave.
-__device__ __forceinline__ void prompt_wait_slow(uint64_t* bar, uint32_t parity, int* abort_flag, uint64_t lim,
-                                                 int* err) {
-    const uint64_t start = global_timer_ns();
-    while (!prompt_aborted(abort_flag)) {
-#pragma unroll 1
-        for (int i = 0; i < 16; ++i)
-            if (mbar_try_wait(bar, parity)) return;
-        if (global_timer_ns() - start > lim) {
-            set_error(err, PA_DEVERR_TIMEOUT);
-            atomicExch(abort_flag, 1);
-        }
-    }
-}
+// nothing more) and then leave, and the CTA reports PA_DEVERR_TIMEOUT.  Kept
+// short: it is inlined in some twenty places, and the roles' code competes for
+// the instruction caches.
 template <class Smem>
 __device__ __forceinline__ void prompt_wait(const PromptParams& p, Smem& sm, uint64_t* bar, uint32_t parity) {
-    if (!mbar_try_wait(bar, parity)) prompt_wait_slow(bar, parity, &sm.abort_flag, p.wait_limit_ns, p.err);
+    if (mbar_try_wait(bar, parity)) return;
+    const uint64_t start = global_timer_ns();
+    do {
+        if (prompt_aborted(&sm.abort_flag)) return;
+        if (global_timer_ns() - start > p.wait_limit_ns) *reinterpret_cast<volatile int*>(&sm.abort_flag) = 1;
+    } while (!mbar_try_wait(bar, parity));
 }
 
 // What an item is made of, for every role alike.
@@ -197,7 +191,7 @@ __device__ __forceinline__ bool prompt_next_item(const PromptParams& p, typename
 // time.
 struct PromptWalk {
     int base;    // sequences [base, base + 32) are in the lanes
-    int64_t before;  // (sequence, query tile pair) units before them
+    int before;  // (sequence, query tile pair) units before them
     int row0, len, nb, incl;  // this lane's sequence; inclusive sum of nb over the lanes
 };
 
@@ -223,8 +217,8 @@ __device__ __forceinline__ void prompt_walk_load(const PromptParams& p, PromptWa
 }
 
 // The item with number `index`; length 0 when there is none.
-__device__ __forceinline__ int4 prompt_walk_to(const PromptParams& p, PromptWalk& k, int lane, int64_t index) {
-    const int64_t unit = index / p.num_kv_heads;
+__device__ __forceinline__ int4 prompt_walk_to(const PromptParams& p, PromptWalk& k, int lane, int index) {
+    const int unit = index / p.num_kv_heads;
     while (true) {
         const int total = __shfl_sync(kFullMask, k.incl, 31);
         if (unit < k.before + total) break;
@@ -233,11 +227,11 @@ __device__ __forceinline__ int4 prompt_walk_to(const PromptParams& p, PromptWalk
         if (k.base >= p.num_seqs) return make_int4(0, 0, 0, 0);
         prompt_walk_load(p, k, lane);
     }
-    const int u = (int)(unit - k.before);
+    const int u = unit - k.before;
     const int src = __ffs(__ballot_sync(kFullMask, u < k.incl)) - 1;
     const int row0 = __shfl_sync(kFullMask, k.row0, src), len = __shfl_sync(kFullMask, k.len, src);
     const int incl = __shfl_sync(kFullMask, k.incl, src);
-    return make_int4(row0, len, incl - 1 - u, (int)(index - unit * p.num_kv_heads));
+    return make_int4(row0, len, incl - 1 - u, index - unit * p.num_kv_heads);
 }
 
 template <class Shape>
@@ -245,43 +239,10 @@ __device__ void prompt_load(const PromptParams& p, typename Shape::Smem& sm, int
                             const CUtensorMap* tk, const CUtensorMap* tv) {
     constexpr int HALF_BYTES = Shape::HALF * 128;
     const uint32_t q_bytes = (uint32_t)(Shape::SLABS * p.tile_tokens * p.group * 128);
-    uint32_t q_used[2] = {0, 0};  // items that loaded Q_i
+    uint32_t q_used = 0, q_loaded = 0;  // bit i: parity of the loads of Q_i, whether there was one
     uint32_t slot = 0, round = 0, filled = 0;
     const int total = p.items ? __ldg(p.num_units) * p.num_kv_heads : 0;
     bool ok = true;
-    // One K or V tile of `rows` positions (rounded up to whole halves).
-    auto load_tile = [&](const CUtensorMap* map, const PromptItem& w, int j, int end, bool check) {
-        if (!ok) return;
-        prompt_wait(p, sm, &sm.kv_empty[slot], (round & 1u) ^ 1u);
-        ok = !prompt_aborted(&sm.abort_flag);
-        if (!ok) return;
-        const int halves = end - j * Shape::BN > Shape::HALF ? 2 : 1;
-        mbar_arrive_expect_tx(&sm.kv_full[slot], (uint32_t)(halves * Shape::SLABS * HALF_BYTES));
-        for (int h = 0; h < halves; ++h)
-#pragma unroll
-            for (int s = 0; s < Shape::SLABS; ++s)
-                tma_load_3d_plain(sm.kv[slot][s] + h * HALF_BYTES, map, s * 64, w.kv_head,
-                                  w.row0 + j * Shape::BN + h * Shape::HALF, &sm.kv_full[slot]);
-        filled |= 1u << slot;
-        if (check) mbar_arrive(&sm.check_go[slot]);
-        if (++slot == Shape::NSLOT) {
-            slot = 0;
-            ++round;
-        }
-    };
-    auto load_q = [&](const PromptItem& w, int i) {
-        if (!ok) return;
-        prompt_wait(p, sm, &sm.q_empty[i], (q_used[i] & 1u) ^ 1u);
-        ok = !prompt_aborted(&sm.abort_flag);
-        if (!ok) return;
-        mbar_arrive_expect_tx(&sm.q_full[i], q_bytes);
-#pragma unroll
-        for (int s = 0; s < Shape::SLABS; ++s)
-            tma_load_3d_plain(sm.q[i][s], tq, s * 64, w.kv_head * p.group, w.row0 + w.t0 + i * p.tile_tokens,
-                              &sm.q_full[i]);
-        ++q_used[i];
-    };
-
     auto listed = [&](int index) {
         int4 e = make_int4(0, 0, 0, 0);
         if (index < total) {
@@ -315,13 +276,42 @@ __device__ void prompt_load(const PromptParams& p, typename Shape::Smem& sm, int
         if (lane == 0) {
             const PromptItem w = prompt_item(it, p.tile_tokens);
             const int end = w.last(), nt = (end + 127) >> 7;
-            load_q(w, 0);
-            load_tile(tk, w, 0, end, false);
-            if (w.end1) load_q(w, 1);
-            load_tile(tv, w, 0, end, w.first_masked == 0);
-            for (int j = 1; j < nt && ok; ++j) {
-                load_tile(tk, w, j, end, false);
-                load_tile(tv, w, j, end, j >= w.first_masked);
+            // Q_0, K_0, Q_1, V_0, K_1, V_1, ...
+#pragma unroll 1
+            for (int t = 0; t < 2 * nt && ok; ++t) {
+                if (t < 2 && w.end(t)) {
+                    prompt_wait(p, sm, &sm.q_empty[t], ((q_used >> t) & 1u) ^ 1u);
+                    ok = !prompt_aborted(&sm.abort_flag);
+                    if (!ok) break;
+                    mbar_arrive_expect_tx(&sm.q_full[t], q_bytes);
+#pragma unroll
+                    for (int s = 0; s < Shape::SLABS; ++s)
+                        tma_load_3d_plain(sm.q[t][s], tq, s * 64, w.kv_head * p.group,
+                                          w.row0 + w.t0 + t * p.tile_tokens, &sm.q_full[t]);
+                    q_used ^= 1u << t;
+                    q_loaded |= 1u << t;
+                }
+                // One K or V tile, in halves of 64 positions.
+                const bool is_v = t & 1;
+                const int j = t >> 1, row = w.row0 + j * Shape::BN;
+                prompt_wait(p, sm, &sm.kv_empty[slot], round ^ 1u);
+                ok = !prompt_aborted(&sm.abort_flag);
+                if (!ok) break;
+                const int halves = end - j * Shape::BN > Shape::HALF ? 2 : 1;
+                mbar_arrive_expect_tx(&sm.kv_full[slot], (uint32_t)(halves * Shape::SLABS * HALF_BYTES));
+                const CUtensorMap* map = is_v ? tv : tk;
+#pragma unroll 1
+                for (int h = 0; h < halves; ++h)
+#pragma unroll
+                    for (int s = 0; s < Shape::SLABS; ++s)
+                        tma_load_3d_plain(sm.kv[slot][s] + h * HALF_BYTES, map, s * 64, w.kv_head,
+                                          row + h * Shape::HALF, &sm.kv_full[slot]);
+                filled |= 1u << slot;
+                if (is_v && j >= w.first_masked) mbar_arrive(&sm.check_go[slot]);
+                if (++slot == Shape::NSLOT) {
+                    slot = 0;
+                    round ^= 1u;
+                }
             }
         }
         if (!__shfl_sync(kFullMask, ok, 0)) break;
@@ -332,12 +322,14 @@ __device__ void prompt_load(const PromptParams& p, typename Shape::Smem& sm, int
     // Every copy this warp issued lands before the CTA exits (bounded).
     if (lane == 0) {
         bool drained = true;
+#pragma unroll 1
         for (int i = 0; i < 2; ++i)
-            if (q_used[i]) drained = mbar_wait_bounded(&sm.q_full[i], (q_used[i] & 1u) ^ 1u, p.wait_limit_ns) && drained;
+            if (q_loaded & (1u << i))
+                drained = mbar_wait_bounded(&sm.q_full[i], ((q_used >> i) & 1u) ^ 1u, p.wait_limit_ns) && drained;
+#pragma unroll 1
         for (uint32_t s = 0; s < Shape::NSLOT; ++s)
             if (filled & (1u << s))
-                drained = mbar_wait_bounded(&sm.kv_full[s], (s < slot ? round : round - 1) & 1u, p.wait_limit_ns) &&
-                          drained;
+                drained = mbar_wait_bounded(&sm.kv_full[s], s < slot ? round : round ^ 1u, p.wait_limit_ns) && drained;
         if (!drained) set_error(p.err, PA_DEVERR_TIMEOUT);
     }
     __syncwarp();
@@ -449,13 +441,13 @@ __device__ void prompt_mma(const PromptParams& p, typename Shape::Smem& sm, uint
                 const int nti = i ? tiles1 : tiles0;
                 if (j >= nti) continue;
                 const int cols = cols_of(w.end(i), j);
-                prompt_wait(p, sm, &sm.p_full[i][0], (np >> i) & 1u);
-                tc_fence_after_sync();
-                issue_pv(i, vslot, cols, 0, j == 0);
-                prompt_wait(p, sm, &sm.p_full[i][1], (np >> i) & 1u);
-                tc_fence_after_sync();
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    prompt_wait(p, sm, &sm.p_full[i][half], (np >> i) & 1u);
+                    tc_fence_after_sync();
+                    issue_pv(i, vslot, cols, half, j == 0 && half == 0);
+                }
                 np ^= 1u << i;
-                issue_pv(i, vslot, cols, 1, false);
                 if (j + 1 < nti) {
                     issue_s(i, kslot, cols_of(w.end(i), j + 1));
                     if (j + 2 == nti) prompt_commit(&sm.q_empty[i]);
@@ -828,6 +820,7 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
+    if (threadIdx.x == 0 && sm.abort_flag) set_error(p.err, PA_DEVERR_TIMEOUT);
     if (warp == Shape::MMA_WARP) tmem_dealloc(tmem, Shape::TMEM_COLS);
 }
 
