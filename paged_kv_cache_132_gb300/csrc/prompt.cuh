@@ -62,13 +62,13 @@ struct PromptShape {
     static constexpr int NSLOT = D == 128 ? 5 : 8;  // K/V ring: K_0, V_0, K_1, V_1, ... one tile per slot
     static constexpr int NITEM = 4;              // work items announced ahead of their last reader
     static constexpr int SOFTMAX_WARPS = 4;      // per query tile
-    static constexpr int MMA_WARP = 0;
-    static constexpr int LOAD_WARP = 1;
-    static constexpr int CHECK_WARP = 2;         // first of two
+    static constexpr int MMA_WARP = 0;           // first of two, one per query tile
+    static constexpr int LOAD_WARP = 2;
+    static constexpr int CHECK_WARP = 3;
     static constexpr int SOFTMAX_WARP = 4;       // first of eight
     static constexpr int OUT_WARP = 12;          // first of four
     static constexpr int THREADS = 512;
-    static constexpr int ITEM_READERS = 8 + 4 + 1 + 2;  // softmax, output, MMA and check warps
+    static constexpr int ITEM_READERS = 8 + 4 + 2 + 1;  // softmax, output, MMA and check warps
     // Registers per thread after the split: 256 * 176 + 128 * 64 + 128 * 96
     // = 512 * 128, the launch's total.
     static constexpr int REGS_SOFTMAX = 176, REGS_OUT = 64, REGS_OTHER = 96;
@@ -89,7 +89,7 @@ struct PromptShape {
         uint64_t q_full[2];         // Q_i landed
         uint64_t q_empty[2];        // last S_i of the item complete
         uint64_t kv_full[NSLOT];    // tile landed
-        uint64_t kv_empty[NSLOT];   // the MMAs that read it complete
+        uint64_t kv_empty[NSLOT];   // the MMAs of both query tiles that read it complete
         uint64_t check_go[NSLOT];   // the copy of a V tile with masked positions was issued (load warp)
         uint64_t v_checked[NSLOT];  // ... and the tile is fit for P.V (check warps)
         uint64_t s_full[2];         // S_i complete
@@ -97,7 +97,8 @@ struct PromptShape {
         uint64_t o_full[2];         // last P_i V_j of the item complete
         uint64_t l_full[2];         // row sums written (softmax warps)
         uint64_t o_empty[2];        // O_i and the row sums read (output warps)
-        uint64_t mma_done;
+        uint64_t turn[2];           // MMA warp i may issue its step
+        uint64_t mma_done[2];
         uint32_t tmem_base;
         int abort_flag;
     };
@@ -137,6 +138,29 @@ __device__ __forceinline__ void prompt_wait(const PromptParams& p, Smem& sm, uin
         if (prompt_aborted(&sm.abort_flag)) return;
         if (global_timer_ns() - start > p.wait_limit_ns) *reinterpret_cast<volatile int*>(&sm.abort_flag) = 1;
     } while (!mbar_try_wait(bar, parity));
+}
+
+// The same for a barrier given by its shared-memory address (the MMA warp, whose
+// every instruction between a P and its MMAs is waited for).
+__device__ __forceinline__ bool try_wait_at(uint32_t bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+template <class Smem>
+__device__ __forceinline__ void prompt_wait_at(const PromptParams& p, Smem& sm, uint32_t bar, uint32_t parity) {
+    if (try_wait_at(bar, parity)) return;
+    const uint64_t start = global_timer_ns();
+    do {
+        if (prompt_aborted(&sm.abort_flag)) return;
+        if (global_timer_ns() - start > p.wait_limit_ns) *reinterpret_cast<volatile int*>(&sm.abort_flag) = 1;
+    } while (!try_wait_at(bar, parity));
 }
 
 // What an item is made of, for every role alike.
@@ -351,51 +375,71 @@ __device__ __forceinline__ bool elect_one() {
         : "=r"(lead));
     return lead != 0;
 }
-__device__ __forceinline__ void prompt_commit(uint64_t* bar) {
-    if (elect_one()) mma_commit(bar);
+__device__ __forceinline__ void commit_at(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// The operands' descriptors (smem_desc_sw128) differ in their lower halves only:
+// stride 1024 bytes, version 1, 128-byte swizzle above.  Addresses / 16 stay
+// below 2^14, so a step never carries out of its field.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ void mma_ss_lo(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, bool first) {
+    asm volatile(
+        "{\n\t.reg .b64 a, b;\n\t.reg .pred acc;\n\t"
+        "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+        "setp.ne.b32 acc, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, acc;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(first ? 0u : 1u), "n"(kDescHi)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts_lo(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, bool first) {
+    asm volatile(
+        "{\n\t.reg .b64 b;\n\t.reg .pred acc;\n\t"
+        "mov.b64 b, {%2, %5};\n\t"
+        "setp.ne.b32 acc, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, acc;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(first ? 0u : 1u), "n"(kDescHi)
+        : "memory");
 }
 
 template <class Shape, bool BF16>
-__device__ void prompt_mma(const PromptParams& p, typename Shape::Smem& sm, uint32_t tmem, int lane) {
+__device__ void prompt_mma(const PromptParams& p, typename Shape::Smem& sm, uint32_t tmem, int i, int lane) {
+    using Smem = typename Shape::Smem;
     constexpr int D = Shape::SLABS * 64;
-    constexpr uint32_t IDESC_S = mma_idesc_f16(BF16, false, Shape::BM, 0);  // N is added per tile
     constexpr uint32_t IDESC_O = mma_idesc_f16(BF16, true, Shape::BM, D);
+    constexpr uint32_t IDESC_S = mma_idesc_f16(BF16, false, Shape::BM, 128);
+    constexpr uint32_t IDESC_S64 = mma_idesc_f16(BF16, false, Shape::BM, 64);
     constexpr uint32_t SLOT16 = sizeof(sm.kv[0]) >> 4, Q16 = sizeof(sm.q[0]) >> 4;
-    const uint64_t dq = smem_desc_sw128(smem_addr(sm.q[0][0]), 16, 1024);
-    const uint64_t dk = smem_desc_sw128(smem_addr(sm.kv[0][0]), 16, 1024);
-    const uint64_t dv = smem_desc_sw128(smem_addr(sm.kv[0][0]), Shape::SLAB, 1024);
+    const uint32_t base = smem_addr(&sm);
+    const uint32_t q_lo = (uint32_t)smem_desc_sw128(base + offsetof(Smem, q), 16, 1024);
+    const uint32_t k_lo = (uint32_t)smem_desc_sw128(base + offsetof(Smem, kv), 16, 1024);
+    const uint32_t v_lo = (uint32_t)smem_desc_sw128(base + offsetof(Smem, kv), Shape::SLAB, 1024);
+    auto bar = [&](size_t member, uint32_t index) { return base + (uint32_t)member + 8u * index; };
+    auto wait = [&](uint32_t at, uint32_t parity) { prompt_wait_at(p, sm, at, parity); };
 
-    // S_i = Q_i K^T over the first `cols` (a multiple of 16) positions of the tile.
-    auto issue_s = [&](int i, uint32_t slot, int cols) {
-        const uint32_t idesc = IDESC_S | ((uint32_t)(cols >> 3) << 17), d = tmem + i * Shape::BN;
-        const uint64_t a = dq + i * Q16, b = dk + slot * SLOT16;
-        if (elect_one()) {
+    // For the elected lane: S = Q K^T over the K tile's first half or all of it.
+    const uint32_t s_tmem = tmem + i * Shape::BN, o_tmem = tmem + Shape::O_COL + i * D, qi_lo = q_lo + i * Q16;
+    auto issue_s = [&](uint32_t slot, bool whole) {
+        const uint32_t idesc = whole ? IDESC_S : IDESC_S64, b = k_lo + slot * SLOT16;
 #pragma unroll
-            for (int ks = 0; ks < Shape::SLABS * 4; ++ks) {
-                const uint32_t off = (uint32_t)((ks >> 2) * (Shape::SLAB >> 4) + (ks & 3) * 2);
-                mma_f16_ss(d, a + off, b + off, idesc, ks > 0 ? 1u : 0u);
-            }
-            mma_commit(&sm.s_full[i]);
+        for (int ks = 0; ks < Shape::SLABS * 4; ++ks) {
+            const uint32_t off = (uint32_t)((ks >> 2) * (Shape::SLAB >> 4) + (ks & 3) * 2);
+            mma_ss_lo(s_tmem, qi_lo + off, b + off, idesc, ks == 0);
         }
-        __syncwarp();
+        commit_at(bar(offsetof(Smem, s_full), i));
     };
-    // O_i (+)= P_i V over one half (64) of the same positions.
-    auto issue_pv = [&](int i, uint32_t slot, int cols, int half, bool first) {
-        const uint32_t a = tmem + i * Shape::BN + half * 32, o = tmem + Shape::O_COL + i * D;
-        const uint64_t b = dv + slot * SLOT16 + half * 512;
-        if (elect_one()) {
+    // O (+)= P V over one half (64) of the V tile's positions.
+    auto issue_pv = [&](uint32_t slot, int half, bool first) {
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-                if (half * 64 + ks * 16 < cols)
-                    mma_f16_ts(o, a + ks * 8, b + ks * 128, IDESC_O, (ks > 0 || !first) ? 1u : 0u);
-        }
-        __syncwarp();
+        for (int ks = 0; ks < 4; ++ks)
+            mma_ts_lo(o_tmem, s_tmem + half * 32 + ks * 8, v_lo + slot * SLOT16 + half * 512 + ks * 128, IDESC_O,
+                      first && ks == 0);
     };
-    auto cols_of = [](int end, int j) { return min(Shape::BN, (end - j * Shape::BN + 15) & ~15); };
 
-    uint32_t slot = 0, round = 0;  // ring position of the next tile, parity of its round
-    uint32_t used = 0, np = 0;     // bit i: parities of tile i's items and P so far
-    uint32_t checked = 0;          // bit slot: of the slot's checked V tiles so far
+    uint32_t slot = 0, round = 0;         // ring position of the next tile, parity of its round
+    uint32_t nq = 0, no = 0, np = 0;      // parities of the tile's Q, O and P so far
+    uint32_t turn = i ^ 1;                // parity of the turn to wait for: the other warp's last one
+    uint32_t checked = 0;                 // bit slot: of the slot's checked V tiles so far
     auto advance = [&] {
         if (++slot == Shape::NSLOT) {
             slot = 0;
@@ -404,65 +448,79 @@ __device__ void prompt_mma(const PromptParams& p, typename Shape::Smem& sm, uint
     };
     int n = 0;
     PromptItem w;
-    while (prompt_next_item<Shape>(p, sm, lane, n, w)) {
-        const int tiles0 = w.tiles(0), tiles1 = w.tiles(1), nt = max(tiles0, tiles1);
-        const int both = w.end1 ? 2 : 1;
-        prompt_wait(p, sm, &sm.kv_full[slot], round);
-#pragma unroll 1
-        for (int i = 0; i < both; ++i) {
-            prompt_wait(p, sm, &sm.q_full[i], (used >> i) & 1u);
-            issue_s(i, slot, cols_of(w.end(i), 0));
-            if (w.tiles(i) == 1) prompt_commit(&sm.q_empty[i]);
+    bool more = prompt_next_item<Shape>(p, sm, lane, n, w);
+    if (more) {
+        wait(bar(offsetof(Smem, kv_full), slot), round);
+        if (w.end(i)) wait(bar(offsetof(Smem, q_full), i), nq++);
+        if (elect_one()) {
+            if (w.end(i)) issue_s(slot, w.end(i) > 64);
+            if (w.tiles(i) == 1) commit_at(bar(offsetof(Smem, q_empty), i));
+            commit_at(bar(offsetof(Smem, kv_empty), slot));
         }
-        prompt_commit(&sm.kv_empty[slot]);
+        __syncwarp();
         advance();
-        // The accumulators: free once the output warps have read the item before.
-#pragma unroll 1
-        for (int i = 0; i < both; ++i) prompt_wait(p, sm, &sm.o_empty[i], ((used >> i) & 1u) ^ 1u);
+    }
+    // A step: O += P V_j and S of the next K tile, which after an item's last step
+    // is the first one of the next item.
+    while (more) {
+        const int nt = (w.last() + 127) >> 7;
+        PromptItem next = w;
 #pragma unroll 1
         for (int j = 0; j < nt; ++j) {
-            // V_j and K_j+1 are waited for here, before the P that takes longest,
-            // so that between the MMAs of a step there is no wait but for P.
             const uint32_t vslot = slot;
             if (j >= w.first_masked) {
-                prompt_wait(p, sm, &sm.v_checked[vslot], (checked >> vslot) & 1u);
+                wait(bar(offsetof(Smem, v_checked), vslot), (checked >> vslot) & 1u);
                 checked ^= 1u << vslot;
             } else {
-                prompt_wait(p, sm, &sm.kv_full[vslot], round);
+                wait(bar(offsetof(Smem, kv_full), vslot), round);
             }
             advance();
-            const uint32_t kslot = slot;
-            if (j + 1 < nt) {
-                prompt_wait(p, sm, &sm.kv_full[kslot], round);
+            const uint32_t kslot = slot, kround = round;
+            const bool last = j + 1 == nt;
+            if (last) more = prompt_next_item<Shape>(p, sm, lane, n, next);
+            const bool has_k = !last || more;
+            if (has_k) {
+                wait(bar(offsetof(Smem, kv_full), kslot), kround);
                 advance();
             }
-#pragma unroll 1
-            for (int i = 0; i < both; ++i) {
-                const int nti = i ? tiles1 : tiles0;
-                if (j >= nti) continue;
-                const int cols = cols_of(w.end(i), j);
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    prompt_wait(p, sm, &sm.p_full[i][half], (np >> i) & 1u);
-                    tc_fence_after_sync();
-                    issue_pv(i, vslot, cols, half, j == 0 && half == 0);
-                }
-                np ^= 1u << i;
-                if (j + 1 < nti) {
-                    issue_s(i, kslot, cols_of(w.end(i), j + 1));
-                    if (j + 2 == nti) prompt_commit(&sm.q_empty[i]);
-                } else {
-                    prompt_commit(&sm.o_full[i]);
-                }
+            // Positions of the item from V_j on, and of what K is the tile of (<= 0: none).
+            const int left = w.end(i) - j * Shape::BN;
+            const bool leaves = last && more && next.end(i) > 0;
+            const int left_k = last ? (leaves ? next.end(i) : 0) : left - Shape::BN;
+            if (left > 0) {
+                if (j == 0) wait(bar(offsetof(Smem, o_empty), i), (no++ & 1u) ^ 1u);  // read by the output warps
+                wait(bar(offsetof(Smem, p_full), 2 * i), np & 1u);
             }
-            prompt_commit(&sm.kv_empty[vslot]);
-            if (j + 1 < nt) prompt_commit(&sm.kv_empty[kslot]);
+            // The two warps take turns: the tensor cores get one query tile's step
+            // while the other's softmax runs.  What a warp does between its steps is
+            // hidden behind the other's MMAs.
+            wait(bar(offsetof(Smem, turn), i), turn & 1u);
+            ++turn;
+            if (left > 0) {
+                tc_fence_after_sync();
+                if (elect_one()) issue_pv(vslot, 0, j == 0);
+                __syncwarp();
+                wait(bar(offsetof(Smem, p_full), 2 * i + 1), np++ & 1u);
+                tc_fence_after_sync();
+            }
+            if (leaves) wait(bar(offsetof(Smem, q_full), i), nq++ & 1u);
+            if (elect_one()) {
+                if (left > 64) issue_pv(vslot, 1, false);
+                if (left > 0 && left <= Shape::BN) commit_at(bar(offsetof(Smem, o_full), i));
+                if (left_k > 0) issue_s(kslot, left_k > 64);
+                mbar_arrive(&sm.turn[i ^ 1]);
+                if (left_k > 0 && left_k <= Shape::BN) commit_at(bar(offsetof(Smem, q_empty), i));
+                commit_at(bar(offsetof(Smem, kv_empty), vslot));
+                if (has_k) commit_at(bar(offsetof(Smem, kv_empty), kslot));
+            }
+            __syncwarp();
         }
-        used ^= both == 2 ? 3u : 1u;
+        w = next;
     }
     // Nothing this warp issued may still be running when TMEM is released.
-    prompt_commit(&sm.mma_done);
-    if (lane == 0 && !mbar_wait_bounded(&sm.mma_done, 0, p.wait_limit_ns)) set_error(p.err, PA_DEVERR_TIMEOUT);
+    if (elect_one()) commit_at(bar(offsetof(Smem, mma_done), i));
+    __syncwarp();
+    if (lane == 0 && !mbar_wait_bounded(&sm.mma_done[i], 0, p.wait_limit_ns)) set_error(p.err, PA_DEVERR_TIMEOUT);
     __syncwarp();
 }
 
@@ -632,9 +690,8 @@ __device__ __forceinline__ uint32_t nonfinite2(uint32_t w) {
 }
 
 template <typename T, class Shape>
-__device__ void prompt_check(const PromptParams& p, typename Shape::Smem& sm, int thread) {
+__device__ void prompt_check(const PromptParams& p, typename Shape::Smem& sm, int lane) {
     constexpr int CHUNKS = Shape::SLABS * 8;  // 16-byte chunks of a row
-    const int lane = thread & 31;
     uint32_t tiles = 0;   // ring tiles before the item
     uint32_t parity = 0;  // per slot: of its next masked V tile
     int n = 0;
@@ -651,20 +708,20 @@ __device__ void prompt_check(const PromptParams& p, typename Shape::Smem& sm, in
             parity ^= 1u << slot;
             // Rows up to the item's first token are attended by all its rows.
             const int first = max(w.t0 + 1 - j * Shape::BN, 0);
-            const int rows = min(Shape::BN, end - j * Shape::BN), rows16 = (rows + 15) & ~15;
+            const int rows = min(Shape::BN, end - j * Shape::BN), all = (rows + 63) & ~63;
             auto chunk_at = [&](int idx) {
                 return reinterpret_cast<uint4*>(sm.kv[slot][(idx % CHUNKS) >> 3] + idx / CHUNKS * 128) + (idx & 7);
             };
-            for (int idx = rows * CHUNKS + thread; idx < rows16 * CHUNKS; idx += 64)
+            for (int idx = rows * CHUNKS + lane; idx < all * CHUNKS; idx += 32)
                 *chunk_at(idx) = make_uint4(0u, 0u, 0u, 0u);
             uint32_t found = 0;
 #pragma unroll 8
-            for (int idx = first * CHUNKS + thread; idx < rows * CHUNKS; idx += 64) {
+            for (int idx = first * CHUNKS + lane; idx < rows * CHUNKS; idx += 32) {
                 const uint4 v = *chunk_at(idx);
                 found |= nonfinite2<T>(v.x) | nonfinite2<T>(v.y) | nonfinite2<T>(v.z) | nonfinite2<T>(v.w);
             }
             if (found) {
-                for (int idx = first * CHUNKS + thread; idx < rows * CHUNKS; idx += 64) {
+                for (int idx = first * CHUNKS + lane; idx < rows * CHUNKS; idx += 32) {
                     uint32_t* v = reinterpret_cast<uint32_t*>(chunk_at(idx));
                     for (int e = 0; e < 4; ++e) {
                         const uint32_t bad = nonfinite2<T>(v[e]);
@@ -773,12 +830,14 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
         }
         for (int s = 0; s < Shape::NSLOT; ++s) {
             mbar_init(&sm.kv_full[s], 1);
-            mbar_init(&sm.kv_empty[s], 1);
+            mbar_init(&sm.kv_empty[s], 2);
             mbar_init(&sm.check_go[s], 1);
-            mbar_init(&sm.v_checked[s], 2);
+            mbar_init(&sm.v_checked[s], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.q_full[i], 1);
+            mbar_init(&sm.turn[i], 1);
+            mbar_init(&sm.mma_done[i], 1);
             mbar_init(&sm.q_empty[i], 1);
             mbar_init(&sm.s_full[i], 1);
             mbar_init(&sm.p_full[i][0], Shape::SOFTMAX_WARPS);
@@ -787,7 +846,6 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
             mbar_init(&sm.l_full[i], Shape::SOFTMAX_WARPS);
             mbar_init(&sm.o_empty[i], 4);
         }
-        mbar_init(&sm.mma_done, 1);
         sm.abort_flag = 0;
         sm.last_dirty = -1;
         fence_mbar_init();
@@ -802,12 +860,12 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
 
     if (warp < Shape::SOFTMAX_WARP) {
         regs_dec<Shape::REGS_OTHER>();
-        if (warp == Shape::MMA_WARP)
-            prompt_mma<Shape, std::is_same<T, __nv_bfloat16>::value>(p, sm, tmem, lane);
+        if (warp < Shape::LOAD_WARP)
+            prompt_mma<Shape, std::is_same<T, __nv_bfloat16>::value>(p, sm, tmem, warp, lane);
         else if (warp == Shape::LOAD_WARP)
             prompt_load<Shape>(p, sm, lane, &tmap_q, &tmap_k, &tmap_v);
         else
-            prompt_check<T, Shape>(p, sm, threadIdx.x - Shape::CHECK_WARP * 32);
+            prompt_check<T, Shape>(p, sm, lane);
     } else if (warp < Shape::OUT_WARP) {
         regs_inc<Shape::REGS_SOFTMAX>();
         const int v = warp - Shape::SOFTMAX_WARP;
