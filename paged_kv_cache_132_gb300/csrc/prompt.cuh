@@ -661,9 +661,11 @@ __device__ void prompt_softmax(const PromptParams& p, typename Shape::Smem& sm, 
             };
             piece(x0, s_addr);
             piece(x0 + 32, s_addr + 16);
-            if (cols > 64) piece(x1, s_addr + 32);
             written(0);
-            if (cols > 64) piece(x1 + 32, s_addr + 48);
+            if (cols > 64) {
+                piece(x1, s_addr + 32);
+                piece(x1 + 32, s_addr + 48);
+            }
             written(1);
             l += (ps[0] + ps[1]) + (ps[2] + ps[3]);
         }
