@@ -362,8 +362,8 @@ size_t pa_prompt_attention_workspace_size(int32_t num_seqs, int32_t num_tokens, 
  * array; its token i attends to its tokens 0 .. i:
  *   out[q][h][:] = sum_j softmax_j(scale * query[q][h] . key_j) value_j,
  * query head h reading KV head h / G, G = num_heads / num_kv_heads.
- *   out               device, [num_tokens][num_heads][head_dim] of `dtype`;
- *                     rows not covered by a sequence are not written
+ *   out               device, 32-byte aligned, [num_tokens][num_heads][head_dim]
+ *                     of `dtype`; rows not covered by a sequence are not written
  *   query, key, value device, of `dtype`: rows of num_heads (num_kv_heads)
  *                     heads of head_dim contiguous elements, *_stride elements
  *                     from one token's row to the next: at least the row, a

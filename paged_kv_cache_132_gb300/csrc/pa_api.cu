@@ -659,7 +659,7 @@ int pa_prompt_attention(void* out, const void* query, int64_t query_stride, cons
         key_stride % head_dim != 0 || value_stride % head_dim != 0)
         return PA_ERR_INVALID_ARG;
     if (num_seqs == 0 || num_tokens == 0) return PA_OK;
-    if (!aligned(out, 16) || !aligned(query, 16) || !aligned(key, 16) || !aligned(value, 16) ||
+    if (!aligned(out, 32) || !aligned(query, 16) || !aligned(key, 16) || !aligned(value, 16) ||
         !aligned(query_start_loc, 4))
         return PA_ERR_INVALID_ARG;
     if (dtype == PA_F32) return PA_ERR_UNSUPPORTED;

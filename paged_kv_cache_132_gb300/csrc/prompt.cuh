@@ -753,6 +753,15 @@ __device__ __noinline__ void prompt_add_nonfinite(const PromptParams& p, const P
     }
 }
 
+// A whole sector of a row by one thread: the rows of a warp are far apart, and
+// 16-byte stores take twice as many passes of the memory pipeline, which the
+// softmax warps' TMEM accesses share.
+__device__ __forceinline__ void store_32_bytes(void* dst, const uint32_t (&q)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(q[0]), "r"(q[1]), "r"(q[2]),
+                 "r"(q[3]), "r"(q[4]), "r"(q[5]), "r"(q[6]), "r"(q[7])
+                 : "memory");
+}
+
 template <typename T, class Shape>
 __device__ void prompt_output(const PromptParams& p, typename Shape::Smem& sm, uint32_t tmem, int warp, int lane) {
     constexpr int D = Shape::SLABS * 64;
@@ -788,13 +797,13 @@ __device__ void prompt_output(const PromptParams& p, typename Shape::Smem& sm, u
                 }
                 if (store) {
 #pragma unroll
-                    for (int k = 0; k < 32; k += 8) {
-                        uint4 q;
-                        q.x = pack_rn<T>(__uint_as_float(u[k]) * inv, __uint_as_float(u[k + 1]) * inv);
-                        q.y = pack_rn<T>(__uint_as_float(u[k + 2]) * inv, __uint_as_float(u[k + 3]) * inv);
-                        q.z = pack_rn<T>(__uint_as_float(u[k + 4]) * inv, __uint_as_float(u[k + 5]) * inv);
-                        q.w = pack_rn<T>(__uint_as_float(u[k + 6]) * inv, __uint_as_float(u[k + 7]) * inv);
-                        *reinterpret_cast<uint4*>(dst + c0 + k) = q;
+                    for (int k = 0; k < 32; k += 16) {
+                        uint32_t q[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            q[e] = pack_rn<T>(__uint_as_float(u[k + 2 * e]) * inv,
+                                              __uint_as_float(u[k + 2 * e + 1]) * inv);
+                        store_32_bytes(dst + c0 + k, q);
                     }
                 }
             }

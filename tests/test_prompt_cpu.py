@@ -41,6 +41,7 @@ def _call(lib, **over):
     (dict(qs=256 + 8), -1),             # not a multiple of head_dim
     (dict(ks=128 + 32), -1),
     (dict(out=0), -1),
+    (dict(out=FAKE + 16), -1),          # 32 bytes
     (dict(q=0), -1),
     (dict(q=FAKE + 8), -1),             # misaligned
     (dict(k=FAKE + 2), -1),
