@@ -686,9 +686,22 @@ __device__ __forceinline__ uint32_t nonfinite2(uint32_t w) {
         return ((w & 0x7c007c00u) + 0x04000400u) & 0x80008000u;
 }
 
+// 0 * w + a on both 16-bit halves.
+template <typename T>
+__device__ __forceinline__ uint32_t times_zero_plus(uint32_t w, uint32_t a) {
+    uint32_t d;
+    if constexpr (std::is_same<T, __nv_bfloat16>::value)
+        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(w), "r"(0u), "r"(a));
+    else
+        asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(w), "r"(0u), "r"(a));
+    return d;
+}
+
 template <typename T, class Shape>
 __device__ void prompt_check(const PromptParams& p, typename Shape::Smem& sm, int lane) {
     constexpr int CHUNKS = Shape::SLABS * 8;  // 16-byte chunks of a row
+    constexpr int STEP = 32 / CHUNKS;         // rows of one pass of the warp
+    const int my_chunk = lane % CHUNKS, my_row = lane / CHUNKS;
     uint32_t tiles = 0;   // ring tiles before the item
     uint32_t parity = 0;  // per slot: of its next masked V tile
     int n = 0;
@@ -706,20 +719,25 @@ __device__ void prompt_check(const PromptParams& p, typename Shape::Smem& sm, in
             // Rows up to the item's first token are attended by all its rows.
             const int first = max(w.t0 + 1 - j * Shape::BN, 0);
             const int rows = min(Shape::BN, end - j * Shape::BN), all = (rows + 63) & ~63;
-            auto chunk_at = [&](int idx) {
-                return reinterpret_cast<uint4*>(sm.kv[slot][(idx % CHUNKS) >> 3] + idx / CHUNKS * 128) + (idx & 7);
-            };
-            for (int idx = rows * CHUNKS + lane; idx < all * CHUNKS; idx += 32)
-                *chunk_at(idx) = make_uint4(0u, 0u, 0u, 0u);
-            uint32_t found = 0;
+            // This lane's chunk of rows lane / CHUNKS, + STEP, ...
+            uint8_t* const column = sm.kv[slot][my_chunk >> 3] + (my_chunk & 7) * 16;
+            auto at = [&](int row) { return reinterpret_cast<uint4*>(column + row * 128); };
+            for (int row = rows + my_row; row < all; row += STEP) *at(row) = make_uint4(0u, 0u, 0u, 0u);
+            // 0 * v: NaN where v is infinite or NaN, and then for good in the sum.
+            uint32_t acc[4] = {0u, 0u, 0u, 0u};
 #pragma unroll 8
-            for (int idx = first * CHUNKS + lane; idx < rows * CHUNKS; idx += 32) {
-                const uint4 v = *chunk_at(idx);
-                found |= nonfinite2<T>(v.x) | nonfinite2<T>(v.y) | nonfinite2<T>(v.z) | nonfinite2<T>(v.w);
+            for (int row = first + my_row; row < rows; row += STEP) {
+                const uint4 v = *at(row);
+                acc[0] = times_zero_plus<T>(v.x, acc[0]);
+                acc[1] = times_zero_plus<T>(v.y, acc[1]);
+                acc[2] = times_zero_plus<T>(v.z, acc[2]);
+                acc[3] = times_zero_plus<T>(v.w, acc[3]);
             }
-            if (found) {
-                for (int idx = first * CHUNKS + lane; idx < rows * CHUNKS; idx += 32) {
-                    uint32_t* v = reinterpret_cast<uint32_t*>(chunk_at(idx));
+            if ((acc[0] | acc[1] | acc[2] | acc[3]) & 0x7fff7fffu) {
+#pragma unroll 1
+                for (int row = first + my_row; row < rows; row += STEP) {
+                    uint32_t* v = reinterpret_cast<uint32_t*>(at(row));
+#pragma unroll 1
                     for (int e = 0; e < 4; ++e) {
                         const uint32_t bad = nonfinite2<T>(v[e]);
                         v[e] &= ~(((bad >> 31) * 0xffff0000u) | ((bad >> 15 & 1u) * 0xffffu));
