@@ -221,7 +221,7 @@ def _require_here(*tensors: torch.Tensor) -> None:
     """The library works on the current device: tensors of another one are refused."""
     dev = torch.cuda.current_device()
     for t in tensors:
-        if not t.is_cuda or t.device.index != dev:
+        if t.get_device() != dev:  # -1 for a CPU tensor
             raise ValueError("tensors must be on the current CUDA device")
 
 
@@ -238,6 +238,8 @@ def _token_stride(t: torch.Tensor, name: str) -> int:
     """Elements from one token's row of heads to the next; the heads of a token are contiguous."""
     tokens, heads, d = t.shape
     by_token, by_head, by_elem = t.stride()
+    if by_elem == 1 and by_head == d and by_token >= heads * d:
+        return by_token
     if (by_elem != 1 and d > 1) or (by_head != d and heads > 1):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
     if tokens <= 1:
@@ -261,24 +263,24 @@ def rotary_and_cache(query: torch.Tensor, key: torch.Tensor, value: torch.Tensor
     The rows may be slices of a fused projection's rows, and query_out / key_out
     the query / key themselves."""
     lib = native.load()
-    _require(query.dim() == 3 and key.dim() == 3 and k_cache.dim() == 4, "rows are [tokens][heads][head_dim]")
+    _require(query.dim() == 3 and key.dim() == 3, "rows are [tokens][heads][head_dim]")
     t, h, d = query.shape
     desc = cache_desc(k_cache)
-    _require(k_cache.shape == v_cache.shape and k_cache.dtype == v_cache.dtype and k_cache.is_contiguous()
+    dtype = k_cache.dtype
+    _require(k_cache.shape == v_cache.shape and v_cache.dtype is dtype and k_cache.is_contiguous()
              and v_cache.is_contiguous(), "K and V pools must match and be contiguous")
-    _require(key.shape == value.shape and tuple(key.shape) == (t, desc.num_kv_heads, d) and d == desc.head_dim,
+    _require(key.shape == (t, desc.num_kv_heads, d) and value.shape == key.shape and d == desc.head_dim,
              "key/value are [num_tokens][num_kv_heads][head_dim] of the pools")
-    _require(query.dtype == k_cache.dtype and key.dtype == k_cache.dtype and value.dtype == k_cache.dtype,
+    _require(query.dtype is dtype and key.dtype is dtype and value.dtype is dtype,
              "query, key and value share the pools' dtype")
-    _require(positions.dtype == torch.int32 and positions.dim() == 1 and positions.numel() == t
-             and positions.is_contiguous(), "positions is int32 [T]")
-    _require(slot_mapping.dtype == torch.int64 and slot_mapping.dim() == 1 and slot_mapping.numel() == t
-             and slot_mapping.is_contiguous(), "slot_mapping is int64 [T]")
-    _require(cos_sin.dtype == torch.float32 and cos_sin.dim() == 2 and cos_sin.is_contiguous(),
+    _require(positions.dtype is torch.int32 and positions.shape == (t,) and positions.is_contiguous()
+             and slot_mapping.dtype is torch.int64 and slot_mapping.shape == (t,) and slot_mapping.is_contiguous(),
+             "positions is int32 [T], slot_mapping int64 [T]")
+    _require(cos_sin.dtype is torch.float32 and cos_sin.dim() == 2 and cos_sin.is_contiguous(),
              "cos_sin is float32 [positions][rotary_dim]")
     if query_out is None:
-        query_out = _empty((t, h, d), query.dtype, query.device, stream)
-    _require(query_out.shape == query.shape and query_out.dtype == query.dtype, "query_out is like query")
+        query_out = _empty((t, h, d), dtype, query.device, stream)
+    _require(query_out.shape == query.shape and query_out.dtype is dtype, "query_out is like query")
     _require_here(query, key, value, positions, cos_sin, slot_mapping, k_cache, v_cache, query_out)
     key_ptr, key_stride = None, 0
     if key_out is not None:
@@ -369,25 +371,26 @@ def prompt_attention(query: torch.Tensor, key: torch.Tensor, value: torch.Tensor
     _require(query.dim() == 3 and key.dim() == 3, "query is [num_tokens][num_heads][head_dim], key its KV heads")
     t, h, d = query.shape
     hkv = key.shape[1]
-    _require(key.shape == value.shape and key.shape[0] == t and key.shape[2] == d,
+    dtype = query.dtype
+    _require(key.shape == (t, hkv, d) and value.shape == key.shape,
              "key/value are [num_tokens][num_kv_heads][head_dim]")
-    _require(query.dtype in DTYPE_CODE and key.dtype == query.dtype and value.dtype == query.dtype,
+    _require(dtype in DTYPE_CODE and key.dtype is dtype and value.dtype is dtype,
              "query, key and value share one dtype")
-    _require(query_start_loc.dtype == torch.int32 and query_start_loc.dim() == 1 and query_start_loc.numel() > 0
+    _require(query_start_loc.dtype is torch.int32 and query_start_loc.dim() == 1 and query_start_loc.numel() > 0
              and query_start_loc.is_contiguous(), "query_start_loc is int32 [num_seqs + 1]")
     if out is None:
-        out = _empty((t, h, d), query.dtype, query.device, stream)
-    _require(out.shape == query.shape and out.dtype == query.dtype and out.is_contiguous(),
+        out = _empty((t, h, d), dtype, query.device, stream)
+    _require(out.shape == query.shape and out.dtype is dtype and out.is_contiguous(),
              "out is contiguous [num_tokens][num_heads][head_dim] of the inputs' dtype")
     if workspace is None:
         need = lib.pa_prompt_attention_workspace_size(query_start_loc.numel() - 1, t, h, hkv)
         workspace = _empty((max(need, 256),), torch.uint8, query.device, stream)
-    _require(workspace.dtype == torch.uint8 and workspace.is_contiguous(), "workspace is bytes")
+    _require(workspace.dtype is torch.uint8 and workspace.is_contiguous(), "workspace is bytes")
     _require_here(query, key, value, query_start_loc, out, workspace)
     _raise(lib.pa_prompt_attention(out.data_ptr(), query.data_ptr(), _token_stride(query, "query"), key.data_ptr(),
                                    _token_stride(key, "key"), value.data_ptr(), _token_stride(value, "value"),
                                    query_start_loc.data_ptr(), query_start_loc.numel() - 1, t, h, hkv, d,
-                                   DTYPE_CODE[query.dtype], float(scale), workspace.data_ptr(), workspace.numel(),
+                                   DTYPE_CODE[dtype], float(scale), workspace.data_ptr(), workspace.numel(),
                                    _stream_ptr(stream)),
            "pa_prompt_attention")
     return out
