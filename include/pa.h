@@ -377,8 +377,8 @@ size_t pa_prompt_attention_workspace_size(int32_t num_seqs, int32_t num_tokens, 
  * sequences, rows outside every sequence -- may hold anything, NaN included.
  * Supported: f16 or bf16, head_dim 64 or 128, G <= 128; else
  * PA_ERR_UNSUPPORTED.  A sequence whose start rows break the rules above sets
- * PA_DEVERR_CONTEXT_LEN and is skipped; start rows that overlap may set it too,
- * and what the workspace's list has no room for is then not computed.
+ * PA_DEVERR_CONTEXT_LEN and is skipped; when the others together have more rows
+ * than num_tokens (they overlap), it is set and none is computed.
  *   workspace         device, 256-byte aligned, at least
  *                     pa_prompt_attention_workspace_size(...) bytes
  */

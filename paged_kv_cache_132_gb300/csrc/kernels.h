@@ -235,7 +235,6 @@ struct PromptParams {
     int4* items;                  // (first row, length, pair of query tiles, 0) of each unit, longest sequences first
     int* num_units;               // units listed; an item is a unit and a KV head
     int* next_item;               // items taken beyond the first one of each CTA
-    int max_units;                // entries of the list
     int* err;
     unsigned long long wait_limit_ns;
 };

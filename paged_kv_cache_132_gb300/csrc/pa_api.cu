@@ -700,7 +700,6 @@ int pa_prompt_attention(void* out, const void* query, int64_t query_stride, cons
         p.num_units = reinterpret_cast<int*>(ws);
         p.next_item = p.num_units + 1;
         p.items = reinterpret_cast<int4*>(ws + pa::kPromptHeaderBytes);
-        p.max_units = (int)units;
     }
 
     CUtensorMap tmap_q, tmap_k, tmap_v;  // copies: later lookups may reuse a cache slot

@@ -23,8 +23,10 @@ __device__ inline int plan_bucket(int units) {
 // the units at their bucket's place, in any order inside a bucket).
 __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PromptParams p) {
     __shared__ int place[kPlanBuckets];
+    __shared__ unsigned long long rows;  // of all sequences
     const int lane = threadIdx.x & 31;
     if (threadIdx.x < kPlanBuckets) place[threadIdx.x] = 0;
+    if (threadIdx.x == 0) rows = 0;
     pdl_launch_dependents();
     pdl_wait_prerequisites();
     __syncthreads();
@@ -40,13 +42,27 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PromptP
         row0 = a;
         len = b - a;
     };
-    for (int s = threadIdx.x; s < p.num_seqs; s += kPlanThreads) {
+    unsigned long long warp_rows = 0;
+    for (int s0 = threadIdx.x - lane; s0 < p.num_seqs; s0 += kPlanThreads) {
         int row0, len;
-        sequence(s, row0, len);
+        sequence(s0 + lane, row0, len);
         const int units = (len + span - 1) / span;
         if (units) atomicAdd(&place[plan_bucket(units)], units);
+        // a warp's sum needs 36 bits: two of 21
+        warp_rows += __reduce_add_sync(0xffffffffu, (unsigned)len & 0xffffu) +
+                     ((unsigned long long)__reduce_add_sync(0xffffffffu, (unsigned)len >> 16) << 16);
     }
+    if (lane == 0 && warp_rows) atomicAdd(&rows, warp_rows);
     __syncthreads();
+    if (rows > (unsigned long long)p.num_tokens) {
+        // Sequences that overlap: the list need not have room for them.
+        if (threadIdx.x == 0) {
+            set_error(p.err, PA_DEVERR_CONTEXT_LEN);
+            *p.num_units = 0;
+            *p.next_item = 0;
+        }
+        return;
+    }
     if (threadIdx.x < 32) {
         // Places of the buckets, the largest first: lane l has buckets 127 - 4 l ... 124 - 4 l.
         int before[4], run = 0;
@@ -64,10 +80,8 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PromptP
 #pragma unroll
         for (int k = 0; k < 4; ++k) place[kPlanBuckets - 1 - 4 * lane - k] = incl - run + before[k];
         if (lane == 31) {
-            // More units than the list holds: start rows that overlap.
-            *p.num_units = incl < p.max_units ? incl : p.max_units;
+            *p.num_units = incl;  // <= max_units: the sequences' rows do not exceed num_tokens
             *p.next_item = 0;
-            if (incl > p.max_units) set_error(p.err, PA_DEVERR_CONTEXT_LEN);
         }
     }
     __syncthreads();
@@ -79,13 +93,13 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PromptP
         const int at = units ? atomicAdd(&place[plan_bucket(units)], units) : 0;
         if (units <= 4)
             for (int k = 0; k < units; ++k)
-                if (at + k < p.max_units) p.items[at + k] = make_int4(row0, len, units - 1 - k, 0);
+                p.items[at + k] = make_int4(row0, len, units - 1 - k, 0);
         for (unsigned wide = __ballot_sync(0xffffffffu, units > 4); wide; wide &= wide - 1) {
             const int src = __ffs(wide) - 1;
             const int w_row0 = __shfl_sync(0xffffffffu, row0, src), w_len = __shfl_sync(0xffffffffu, len, src);
             const int w_units = __shfl_sync(0xffffffffu, units, src), w_at = __shfl_sync(0xffffffffu, at, src);
             for (int k = lane; k < w_units; k += 32)
-                if (w_at + k < p.max_units) p.items[w_at + k] = make_int4(w_row0, w_len, w_units - 1 - k, 0);
+                p.items[w_at + k] = make_int4(w_row0, w_len, w_units - 1 - k, 0);
         }
     }
 }

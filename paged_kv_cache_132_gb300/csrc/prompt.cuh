@@ -280,9 +280,22 @@ __device__ void prompt_load(const PromptParams& p, typename Shape::Smem& sm, int
     if (p.items) {
         next = listed(blockIdx.x);
     } else {
+        // Sequences that overlap make more items than the grid has CTAs: none is
+        // computed, as with a list.
         PromptWalk walk{};
-        prompt_walk_load(p, walk, lane);
-        next = prompt_walk_to(p, walk, lane, blockIdx.x);
+        long long rows = 0;
+        for (walk.base = 0; walk.base < p.num_seqs; walk.base += 32) {
+            prompt_walk_load(p, walk, lane);
+            rows += __reduce_add_sync(kFullMask, walk.len);  // at most 32 * 2^15: few rows without a list
+        }
+        if (rows > p.num_tokens) {
+            set_error(p.err, PA_DEVERR_CONTEXT_LEN);
+            next = make_int4(0, 0, 0, 0);
+        } else {
+            walk.base = 0;
+            prompt_walk_load(p, walk, lane);
+            next = prompt_walk_to(p, walk, lane, blockIdx.x);
+        }
     }
     for (int n = 0;; ++n) {
         const int4 it = next;
@@ -634,7 +647,7 @@ __device__ void prompt_softmax(const PromptParams& p, typename Shape::Smem& sm, 
             }
             // P in four pieces of 32 positions; P.V starts on the first half
             // while the second is made.
-            const float nm = -m;
+            const float nm = m > NEG_INF ? -m : 0.f;  // no weight for scores of -inf alone
             float ps[4] = {0.f, 0.f, 0.f, 0.f};
             auto piece = [&](float* x, uint32_t addr) {
                 uint32_t u[16];

@@ -178,17 +178,19 @@ def test_non_finite_values_reach_what_attends_them():
 
 
 def test_bad_start_rows_are_reported():
-    """Start rows out of order or out of range: the sequences they spoil are
-    skipped, the others computed."""
+    """Start rows out of range: the sequences they spoil are skipped, the others
+    computed.  Out of order, so that sequences overlap: none is."""
     q, k, v = rows(300, 4, 2, 64, torch.float16, 13)
-    loc = torch.tensor([0, 90, 50, 300, 301], dtype=torch.int32, device="cuda")
+    loc = torch.tensor([0, 90, 90, 300, 301], dtype=torch.int32, device="cuda")
     out = torch.full_like(q, 7.0)
     api.prompt_attention(q, k, v, loc, 0.125, out=out)
     assert api.get_device_error() == (-5, native.DEVERR_CONTEXT_LEN)
-    # rows 50 .. 89 belong to two sequences here: either may write them last
-    check(q[:50], k[:50], v[:50], [50], 0.125, out[:50])
-    ref, tol = exact(q[50:], k[50:], v[50:], 0.125)
-    assert float(((out[90:].double() - ref[40:]).abs() - tol[40:]).max()) <= 0
+    check(q, k, v, [90, 210], 0.125, out)
+    loc = torch.tensor([0, 90, 50, 300], dtype=torch.int32, device="cuda")
+    out.fill_(7.0)
+    api.prompt_attention(q, k, v, loc, 0.125, out=out)
+    assert api.get_device_error() == (-5, native.DEVERR_CONTEXT_LEN)
+    assert bool((out == 7).all())
     loc = torch.tensor([-3, 100], dtype=torch.int32, device="cuda")
     out.fill_(7.0)
     api.prompt_attention(q, k, v, loc, 0.125, out=out)
@@ -263,6 +265,21 @@ def test_overlapping_start_rows_stay_inside_the_workspace(h, hkv):
     loc = torch.tensor([0, n] * 20, dtype=torch.int32, device="cuda")
     need = api.prompt_attention_workspace_size(39, n, h, hkv)
     room = torch.full((need + 4096,), 0x5a, dtype=torch.uint8, device="cuda")
-    api.prompt_attention(q, k, v, loc, 0.1, workspace=room[:need])
+    out = torch.full_like(q, 7.0)
+    api.prompt_attention(q, k, v, loc, 0.1, workspace=room[:need], out=out)
     assert api.get_device_error() == (-5, native.DEVERR_CONTEXT_LEN)
-    assert bool((room[need:] == 0x5a).all())
+    assert bool((room[need:] == 0x5a).all()) and bool((out == 7).all())
+
+
+def test_scores_of_minus_infinity_have_no_weight():
+    """A whole tile of keys whose scores overflow to -inf: weight 0, whatever comes later."""
+    n, d = 300, 64
+    q, k, v = rows(n, 2, 2, d, torch.bfloat16, 19)
+    q = q.abs() + 1
+    k2 = k.clone()
+    k2[:140] = -3e38
+    out = api.prompt_attention(q, k2, v, starts([n]), d ** -0.5)
+    assert api.get_device_error() == (0, 0)
+    ref, tol = exact(q[140:], k[140:], v[140:], d ** -0.5)
+    assert bool(out[:140].isnan().all())  # nothing but such scores
+    assert float(((out[140:].double() - ref).abs() - tol).max()) <= 0
