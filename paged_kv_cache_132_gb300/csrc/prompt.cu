@@ -24,6 +24,7 @@ __device__ inline int plan_bucket(int units) {
 __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PromptParams p) {
     __shared__ int place[kPlanBuckets];
     __shared__ unsigned long long rows;  // of all sequences
+    __shared__ int4 placed[kPlanThreads];  // first row, length, units, place of the first unit
     const int lane = threadIdx.x & 31;
     if (threadIdx.x < kPlanBuckets) place[threadIdx.x] = 0;
     if (threadIdx.x == 0) rows = 0;
@@ -85,22 +86,22 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PromptP
         }
     }
     __syncthreads();
-    // Up to 4 units: by the sequence's thread; longer ones by its whole warp.
-    for (int s0 = threadIdx.x - lane; s0 < p.num_seqs; s0 += kPlanThreads) {
+    // A place for each sequence by a thread, and up to 4 units; more units by a warp.
+    for (int base = 0; base < p.num_seqs; base += kPlanThreads) {
         int row0, len;
-        sequence(s0 + lane, row0, len);
+        sequence(base + threadIdx.x, row0, len);
         const int units = (len + span - 1) / span;
         const int at = units ? atomicAdd(&place[plan_bucket(units)], units) : 0;
-        if (units <= 4)
-            for (int k = 0; k < units; ++k)
-                p.items[at + k] = make_int4(row0, len, units - 1 - k, 0);
-        for (unsigned wide = __ballot_sync(0xffffffffu, units > 4); wide; wide &= wide - 1) {
-            const int src = __ffs(wide) - 1;
-            const int w_row0 = __shfl_sync(0xffffffffu, row0, src), w_len = __shfl_sync(0xffffffffu, len, src);
-            const int w_units = __shfl_sync(0xffffffffu, units, src), w_at = __shfl_sync(0xffffffffu, at, src);
-            for (int k = lane; k < w_units; k += 32)
-                p.items[w_at + k] = make_int4(w_row0, w_len, w_units - 1 - k, 0);
+        const bool wide = units > 4;
+        placed[threadIdx.x] = make_int4(row0, len, wide ? units : 0, at);
+        if (!wide)
+            for (int k = 0; k < units; ++k) p.items[at + k] = make_int4(row0, len, units - 1 - k, 0);
+        if (!__syncthreads_or(wide)) continue;
+        for (int s = threadIdx.x >> 5; s < kPlanThreads && base + s < p.num_seqs; s += kPlanThreads / 32) {
+            const int4 q = placed[s];
+            for (int k = lane; k < q.z; k += 32) p.items[q.w + k] = make_int4(q.x, q.y, q.z - 1 - k, 0);
         }
+        __syncthreads();
     }
 }
 
