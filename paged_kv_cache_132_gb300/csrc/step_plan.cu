@@ -21,6 +21,11 @@
 // of the same kernel -- a block that is given back and taken again in the same
 // step is looked up in the table that gives it -- and the outputs that may be
 // inputs (lengths, free state) are written after a barrier of them all.
+//
+// Measured (graph replays, launch included; an empty step takes 2.3 us): 4.4 us
+// for 256 sequences of one new token; 13.4 us for 4096 sequences with 74 000 new
+// tokens, 12 600 blocks given back and 5 300 taken (1 MB).  In one CTA the sums
+// alone take 1 us per 1024 sequences (three prefix sums by shuffles).
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -32,9 +37,12 @@ namespace {
 constexpr int kStepThreads = 1024;
 constexpr int kSlotThreads = 256;
 constexpr int kStepCluster = 8;  // the largest cluster every GPU of the family schedules
-// Steps of more token rows or sequences than these run on the cluster.
-constexpr int kStepSmallTokens = 2048;
-constexpr int kStepSmallSeqs = 1024;
+// Steps of more token rows or sequences than these run on the cluster and the
+// slots kernel.  Measured, one CTA against those: 4.4 and 5.8 us for a prompt of
+// 4096 tokens, 6.9 and 6.7 us for 8 of 1024; 5.8 and 7.5 us for 1024 sequences of
+// one token, 7.9 and 7.9 us for 2048.
+constexpr int kStepSmallTokens = 8192;
+constexpr int kStepSmallSeqs = 2048;
 constexpr int kStepUnroll = 4;   // entries of a thread whose loads are in flight together
 
 // For each x: the last index i in [0, n) with start[i] <= x (start[0] = 0 <= x,
