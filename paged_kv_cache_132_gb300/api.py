@@ -238,7 +238,7 @@ def _token_stride(t: torch.Tensor, name: str) -> int:
     """Elements from one token's row of heads to the next; the heads of a token are contiguous."""
     tokens, heads, d = t.shape
     by_token, by_head, by_elem = t.stride()
-    if by_elem == 1 and by_head == d and by_token >= heads * d:
+    if tokens > 1 and by_elem == 1 and by_head == d and by_token >= heads * d:
         return by_token
     if (by_elem != 1 and d > 1) or (by_head != d and heads > 1):
         raise ValueError(f"{name}: the heads of a token must be contiguous")

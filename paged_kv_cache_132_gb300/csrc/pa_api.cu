@@ -652,7 +652,8 @@ int pa_prompt_attention(void* out, const void* query, int64_t query_stride, cons
                         float scale, void* workspace, size_t workspace_bytes, void* stream) {
     NvtxRange range("pa_prompt_attention");
     if (elem_bytes(dtype) == 0 || num_seqs < 0 || num_tokens < 0 || num_heads <= 0 || num_kv_heads <= 0 ||
-        num_heads % num_kv_heads != 0 || head_dim <= 0 || !std::isfinite(scale) || !(scale > 0.f))
+        num_heads % num_kv_heads != 0 || head_dim <= 0 || !(scale > 0.f) ||
+        !std::isfinite(scale * 1.4426950408889634f))
         return PA_ERR_INVALID_ARG;
     const int64_t q_row = (int64_t)num_heads * head_dim, kv_row = (int64_t)num_kv_heads * head_dim;
     if (query_stride < q_row || key_stride < kv_row || value_stride < kv_row || query_stride % head_dim != 0 ||

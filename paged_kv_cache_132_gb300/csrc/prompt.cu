@@ -35,7 +35,7 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PromptP
     auto sequence = [&](int s, int& row0, int& len) {
         row0 = len = 0;
         if (s >= p.num_seqs) return;
-        const int a = __ldg(p.query_start + s), b = __ldg(p.query_start + s + 1);
+        const int a = __ldcg(p.query_start + s), b = __ldcg(p.query_start + s + 1);
         if (a < 0 || b < a || b > p.num_tokens) {
             set_error(p.err, PA_DEVERR_CONTEXT_LEN);
             return;

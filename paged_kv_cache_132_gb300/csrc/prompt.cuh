@@ -35,15 +35,16 @@
 // Values a query must not see: a row's weights after its own position are 0,
 // but 0 * NaN is NaN on the tensor cores.  So before P.V reads a V tile that
 // holds positions some row of the item does not attend (the last one or two of
-// an item), two warps clear its rows after the item's last position and
-// replace non-finite elements by 0; those are added again, to the rows that do
+// an item), a warp clears its rows after the item's last position and
+// replaces non-finite elements by 0; those are added again, to the rows that do
 // attend them, by the output warps (an infinite or NaN term decides a sum
 // whatever its weight is).  Keys need no such care: masked scores are replaced.
 //
 // Warp roles (512 threads, registers moved between the groups by setmaxnreg):
-//   warp 0           MMA issuer, owner of the TMEM allocation
-//   warp 1           work items, Q, K and V copies (TMA)
-//   warps 2, 3       the V tiles with masked positions (above)
+//   warps 0, 1       MMA issuers of query tile 0 / 1 (warp 0 owns the TMEM
+//                    allocation)
+//   warp 2           work items, Q, K and V copies (TMA)
+//   warp 3           the V tiles with masked positions (above)
 //   warps 4-7, 8-11  softmax of query tile 0 / 1
 //   warps 12-15      outputs: O_i / row sum, rounded once, written to memory
 // Every wait is bounded; a wait that runs out sets PA_DEVERR_TIMEOUT and makes
@@ -76,7 +77,7 @@ struct PromptShape {
     static constexpr int SOFTMAX_WARP = 4;       // first of eight
     static constexpr int OUT_WARP = 12;          // first of four
     static constexpr int THREADS = 512;
-    static constexpr int ITEM_READERS = 8 + 4 + 2 + 1;  // softmax, output, MMA and check warps
+    static constexpr int ITEM_READERS = 8 + 4 + 2 + 1;  // softmax, output, MMA, check warps
     // Registers per thread after the split: 256 * 176 + 128 * 64 + 128 * 96
     // = 512 * 128, the launch's total.
     static constexpr int REGS_SOFTMAX = 176, REGS_OUT = 64, REGS_OTHER = 96;
@@ -99,7 +100,7 @@ struct PromptShape {
         uint64_t kv_full[NSLOT];    // tile landed
         uint64_t kv_empty[NSLOT];   // the MMAs of both query tiles that read it complete
         uint64_t check_go[NSLOT];   // the copy of a V tile with masked positions was issued (load warp)
-        uint64_t v_checked[NSLOT];  // ... and the tile is fit for P.V (check warps)
+        uint64_t v_checked[NSLOT];  // ... and the tile is fit for P.V (check warp)
         uint64_t s_full[2];         // S_i complete
         uint64_t p_full[2][2];      // each half of P_i written (softmax warps)
         uint64_t o_full[2];         // last P_i V_j of the item complete
@@ -231,7 +232,7 @@ __device__ __forceinline__ void prompt_walk_load(const PromptParams& p, PromptWa
     const int s = k.base + lane;
     k.row0 = k.len = 0;
     if (s < p.num_seqs) {
-        const int a = __ldg(p.query_start + s), b = __ldg(p.query_start + s + 1);
+        const int a = __ldcg(p.query_start + s), b = __ldcg(p.query_start + s + 1);
         if (a < 0 || b < a || b > p.num_tokens) {
             set_error(p.err, PA_DEVERR_CONTEXT_LEN);
         } else {
@@ -273,13 +274,13 @@ __device__ void prompt_load(const PromptParams& p, typename Shape::Smem& sm, int
     const uint32_t q_bytes = (uint32_t)(Shape::SLABS * p.tile_tokens * p.group * 128);
     uint32_t q_used = 0, q_loaded = 0;  // bit i: parity of the loads of Q_i, whether there was one
     uint32_t slot = 0, round = 0, filled = 0;
-    const int total = p.items ? __ldg(p.num_units) * p.num_kv_heads : 0;
+    const int total = p.items ? __ldcg(p.num_units) * p.num_kv_heads : 0;
     bool ok = true;
     auto listed = [&](int index) {
         int4 e = make_int4(0, 0, 0, 0);
         if (index < total) {
             const int unit = index / p.num_kv_heads;
-            e = __ldg(p.items + unit);
+            e = __ldcg(p.items + unit);  // not through L1: written after this grid was launched
             e.w = index - unit * p.num_kv_heads;
         }
         return e;
@@ -381,7 +382,7 @@ __device__ void prompt_load(const PromptParams& p, typename Shape::Smem& sm, int
 }
 
 // ---------------------------------------------------------------------------
-// MMA issuer (one warp)
+// MMA issuer of query tile i (one warp)
 // ---------------------------------------------------------------------------
 // The whole warp runs the issue loop and one elected lane issues: descriptors
 // then stay in uniform registers.  With the loop inside `if (lane == 0)` every
@@ -695,7 +696,7 @@ __device__ void prompt_softmax(const PromptParams& p, typename Shape::Smem& sm, 
 }
 
 // ---------------------------------------------------------------------------
-// check warps: V tiles with masked positions
+// check warp: V tiles with masked positions
 // ---------------------------------------------------------------------------
 // Not 0 where a 16-bit half of w is infinite or NaN: an exponent of all ones
 // carries into the half's sign bit.
@@ -777,7 +778,7 @@ __device__ void prompt_check(const PromptParams& p, typename Shape::Smem& sm, in
 // ---------------------------------------------------------------------------
 // output warps
 // ---------------------------------------------------------------------------
-// The non-finite values that the check warps took out of V tiles: each decides
+// The non-finite values that the check warp took out of V tiles: each decides
 // its column of the rows that attend it.  Added to the stored output `dst` of
 // the row of `token` by the thread that stored it.
 template <typename T, int D>
@@ -895,6 +896,7 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
         sm.last_dirty = -1;
         fence_mbar_init();
     }
+    __syncwarp();  // the allocation is one instruction of the whole warp
     if (warp == Shape::MMA_WARP) tmem_alloc(&sm.tmem_base, Shape::TMEM_COLS);
     tc_fence_before_sync();
     __syncthreads();
@@ -924,6 +926,7 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
     __syncthreads();
     tc_fence_after_sync();
     if (threadIdx.x == 0 && sm.abort_flag) set_error(p.err, PA_DEVERR_TIMEOUT);
+    __syncwarp();
     if (warp == Shape::MMA_WARP) tmem_dealloc(tmem, Shape::TMEM_COLS);
 }
 

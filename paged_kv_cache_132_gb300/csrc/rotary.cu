@@ -82,8 +82,10 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const RotaryPara
             if (has1) x[u][1] = __ldcs(src + chunk1);
         }
     };
-    const int pos = __ldg(p.positions + token);
-    const int64_t slot = __ldg(p.slot_mapping + token);
+    // Not through the read-only path: the kernel before may have written them
+    // after this grid was launched.
+    const int pos = __ldcg(p.positions + token);
+    const int64_t slot = __ldcg(p.slot_mapping + token);
     load(row0);
     if (pos < 0) return;  // a padding row
     if (pos >= p.num_positions) {
@@ -100,7 +102,7 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const RotaryPara
         const float4* row = reinterpret_cast<const float4*>(p.cos_sin + (int64_t)pos * p.rotary_dim + c * V);
 #pragma unroll
         for (int i = 0; i < V / 4; ++i) {
-            const float4 a = __ldg(row + i), b = __ldg(row + p.rotary_dim / 8 + i);
+            const float4 a = row[i], b = row[p.rotary_dim / 8 + i];
             cs[4 * i] = a.x, cs[4 * i + 1] = a.y, cs[4 * i + 2] = a.z, cs[4 * i + 3] = a.w;
             sn[4 * i] = b.x, sn[4 * i + 1] = b.y, sn[4 * i + 2] = b.z, sn[4 * i + 3] = b.w;
         }

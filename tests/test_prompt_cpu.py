@@ -35,6 +35,7 @@ def _call(lib, **over):
     (dict(scale=-1.0), -1),
     (dict(scale=float("nan")), -1),
     (dict(scale=float("inf")), -1),
+    (dict(scale=3e38), -1),             # in base-2 units infinite
     (dict(qs=192), -1),                 # shorter than a row
     (dict(ks=64), -1),
     (dict(vs=0), -1),

@@ -231,6 +231,40 @@ def test_another_stream_and_two_calls_at_once():
         check(*b, [600], 0.1, y)
 
 
+def test_one_token_of_a_wider_array():
+    """The stride of a single row does not matter."""
+    wide = torch.randn(3, 4 * 64 + 8, device="cuda").half()[1:2, :256]
+    q, k, v = wide.unflatten(1, (4, 64)), wide[:, :128].unflatten(1, (2, 64)), wide[:, 128:].unflatten(1, (2, 64))
+    out = api.prompt_attention(q, k, v, starts([1]), 0.125)
+    assert api.get_device_error() == (0, 0)
+    assert torch.equal(out, v.repeat_interleave(2, 1))
+
+
+def test_two_graphs_share_a_workspace():
+    """Replayed one after the other: each call resets what it needs."""
+    a, b = rows(700, 32, 8, 64, torch.bfloat16, 20), rows(900, 32, 8, 64, torch.bfloat16, 21)
+    la, lb = starts([300, 400]), starts([50] * 18)
+    size = max(api.prompt_attention_workspace_size(n, t, 32, 8) for n, t in ((2, 700), (18, 900)))
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    oa, ob = torch.empty_like(a[0]), torch.empty_like(b[0])
+    graphs = []
+    for x, loc, o in ((a, la, oa), (b, lb, ob)):
+        api.prompt_attention(*x, loc, 0.125, out=o, workspace=ws)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            api.prompt_attention(*x, loc, 0.125, out=o, workspace=ws)
+        graphs.append(g)
+    for _ in range(3):
+        oa.zero_(), ob.zero_()
+        for g in graphs + graphs[::-1]:
+            g.replay()
+        torch.cuda.synchronize()
+        check(*a, [300, 400], 0.125, oa)
+        check(*b, [50] * 18, 0.125, ob)
+    assert api.get_device_error() == (0, 0)
+
+
 def test_refusals():
     q, k, v = rows(20, 4, 2, 64, torch.float16, 17)
     loc = starts([20])
