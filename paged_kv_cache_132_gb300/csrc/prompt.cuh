@@ -349,7 +349,7 @@ __device__ void prompt_load(const PromptParams& p, typename Shape::Smem& sm, int
         const int st = n % Shape::NITEM;
         // The next item's number and entry arrive while this one's copies are
         // issued and waited for: 3000 cycles an item when they did not.
-        const int taken = take_item(lane == 0 ? p.next_item : nullptr);
+        int taken = 0;
         prompt_wait(p, sm, &sm.item_empty[st], ((uint32_t)(n / Shape::NITEM) & 1u) ^ 1u);
         if (__any_sync(kFullMask, prompt_aborted(&sm.abort_flag))) break;
         if (elect_one()) {
@@ -369,6 +369,7 @@ __device__ void prompt_load(const PromptParams& p, typename Shape::Smem& sm, int
             prompt_wait(p, sm, &sm.kv_empty[slot], round ^ 1u);
             ok = !__any_sync(kFullMask, prompt_aborted(&sm.abort_flag));
             if (!ok) break;
+            if (t == 2 * nt - 2) taken = take_item(lane == 0 ? p.next_item : nullptr);
             const int halves = end - j * Shape::BN > Shape::HALF ? 2 : 1;
             const CUtensorMap* map = is_v ? tv : tk;
             if (elect_one()) {
@@ -402,7 +403,7 @@ __device__ void prompt_load(const PromptParams& p, typename Shape::Smem& sm, int
                 q_used ^= 1u << t;
                 q_loaded |= 1u << t;
             }
-            if (t == 1) next = listed((int)gridDim.x + __shfl_sync(kFullMask, taken, 0));
+            if (t == 2 * nt - 1) next = listed((int)gridDim.x + __shfl_sync(kFullMask, taken, 0));
         }
         if (!ok) break;
     }
