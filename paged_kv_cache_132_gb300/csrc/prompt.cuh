@@ -29,8 +29,9 @@
 // 1600: 128 exponentials a thread at 4.3 cycles, the scores' load, the maximum;
 // then P V and S 1040 and their latency).  Measured: 1.65 PFLOP/s (0.87 of
 // the cuBLAS burst rate, 0.95 of the sustained one) for 32768 tokens of 32 heads
-// of 128, where power sets the clock; 1.04 PFLOP/s for 32 prompts of 128-1024
-// tokens (122 us), where an item is 3.5 steps and starting it costs another.
+// of 128, where power sets the clock; 1.02-1.11 PFLOP/s for 32 prompts of
+// 128-1024 tokens (114-125 us, by the clock), where an item is 3.5 steps and
+// starting it costs a third of one.
 //
 // Values a query must not see: a row's weights after its own position are 0,
 // but 0 * NaN is NaN on the tensor cores.  So before P.V reads a V tile that
