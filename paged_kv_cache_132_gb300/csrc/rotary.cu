@@ -17,7 +17,7 @@
 // rows are loaded before the position is known.
 //
 // Measured: 85.0 us for 20 588 bf16 tokens of 32 + 2 * 8 heads of 128 with the
-// keys kept (559 MB: 6.6 TB/s, 0.97 of the copy bandwidth) with 64 threads a
+// keys kept (559 MB: 6.6 TB/s, 0.98 of the copy bandwidth) with 64 threads a
 // token, 108.5 us with 256; 2.9 us for 256 tokens (6.4 MB) with 256 threads,
 // 3.5 us with 64.
 #include "attn_common.cuh"
