@@ -122,6 +122,16 @@ __device__ inline void bulk_copy_g2s(void* smem_dst, const void* gmem_src, uint3
 // Programmatic dependent launch: let the next kernel in the stream start
 // launching, and (in that kernel) wait until the previous one has completed
 // and its memory is visible.  Without the launch attribute both are no-ops.
+//
+// What a kernel may do before its own wait depends on where the kernels before it
+// signal, since a signal reaches on through a chain of kernels that all start
+// early.  The rule, which the decode planning kernel (it reads the context
+// lengths before its wait) and the read-only loads of lengths and tables rely on:
+//   - nothing is written before the wait: any buffer may be memory that the
+//     kernel before is still using;
+//   - a kernel signals after its own wait (or was launched without the attribute),
+//     unless the kernel that follows it belongs to the same call and waits first;
+//   - a kernel that writes lengths, start rows or tables does not signal at all.
 __device__ inline void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ inline void pdl_wait_prerequisites() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 

@@ -68,10 +68,7 @@ __global__ void __launch_bounds__(kPlanThreads) decode_plan_kernel(const __grid_
     // before it reads the work list.
     pdl_launch_dependents();
     const int tid = threadIdx.x;
-    if (tid == 0) {
-        carry[0] = carry[1] = 0;
-        *p.next_item = 0;
-    }
+    if (tid == 0) carry[0] = carry[1] = 0;
     __syncthreads();
     for (int base = 0; base < p.num_seqs; base += kPlanThreads) {
         const int s = base + tid;
@@ -87,6 +84,15 @@ __global__ void __launch_bounds__(kPlanThreads) decode_plan_kernel(const __grid_
         const int multi = np > 1 ? 1 : 0;
         const int items_incl = block_inclusive_scan(np, scratch);
         const int multi_incl = block_inclusive_scan(multi, scratch);
+        if (base == 0) {
+            // The lengths and their sums so far overlapped with the previous kernel in
+            // the stream: no kernel that writes lengths lets its dependents start
+            // before they are written (pdl_launch_dependents).  The workspace may be
+            // memory that that kernel still reads or writes, so nothing is written
+            // before it has completed; the decode kernel's wait on this one covers both.
+            pdl_wait_prerequisites();
+            if (tid == 0) *p.next_item = 0;
+        }
         const int first = carry[0] + items_incl - np;
         for (int k = 0; k < np; ++k) p.items[first + k] = make_int2(s, k);
         if (multi) p.multi_seqs[carry[1] + multi_incl - 1] = make_int2(s, np);
@@ -101,10 +107,6 @@ __global__ void __launch_bounds__(kPlanThreads) decode_plan_kernel(const __grid_
         *p.num_items = carry[0] * p.num_kv_heads;
         *p.num_multi = carry[1];
     }
-    // This kernel may have been launched before the previous kernel in the
-    // stream finished (it reads nothing that kernel writes); it completes only
-    // after that kernel has, so the decode kernel's wait on it covers both.
-    pdl_wait_prerequisites();
 }
 
 template <int D>
@@ -279,7 +281,7 @@ cudaError_t launch_decode(const DecodeParams& p, int dtype, int head_dim, int bl
     cudaError_t e = cudaSuccess;
     if (p.direct_items == 0) {
         // The planning kernel may overlap the previous kernel in the stream (it
-        // waits for it before completing).
+        // waits for it before it writes anything).
         cudaLaunchConfig_t cfg{};
         cfg.gridDim = dim3(1);
         cfg.blockDim = dim3(kPlanThreads);

@@ -51,8 +51,10 @@ __device__ inline uint4 pack_chunk(const float* x) {
 template <typename T, bool INTERLEAVED>
 __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const RotaryParams p) {
     constexpr int V = 16 / sizeof(T);  // elements of a chunk, and pairs of a lane
-    pdl_launch_dependents();           // the attention's planning kernel, as after the plain cache write
     pdl_wait_prerequisites();
+    // The attention's planning kernel, as after the plain cache write.  Not before
+    // the wait: the plan of the step may be what comes before.
+    pdl_launch_dependents();
     const int64_t token = blockIdx.x;
     const int rows_per_pass = blockDim.x / p.lanes;
     const int row0 = threadIdx.x / p.lanes;

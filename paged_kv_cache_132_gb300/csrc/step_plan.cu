@@ -126,7 +126,9 @@ __global__ void __launch_bounds__(kStepThreads) step_plan_kernel(const StepPlanP
     int* token_start = starts;
     int* given_start = starts + p.num_seqs;
     int* taken_start = starts + 2 * p.num_seqs;
-    pdl_launch_dependents();
+    // Only for the slots kernel of the same call: any other kernel starts when the
+    // lengths and tables are written.
+    if (LARGE && p.max_tokens > 0) pdl_launch_dependents();
     pdl_wait_prerequisites();
 
     // The sums, EACH sequences of a thread at a time; the next ones load meanwhile.
@@ -315,7 +317,6 @@ __global__ void __launch_bounds__(kStepThreads) step_plan_kernel(const StepPlanP
 // tables.  The start rows are searched in shared memory.
 __global__ void __launch_bounds__(kSlotThreads) step_slots_kernel(const StepPlanParams p) {
     extern __shared__ int starts[];
-    pdl_launch_dependents();
     pdl_wait_prerequisites();
     const int64_t base = (int64_t)blockIdx.x * (kSlotThreads * kStepUnroll) + threadIdx.x;
     const int tokens = p.query_start_loc[p.num_seqs];
