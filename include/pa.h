@@ -110,8 +110,9 @@ typedef enum {
  *   PA_OPT_DECODE_KERNEL (env PA_DECODE_KERNEL=simt -> 1): decode kernel for
  *     16-bit pools: 0 = tensor-core consumer (default), 1 = CUDA-core one.
  *   PA_OPT_DROP_FIRST_FILL (env PA_DEBUG_DROP_FIRST_FILL=1): test hook of the
- *     bounded waits -- every decode CTA leaves its first pipeline stage
- *     unfilled, its wait runs out and the call reports PA_DEVERR_TIMEOUT.
+ *     bounded waits -- the first pipeline stage of every CTA of pa_decode and
+ *     pa_prompt_attention never becomes full, the wait for it runs out and the
+ *     call reports PA_DEVERR_TIMEOUT.
  */
 typedef enum { PA_OPT_DEBUG_CHECKS = 0, PA_OPT_DECODE_KERNEL = 1, PA_OPT_DROP_FIRST_FILL = 2 } pa_option;
 

@@ -145,9 +145,11 @@ struct DecodeParams {
     int direct_items;
 };
 
-// Test hook (environment variable PA_DEBUG_DROP_FIRST_FILL=1): every decode
-// CTA leaves its first pipeline stage unfilled, so that its consumers' bounded
-// wait runs out and the call reports PA_DEVERR_TIMEOUT.
+// Test hook (environment variable PA_DEBUG_DROP_FIRST_FILL=1): the first pipeline
+// stage of every CTA of the decode and prompt attention kernels never becomes full
+// (decode: its copies are left out; prompt: its barrier expects one arrival too
+// many), so that the bounded wait for it runs out and the call reports
+// PA_DEVERR_TIMEOUT.
 constexpr int kDebugDropFirstFill = 1;
 
 struct DecodeWorkspaceLayout {
@@ -237,6 +239,7 @@ struct PromptParams {
     int* next_item;               // items taken beyond the first one of each CTA
     int* err;
     unsigned long long wait_limit_ns;
+    int debug_flags;              // kDebugDropFirstFill
 };
 
 // Units (pairs of query tiles of a sequence) of a call, at most: every sequence

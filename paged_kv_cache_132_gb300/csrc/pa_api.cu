@@ -690,6 +690,7 @@ int pa_prompt_attention(void* out, const void* query, int64_t query_stride, cons
     p.scale_log2 = scale * 1.4426950408889634f;
     p.err = err;
     p.wait_limit_ns = wait_limit_ns();
+    p.debug_flags = option(PA_OPT_DROP_FIRST_FILL) ? pa::kDebugDropFirstFill : 0;
     if (!aligned(workspace, 256) ||
         workspace_bytes < pa_prompt_attention_workspace_size(num_seqs, num_tokens, num_heads, num_kv_heads))
         return PA_ERR_WORKSPACE;

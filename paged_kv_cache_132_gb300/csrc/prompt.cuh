@@ -136,10 +136,10 @@ __device__ __forceinline__ bool prompt_aborted(int* abort_flag) { return *reinte
 
 // Waits for a phase of a barrier.  When the limit runs out, here or in another
 // role, every wait of the CTA ends: the roles run on to the end of their item
-// without data (nothing they write leaves their buffers; the load warp issues
-// nothing more) and then leave, and the CTA reports PA_DEVERR_TIMEOUT.  Kept
-// short: it is inlined in some twenty places, and the roles' code competes for
-// the instruction caches.
+// without data (in shared and tensor memory only: the output warps store nothing
+// any more, the load warp issues nothing more) and then leave, and the CTA reports
+// PA_DEVERR_TIMEOUT.  Kept short: it is inlined in some twenty places, and the
+// roles' code competes for the instruction caches.
 template <class Smem>
 __device__ __forceinline__ void prompt_wait(const PromptParams& p, Smem& sm, uint64_t* bar, uint32_t parity) {
     if (mbar_try_wait(bar, parity)) return;
@@ -855,10 +855,12 @@ __device__ void prompt_output(const PromptParams& p, typename Shape::Smem& sm, u
             prompt_wait(p, sm, &sm.o_full[i], (parity >> i) & 1u);
             parity ^= 1u << i;
             tc_fence_after_sync();
+            // A wait that ran out left no result: the rows stay as they were.
+            const bool aborted = prompt_aborted(&sm.abort_flag);
             const float l = sm.row_sum[i][r];
             const float inv = 1.f / l;  // l > 0: every row attends its own position (NaN stays NaN)
             const int token = w.t0 + i * p.tile_tokens + t;
-            const bool store = t < p.tile_tokens && token < w.len;
+            const bool store = t < p.tile_tokens && token < w.len && !aborted;
             const bool dirty = *reinterpret_cast<volatile int*>(&sm.last_dirty) >= n - 1;
             T* dst = static_cast<T*>(p.out) +
                      ((int64_t)(w.row0 + token) * p.num_heads + (int64_t)w.kv_head * p.group + g) * D;
@@ -911,7 +913,7 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
             mbar_init(&sm.item_empty[s], Shape::ITEM_READERS);
         }
         for (int s = 0; s < Shape::NSLOT; ++s) {
-            mbar_init(&sm.kv_full[s], 1);
+            mbar_init(&sm.kv_full[s], s == 0 && (p.debug_flags & kDebugDropFirstFill) ? 2 : 1);
             mbar_init(&sm.kv_empty[s], 2);
             mbar_init(&sm.check_go[s], 1);
             mbar_init(&sm.v_checked[s], 1);
