@@ -19,7 +19,12 @@
 // only when a row's maximum grows by more than 8 (a factor of 256), and row
 // sums in binary32 over the unrounded weights.  The rounding of P to 16 bits
 // costs as much as the rounding of the output that follows it (half a step of
-// the type on independent weights), and lets P.V run at the 16-bit rate.
+// the type on independent weights), and lets P.V run at the 16-bit rate.  In f16
+// all weights of a row are 2^7 larger (2^8 by the delayed rescaling, 2^15 in all:
+// half of the type's range), which the division by their sum takes out again, so
+// that a weight loses bits below 2^-21 of the row's largest and rounds to 0 below
+// 2^-32; without, below 2^-14 and 2^-25, and the many small weights of a long row
+// were missing from its output.  bf16 has the range of binary32.
 //
 // Bound: tensor cores (4 d flops per row and position).  The two query tiles
 // alternate on them: while one's softmax runs, the MMAs of the other (P V_j, then
@@ -691,7 +696,8 @@ __device__ void prompt_softmax(const PromptParams& p, typename Shape::Smem& sm, 
             }
             // P in four pieces of 32 positions; P.V starts on the first half
             // while the second is made.
-            const float nm = m > NEG_INF ? -m : 0.f;  // no weight for scores of -inf alone
+            constexpr float LARGER = std::is_same<T, __half>::value ? 7.f : 0.f;
+            const float nm = m > NEG_INF ? LARGER - m : 0.f;  // no weight for scores of -inf alone
             float ps[4] = {0.f, 0.f, 0.f, 0.f};
             auto piece = [&](float* x, uint32_t addr) {
                 uint32_t u[16];
