@@ -115,6 +115,18 @@ __device__ inline void mma_commit(uint64_t* bar) {
 // ---------------------------------------------------------------------------
 // TMEM <-> registers (a warp reads its own quarter of the 128 lanes)
 // ---------------------------------------------------------------------------
+// 16, 32 and 64 consecutive 32-bit columns of this thread's TMEM lane (32x32b
+// shape), waited for inside the same statement so that no use of the registers can
+// be scheduled before the data has arrived.
+__device__ inline void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+
 // 32 consecutive 32-bit columns of this thread's TMEM lane (32x32b shape),
 // waited for inside the same statement so that no use of the registers can be
 // scheduled before the data has arrived.

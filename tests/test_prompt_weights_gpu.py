@@ -47,3 +47,25 @@ def test_one_large_score_among_many_small_ones(h, hkv, d, gap, where):
 def test_random_scores(spread):
     q, k, v = rows(3000, 4, 2, 64, torch.float16, 31)
     check(q, k, v.abs(), spread * 0.125)
+
+
+def test_largest_values():
+    """Weights of 2^15 and values at the type's end: the sums stay in binary32."""
+    q, k, v = rows(700, 4, 4, 64, torch.float16, 32)
+    check(q, k, v.sign() * torch.finfo(torch.float16).max, 1.0)
+
+
+def test_infinite_values_stay():
+    """Only finite sums end at the largest value: an infinite one decides its column."""
+    n, big = 300, torch.finfo(torch.float16).max
+    q, k, v = rows(n, 2, 2, 64, torch.float16, 33)
+    v = v.sign() * big
+    v[0, 0, 3] = float("inf")
+    v[290, 1, 5] = float("-inf")
+    v[10, 1, 7] = float("nan")
+    out = api.prompt_attention(q, k, v, starts([n]), 0.125)
+    assert api.get_device_error() == (0, 0)
+    want = torch.ones_like(out, dtype=torch.bool)
+    want[:, 0, 3], want[290:, 1, 5], want[10:, 1, 7] = False, False, False
+    assert torch.equal(out.isfinite(), want)
+    assert bool((out[:, 0, 3] == float("inf")).all()) and bool((out[290:, 1, 5] == float("-inf")).all())
