@@ -375,7 +375,9 @@ size_t pa_prompt_attention_workspace_size(int32_t num_seqs, int32_t num_tokens, 
  * scale must be > 0.  Computed on the tensor cores; scores, softmax and sums
  * in binary32, the weights rounded to `dtype` before they multiply the values.
  * Rows that a query does not attend -- later tokens of its sequence, other
- * sequences, rows outside every sequence -- may hold anything, NaN included.
+ * sequences, rows outside every sequence -- may hold anything, NaN included.  An
+ * infinite or NaN value makes its column of the rows that attend it infinite or
+ * NaN (an infinite one: NaN where its weight rounds to 0), and no other.
  * Supported: f16 or bf16, head_dim 64 or 128, G <= 128; else
  * PA_ERR_UNSUPPORTED.  A sequence whose start rows break the rules above sets
  * PA_DEVERR_CONTEXT_LEN and is skipped; when the others together have more rows

@@ -43,8 +43,11 @@
 // holds positions some row of the item does not attend (the last one or two of
 // an item), a warp clears its rows after the item's last position and
 // replaces non-finite elements by 0; those are added again, to the rows that do
-// attend them, by the output warps (an infinite or NaN term decides a sum
-// whatever its weight is).  Keys need no such care: masked scores are replaced.
+// attend them, by the output warps.  In the tiles before, which every row of the
+// item attends, the tensor cores multiply such a value by its rounded weight: an
+// infinite one gives NaN where the weight has rounded to 0.  Either way it makes its
+// column of the rows that attend it infinite or NaN, and nothing else.  Keys need no
+// such care: masked scores are replaced.
 //
 // Warp roles (512 threads, registers moved between the groups by setmaxnreg):
 //   warps 0, 1       MMA issuers of query tile 0 / 1 (warp 0 owns the TMEM
