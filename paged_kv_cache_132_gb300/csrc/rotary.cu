@@ -18,8 +18,8 @@
 //
 // Measured: 85.0 us for 20 588 bf16 tokens of 32 + 2 * 8 heads of 128 with the
 // keys kept (559 MB: 6.6 TB/s, 0.98 of the copy bandwidth) with 64 threads a
-// token, 108.5 us with 256; 2.9 us for 256 tokens (6.4 MB) with 256 threads,
-// 3.5 us with 64.
+// token, 108.5 us with 256; 2.6 us for 256 tokens (6.4 MB) with 256 threads,
+// 3.3 us with 64.
 #include "attn_common.cuh"
 #include "common.cuh"
 #include "kernels.h"
@@ -29,9 +29,18 @@ namespace {
 
 constexpr int kRotaryThreads = 256;       // of a token's CTA in small steps, where latency counts
 constexpr int kRotaryThreadsMany = 64;    // ... with many tokens: more CTAs, each with more loads in flight
-// 4.6 us with 256 threads and 5.9 with 64 for 1024 tokens of 48 head rows, 8.5
-// and 7.0 for 2048; 9.1 and 13.4, 18.6 and 17.6 with 120 head rows.
-constexpr int kRotaryManyTokens = 1024;
+// The few threads pay their passes over a token's rows one after the other, the many
+// fill the GPU with fewer tokens: so the tokens are held against the lanes of a
+// token's rows.  From kRotaryManyTokens tokens a lane on, 64 threads.  Measured
+// (graph replays), 256 threads and 64:
+//   384 lanes (48 16-bit rows of 128): 512 tokens 3.2 and 3.6 us, 768 4.4 and 3.9,
+//     2048 8.2 and 6.7, 8192 40 and 33;
+//   768 lanes (48 32-bit rows of 128): 1024 tokens 7.0 and 7.4 us, 1536 9.9 and 11.6,
+//     2560 19.0 and 16.2;
+//   960 lanes (120 16-bit rows of 128): 1024 tokens 8.7 and 10.8 us, 1536 12.7 and
+//     14.5, 2048 18.6 and 17.7, 2560 26.5 and 28.9, 4096 43.0 and 41.9;
+//   48 lanes (6 16-bit rows of 128): 64 tokens 2.0 and 1.9 us, 1024 3.7 and 2.3.
+constexpr int kRotaryManyTokens = 2;
 constexpr int kRotaryRows = 2;            // rows of a lane in flight
 
 template <typename T>
@@ -169,8 +178,9 @@ template <typename T>
 cudaError_t launch(const RotaryParams& p, bool interleaved, int64_t num_tokens, cudaStream_t stream) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)num_tokens);
-    cfg.blockDim = dim3((unsigned)(num_tokens > kRotaryManyTokens && p.lanes <= kRotaryThreadsMany ? kRotaryThreadsMany
-                                                                                                  : kRotaryThreads));
+    const int64_t token_lanes = ((int64_t)p.num_heads + 2 * (int64_t)p.num_kv_heads) * p.lanes;
+    const bool many = num_tokens >= kRotaryManyTokens * token_lanes && p.lanes <= kRotaryThreadsMany;
+    cfg.blockDim = dim3((unsigned)(many ? kRotaryThreadsMany : kRotaryThreads));
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
