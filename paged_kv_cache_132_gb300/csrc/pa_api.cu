@@ -217,7 +217,9 @@ bool encode_rows_map(CUtensorMap* map, const void* base, int dtype, int num_toke
 // pure function of its key (base address, shape, dtype, view), so a cached
 // map is valid for as long as the key matches, whatever the caller did with
 // the memory in between.  Kernel parameters are copied at launch, so the
-// returned pointer is only used before the next lookup on this thread.
+// returned pointer is only used before the next lookup on this thread.  Rows of
+// activations have a cache of their own: new ones come with every call, and would
+// put the pools' maps out, which stay for the life of a server.
 struct MapKey {
     int kind;  // 0: pool, 2-D view; 1: pool, decode's view; 2: rows of tokens
     int dtype;
@@ -233,28 +235,30 @@ struct MapSlot {
     MapKey key;
     bool valid;
 };
-constexpr int kMapSlots = 16;
-thread_local MapSlot t_maps[kMapSlots];
-thread_local unsigned t_map_next = 0;
+struct MapCache {
+    static constexpr int kSlots = 16;
+    MapSlot slots[kSlots];
+    unsigned next;
 
-const CUtensorMap* find_map(const MapKey& key) {
-    for (int i = 0; i < kMapSlots; ++i)
-        if (t_maps[i].valid && t_maps[i].key == key) return &t_maps[i].map;
-    return nullptr;
-}
-
-MapSlot& next_map_slot() {
-    MapSlot& slot = t_maps[t_map_next % kMapSlots];
-    ++t_map_next;
-    slot.valid = false;
-    return slot;
-}
+    const CUtensorMap* find(const MapKey& key) const {
+        for (int i = 0; i < kSlots; ++i)
+            if (slots[i].valid && slots[i].key == key) return &slots[i].map;
+        return nullptr;
+    }
+    MapSlot& take() {  // the oldest
+        MapSlot& slot = slots[next++ % kSlots];
+        slot.valid = false;
+        return slot;
+    }
+};
+thread_local MapCache t_pool_maps;
+thread_local MapCache t_row_maps;
 
 const CUtensorMap* pool_map(const void* base, int dtype, const pa::PoolShape& shape, bool interleave) {
     const MapKey key{interleave ? 1 : 0, dtype, base, shape.num_blocks, shape.num_kv_heads, shape.block_size,
                      shape.head_dim, 0, 0};
-    if (const CUtensorMap* m = find_map(key)) return m;
-    MapSlot& slot = next_map_slot();
+    if (const CUtensorMap* m = t_pool_maps.find(key)) return m;
+    MapSlot& slot = t_pool_maps.take();
     if (!encode_pool_map(&slot.map, base, dtype, shape, interleave)) return nullptr;
     slot.key = key;
     slot.valid = true;
@@ -264,8 +268,8 @@ const CUtensorMap* pool_map(const void* base, int dtype, const pa::PoolShape& sh
 const CUtensorMap* rows_map(const void* base, int dtype, int num_tokens, int num_heads, int head_dim,
                             int64_t token_stride, int box_heads, int box_tokens) {
     const MapKey key{2, dtype, base, num_tokens, num_heads, head_dim, token_stride, box_heads, box_tokens};
-    if (const CUtensorMap* m = find_map(key)) return m;
-    MapSlot& slot = next_map_slot();
+    if (const CUtensorMap* m = t_row_maps.find(key)) return m;
+    MapSlot& slot = t_row_maps.take();
     if (!encode_rows_map(&slot.map, base, dtype, num_tokens, num_heads, head_dim, token_stride, box_heads, box_tokens))
         return nullptr;
     slot.key = key;
