@@ -205,7 +205,9 @@ int pa_rotary_and_cache(void *query_out, int64_t query_out_stride, void *key_out
  *   slot_mapping, positions   device, int64 and int32 [max_tokens]: where each
  *                     new token goes, sequence after sequence; -1 behind the last
  *                     one, which pa_reshape_and_cache and pa_rotary_and_cache skip
- *   max_tokens        host, >= the new tokens (a captured graph's largest step)
+ *   max_tokens        host, >= the new tokens (a captured graph's largest step).  All
+ *                     rows are written, and the launch follows their number: steps of
+ *                     few tokens are best captured with room for few
  * Blocks belong to one sequence each: shared ones are the host manager's.
  * A sequence whose lengths are negative (but -1) or beyond its table row sets
  * PA_DEVERR_CONTEXT_LEN and stays as it is.  A step that does not fit -- blocks,
@@ -369,11 +371,14 @@ size_t pa_prompt_attention_workspace_size(int32_t num_seqs, int32_t num_tokens, 
  *                     heads of head_dim contiguous elements, *_stride elements
  *                     from one token's row to the next: at least the row, a
  *                     multiple of head_dim (slices of a fused projection's
- *                     rows, say).  out must not overlap them.
+ *                     rows, say; rows padded by less, which pa_rotary_and_cache
+ *                     takes, are PA_ERR_INVALID_ARG).  out must not overlap them.
  *   query_start_loc   device, int32 [num_seqs + 1], non-decreasing, first
  *                     entry >= 0, last <= num_tokens; sequences may be empty
  * scale must be > 0.  Computed on the tensor cores; scores, softmax and sums
- * in binary32, the weights rounded to `dtype` before they multiply the values.
+ * in binary32, the weights rounded to `dtype` before they multiply the values
+ * (pa_prefill keeps a bf16 weight's next 8 bits too): half a step of the type of
+ * the weighted sum of |value|, next to as much for the output's own rounding.
  * Rows that a query does not attend -- later tokens of its sequence, other
  * sequences, rows outside every sequence -- may hold anything, NaN included.  An
  * infinite or NaN value makes its column of the rows that attend it infinite or

@@ -338,7 +338,9 @@ __device__ void prompt_load(const PromptParams& p, typename Shape::Smem& sm, int
         long long rows = 0;
         for (walk.base = 0; walk.base < p.num_seqs; walk.base += 32) {
             prompt_walk_load(p, walk, lane);
-            rows += __reduce_add_sync(kFullMask, walk.len);  // at most 32 * 2^15: few rows without a list
+            // 32 lengths of at most num_tokens each, which is below 2 * tile_tokens * SMs
+            // without a list: some 38 000, the sum far below 2^31.
+            rows += __reduce_add_sync(kFullMask, walk.len);
         }
         if (rows > p.num_tokens) {
             set_error(p.err, PA_DEVERR_CONTEXT_LEN);

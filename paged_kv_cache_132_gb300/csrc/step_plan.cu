@@ -13,8 +13,8 @@
 // in the sums, one thread per block or token, so a step of one long prompt and
 // one of thousands of single tokens cost alike.
 //
-// Bound: latency.  A step's data are a few bytes per sequence and 12 per token
-// (a megabyte at most), but its loads depend on one another.  So a step is one
+// Bound: latency.  A step's data are a few bytes per sequence and 12 per token row
+// (1 MB for the large step below), but its loads depend on one another.  So a step is one
 // CTA, or for large steps one cluster of kStepCluster CTAs, each of which makes
 // the sums for itself in shared memory, and then a second kernel that places the
 // tokens on the whole GPU.  Nothing that a thread writes is read by another one
@@ -23,8 +23,8 @@
 // inputs (lengths, free state) are written after a barrier of them all.
 //
 // Measured (graph replays, launch included; an empty step takes 2.3 us): 4.4 us
-// for 256 sequences of one new token; 13.4 us for 4096 sequences with 74 000 new
-// tokens, 12 600 blocks given back and 5 300 taken (1 MB).  In one CTA the sums
+// for 256 sequences of one new token; 13.3 us for 4096 sequences with 74 000 new
+// tokens, 3 700 blocks given back and 4 600 taken (1 MB).  In one CTA the sums
 // alone take 1 us per 1024 sequences (three prefix sums by shuffles).
 #include <cooperative_groups.h>
 
@@ -40,7 +40,9 @@ constexpr int kStepCluster = 8;  // the largest cluster every GPU of the family 
 // Steps of more token rows or sequences than these run on the cluster and the
 // slots kernel.  Measured, one CTA against those: 4.4 and 5.8 us for a prompt of
 // 4096 tokens, 6.9 and 6.7 us for 8 of 1024; 5.8 and 7.5 us for 1024 sequences of
-// one token, 7.9 and 7.9 us for 2048.
+// one token, 7.9 and 7.9 us for 2048.  The rows are those that there is room for
+// (the host knows no others): 256 sequences of one token take 4.4 us with room for
+// 256 rows, 5.6 with 8192, 7.1 with 8193 to 65536.
 constexpr int kStepSmallTokens = 8192;
 constexpr int kStepSmallSeqs = 2048;
 constexpr int kStepUnroll = 4;   // entries of a thread whose loads are in flight together
