@@ -32,6 +32,17 @@ def randn(*shape, seed, dtype=torch.bfloat16):
 def test_a_captured_step_of_plan_rotary_and_decode(seqs, room):
     """The plan advances the lengths in place; the decode that follows reads them.
     Contexts cross blocks and partitions; one CTA, the cluster, and its slots kernel."""
+    captured_steps(seqs, room, ("plan", "rotary", "decode"))
+
+
+@pytest.mark.parametrize("seqs,room", [(300, 300), (300, 9000), (2100, 2100)])
+@pytest.mark.parametrize("order", [("plan", "decode"), ("plan", "prefill"), ("plan", "rotary", "prefill", "decode"),
+                                   ("plan", "rotary", "prompt"), ("plan", "write", "decode", "rotary", "decode")])
+def test_other_orders(order, seqs, room):
+    captured_steps(seqs, room, order)
+
+
+def captured_steps(seqs, room, order):
     steps, width = 12, 44
     g = torch.Generator().manual_seed(seqs)
     ctx0 = torch.randint(240, 640, (seqs,), generator=g).int()
@@ -43,6 +54,7 @@ def test_a_captured_step_of_plan_rotary_and_decode(seqs, room):
     kc, vc = randn(nb, HKV, B, D, seed=1), randn(nb, HKV, B, D, seed=2)
     rows = randn(room, (H + 2 * HKV) * D, seed=3)
     q, k, v = (x.unflatten(1, (-1, D)) for x in rows.split([H * D, HKV * D, HKV * D], 1))
+    kr, vr = k.contiguous(), v.contiguous()
     angles = torch.arange(width * B, dtype=torch.float64)[:, None] * 0.7 ** torch.arange(D // 2)
     cs = torch.cat([angles.cos(), angles.sin()], 1).float().cuda()
     new = torch.ones(seqs, dtype=torch.int32, device="cuda")
@@ -54,16 +66,27 @@ def test_a_captured_step_of_plan_rotary_and_decode(seqs, room):
             i32 = dict(dtype=torch.int32, device="cuda")
             self.plan = api.StepPlan(self.ctx, self.state, torch.empty(seqs + 1, **i32),
                                      torch.empty(room, dtype=torch.int64, device="cuda"), torch.empty(room, **i32))
-            self.q = torch.empty(room, H, D, dtype=q.dtype, device="cuda")
-            self.out = torch.empty(seqs, H, D, device="cuda")
-            self.ws = torch.empty(api.decode_workspace_size(seqs, H, width * B, 0, D), dtype=torch.uint8, device="cuda")
+            self.q = q.contiguous()  # what decode and prefill read where no call rotates it
+            self.out = torch.zeros(seqs, H, D, device="cuda")
+            self.rows = torch.zeros(room, H, D, dtype=q.dtype, device="cuda")
+            need = max(api.decode_workspace_size(seqs, H, width * B, 0, D),
+                       api.prompt_attention_workspace_size(seqs, room, H, HKV))
+            self.ws = torch.empty(need, dtype=torch.uint8, device="cuda")
 
         def calls(self):
-            return (lambda: api.plan_step(new, self.ctx, self.ring, self.state, self.tables, B, room, nb, out=self.plan),
-                    lambda: api.rotary_and_cache(q, k, v, self.plan.positions, cs, self.plan.slot_mapping, self.k,
-                                                 self.v, query_out=self.q),
-                    lambda: api.decode(self.q[:seqs], self.k, self.v, self.tables, self.ctx, D ** -0.5, out=self.out,
-                                       workspace=self.ws))
+            p = self.plan
+            made = dict(
+                plan=lambda: api.plan_step(new, self.ctx, self.ring, self.state, self.tables, B, room, nb, out=p),
+                rotary=lambda: api.rotary_and_cache(q, k, v, p.positions, cs, p.slot_mapping, self.k, self.v,
+                                                    query_out=self.q),
+                write=lambda: api.reshape_and_cache(kr, vr, self.k, self.v, p.slot_mapping),
+                decode=lambda: api.decode(self.q[:seqs], self.k, self.v, self.tables, self.ctx, D ** -0.5, out=self.out,
+                                          workspace=self.ws),
+                prefill=lambda: api.prefill(self.q, p.query_start_loc, self.k, self.v, self.tables, self.ctx, D ** -0.5,
+                                            1, out=self.rows),
+                prompt=lambda: api.prompt_attention(self.q, k, v, p.query_start_loc, D ** -0.5, out=self.rows,
+                                                    workspace=self.ws))
+            return [made[x] for x in order]
 
     waited, graphed = Run(), Run()
     for call in graphed.calls():  # not captured: what the first call of each sets up
@@ -85,7 +108,7 @@ def test_a_captured_step_of_plan_rotary_and_decode(seqs, room):
         assert torch.equal(waited.ctx, graphed.ctx) and torch.equal(waited.tables, graphed.tables)
         assert torch.equal(waited.plan.slot_mapping, graphed.plan.slot_mapping)
         assert same(waited.k, graphed.k) and same(waited.v, graphed.v)
-        assert same(waited.out, graphed.out)
+        assert same(waited.out, graphed.out) and same(waited.rows, graphed.rows)
     assert torch.equal(waited.ctx.cpu(), ctx0 + steps)
 
 
