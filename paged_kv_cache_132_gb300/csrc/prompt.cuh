@@ -32,11 +32,11 @@
 // (2 x (128 + 128) columns at d = 128), so a tile's chain is S -> softmax -> P V ->
 // S; a step of both tiles takes 2080 cycles of MMAs and 2750 by the chain (softmax
 // 1600: 128 exponentials a thread at 4.3 cycles, the scores' load, the maximum;
-// then P V and S 1040 and their latency).  Measured: 1.65 PFLOP/s (0.83 of
-// the cuBLAS burst rate, 0.95 of the sustained one) for 32768 tokens of 32 heads
-// of 128, where power sets the clock; 1.02-1.11 PFLOP/s for 32 prompts of
-// 128-1024 tokens (114-125 us, by the clock), where an item is 3.5 steps and
-// starting it costs a third of one.
+// then P V and S 1040 and their latency).  Measured: 1.59-1.76 PFLOP/s by the box
+// (0.8-0.88 of the cuBLAS burst rate, 0.91-1.0 of the sustained one) for 32768
+// tokens of 32 heads of 128, where power sets the clock; 0.99-1.13 PFLOP/s for 32
+// prompts of 128-1024 tokens (112-128 us, by the clock), where an item is 3.5 steps
+// and starting it costs a third of one.
 //
 // Values a query must not see: a row's weights after its own position are 0,
 // but 0 * NaN is NaN on the tensor cores.  So before P.V reads a V tile that

@@ -41,8 +41,8 @@ constexpr int kStepCluster = 8;  // the largest cluster every GPU of the family 
 // slots kernel.  Measured, one CTA against those: 4.4 and 5.8 us for a prompt of
 // 4096 tokens, 6.9 and 6.7 us for 8 of 1024; 5.8 and 7.5 us for 1024 sequences of
 // one token, 7.9 and 7.9 us for 2048.  The rows are those that there is room for
-// (the host knows no others): 256 sequences of one token take 4.4 us with room for
-// 256 rows, 5.6 with 8192, 7.1 with 8193 to 65536.
+// (the host knows no others): 256 sequences of one token take 4.5 us with room for
+// 256 rows, 5.6 with 8192, 7.2 with 8193 to 65536.
 constexpr int kStepSmallTokens = 8192;
 constexpr int kStepSmallSeqs = 2048;
 constexpr int kStepUnroll = 4;   // entries of a thread whose loads are in flight together
