@@ -74,6 +74,9 @@ typedef enum {
 #define PA_DEVERR_STEP         0x100 /* a step needs more blocks than are free, more ring
                                         entries or more token rows than there are, or its
                                         free_state is out of range                         */
+#define PA_DEVERR_TREE     0x200 /* a node's parent is not before it, its token is outside the
+                                    vocabulary, or a path does not increase                 */
+#define PA_DEVERR_PROBS    0x400 /* a row of probabilities that a token is drawn from has none */
 /* Reported only in checked mode (PA_OPT_DEBUG_CHECKS, below): */
 #define PA_DEVERR_DUP_SLOT     0x20 /* two tokens of one cache write share a slot          */
 #define PA_DEVERR_PAIR_CONFLICT 0x40 /* copy/swap pairs: a destination repeated, or (same
@@ -103,6 +106,7 @@ typedef enum {
  *                             (PA_DEVERR_CONTEXT_LEN), every block id the
  *                             sequence reads in [0, num_blocks)
  *                             (PA_DEVERR_BLOCK_ID)
+ *     (The calls of drafted trees check all they read in every mode.)
  *     The main kernel then runs as usual: its result is unspecified where a
  *     precondition is broken, but no access leaves the caller's buffers.
  *     The pair and slot checks compare all pairs of entries: O(n^2) work,
@@ -396,6 +400,159 @@ int pa_prompt_attention(void *out, const void *query, int64_t query_stride,
                         const int32_t *query_start_loc, int32_t num_seqs, int32_t num_tokens,
                         int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, int32_t dtype,
                         float scale, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * A step of drafted trees (speculative decoding): each sequence brings a tree of
+ * candidate tokens, the model scores them all at once over the paged cache, and the
+ * tokens that the target accepts stay.  The calls of such a step, in order:
+ *   pa_plan_step          new_lens[s] = nodes of the tree: blocks, slots, start rows
+ *   pa_plan_tree          positions and ancestor masks of the nodes
+ *   pa_rotary_and_cache   every layer: the nodes' keys and values into their slots
+ *   pa_tree_attention     every layer
+ *   pa_verify_tree        accepted nodes and the next token
+ *   pa_commit_tree        every layer's pools, lengths, blocks: the accepted path stays
+ * Sequence s owns rows query_start_loc[s] .. query_start_loc[s+1]-1 of the nodes'
+ * arrays, the last n_s of its context_lens[s] cached tokens.  Nodes are numbered from
+ * 0 in a sequence, parents before children; node 0 is the sequence's last token, whose
+ * row of the target predicts the first drafted ones.  At most PA_MAX_TREE_NODES nodes
+ * a sequence.  A sequence whose start rows or lengths break the rules (rows decreasing
+ * or past num_tokens, n_s > context_lens[s]) sets PA_DEVERR_CONTEXT_LEN.
+ */
+#define PA_MAX_TREE_NODES 1024
+
+/*
+ * Positions and masks of drafted trees.  Node i of a sequence attends to itself and
+ * its ancestors: bit j of its mask row is set for those nodes j.  Its position is
+ * context_lens[s] - n_s + depth, the depth of a node without a parent being 0.
+ *   parents       device, int32 [num_tokens]: index in the sequence, less than the
+ *                 node's own; -1: the node follows the cached tokens directly.
+ *                 Another one sets PA_DEVERR_TREE and counts as -1
+ *   query_start_loc, context_lens   device, int32 [num_seqs + 1], [num_seqs]
+ *   positions     device, int32 [num_tokens]
+ *   tree_mask     device, [num_tokens][mask_words] 64-bit words, node j in bit j % 64
+ *                 of word j / 64
+ * Rows of no sequence (a captured step's padding), of one with more than 64 *
+ * mask_words nodes or with bad lengths get position -1, which pa_rotary_and_cache
+ * skips, and no bits.  mask_words <= PA_MAX_TREE_NODES / 64, else PA_ERR_UNSUPPORTED.
+ */
+int pa_plan_tree(const int32_t *parents, const int32_t *query_start_loc, const int32_t *context_lens,
+                 int32_t num_seqs, int32_t num_tokens, int32_t *positions, uint64_t *tree_mask,
+                 int32_t mask_words, void *stream);
+
+/*
+ * Bytes of device workspace pa_tree_attention needs: the parts of items that lie
+ * across two CTAs' shares of the work.  Needs no initialisation; two calls in flight
+ * at once must not share one.  Returns 0 for invalid arguments.
+ */
+size_t pa_tree_attention_workspace_size(int32_t num_tokens, int32_t mask_words, int32_t num_heads,
+                                        int32_t num_kv_heads, int32_t head_dim);
+
+/*
+ * Attention of the nodes of drafted trees over the paged cache ("PagedAttention 论文
+ * 精读笔记", §2.1 attention equation, §5.2 block table).  Node i of sequence s attends
+ * to the positions before the tree, 0 .. context_lens[s] - n_s - 1, and to the nodes j
+ * whose bit of tree_mask's row is set (itself only if its own bit is):
+ *   out[q][h][:] = sum_j softmax_j(scale * query[q][h] . k_j) v_j,
+ * query head h reading KV head h / G, G = num_heads / num_kv_heads.  Any mask may be
+ * given, not only a tree's; bits from n_s on count for nothing.  A row that attends to
+ * nothing is 0.  The nodes' K/V must be in the pools.
+ *   out               device, 32-byte aligned, [num_tokens][num_heads][head_dim] of
+ *                     cache->dtype; rows not covered by a sequence are not written
+ *   query             device, rows of num_heads heads of head_dim contiguous elements
+ *                     of cache->dtype, query_stride elements from one token's row to
+ *                     the next: at least the row, a multiple of 16 bytes
+ *   query_start_loc, tree_mask, mask_words   as pa_plan_tree's
+ *   block_tables      device, int32 [num_seqs][max_blocks_per_seq]
+ *   context_lens      device, int32 [num_seqs], n_s <= context_lens[s] <=
+ *                     max_blocks_per_seq * block_size
+ * scale must be > 0.  Computed on the tensor cores; scores, softmax and sums in
+ * binary32, the weights rounded to the pools' type before they multiply the values:
+ * half a step of the type of the weighted sum of |value|, next to as much for the
+ * output's own rounding.  What a row does not attend to -- other nodes, slots behind
+ * the context -- may hold anything, NaN included.  An infinite or NaN value makes its
+ * column of the rows that attend to it infinite or NaN (an infinite one: NaN where
+ * its weight rounds to 0), and no other.  The result depends on the lengths of the
+ * other sequences of the call within the rounding of binary32 sums (they move the
+ * borders of the work), and is the same from call to call.
+ * Supported: f16 or bf16 pools, head_dim 64 or 128, block_size 8, 16 or 32, G <= 128,
+ * mask_words <= PA_MAX_TREE_NODES / 64; else PA_ERR_UNSUPPORTED.  A sequence with bad
+ * lengths or more than 64 * mask_words nodes sets PA_DEVERR_CONTEXT_LEN and is skipped;
+ * a bad block id sets PA_DEVERR_BLOCK_ID.
+ *   workspace         device, 256-byte aligned, at least
+ *                     pa_tree_attention_workspace_size(...) bytes
+ */
+int pa_tree_attention(void *out, const void *query, int64_t query_stride, const int32_t *query_start_loc,
+                      int32_t num_tokens, const uint64_t *tree_mask, int32_t mask_words,
+                      const void *k_cache, const void *v_cache, const pa_cache_desc *cache,
+                      const int32_t *block_tables, int32_t max_blocks_per_seq,
+                      const int32_t *context_lens, int32_t num_seqs, int32_t num_heads,
+                      int32_t num_kv_heads, float scale, void *workspace, size_t workspace_bytes,
+                      void *stream);
+
+/*
+ * Verification of drafted trees from given random numbers: tokens drawn as the target
+ * would draw them.  From node 0 on, the children of the last accepted node are tried in
+ * order of their numbers.  With that node's rows p of the target and q of the draft,
+ * which its children were drawn from independently, and c = 0, s = 1 at first:
+ *   child x is accepted if  u q(x) s < max(p(x) - c q(x), 0),  u its accept_uniforms;
+ *   otherwise  c += s,  s = sum_t max(p(t) - c q(t), 0)
+ * (the sum of the residual distribution after each refusal).  When no child is accepted
+ * the next token is the lowest t whose cumulative weight max(p(t) - c q(t), 0) exceeds
+ * sample_uniforms[s] times the sum of all; where nothing is left, the row p itself
+ * serves, and the remaining children are not tried.  Without draft_probs (NULL: tokens
+ * that were not drawn, such as looked-up ones) x is accepted if u s < p(x), a refusal
+ * takes p(x) out of s and out of the row, and q plays no part.
+ *   tokens, parents   device, int32 [num_tokens]: node i's token (node 0's is not read)
+ *                     and parent (pa_plan_tree); a child of no node, a parent not before
+ *                     its node and a token outside the vocabulary are not tried, the
+ *                     last two set PA_DEVERR_TREE
+ *   target_probs, draft_probs   device, of `dtype` (any pa_dtype): row i holds the
+ *                     vocab_size probabilities of the token after node i, *_stride
+ *                     elements from row to row.  NaN and negative ones count as 0,
+ *                     those above 1 as 1.  Aligned to 16 bytes with such a stride, or
+ *                     else slower
+ *   accept_uniforms, sample_uniforms   device, float [num_tokens], [num_seqs], in [0, 1)
+ *   accepted_lens     device, int32 [num_seqs]: accepted nodes, node 0 among them
+ *   path              device, int32 [num_tokens]: from each sequence's first row on the
+ *                     accepted nodes, then -1; other rows are not written
+ *   next_tokens       device, int32 [num_seqs]
+ * Sums are exact to 2^-52 a weight, whatever the order.  A sequence without nodes or
+ * with bad lengths gets accepted length 0 and token -1; a row without any weight sets
+ * PA_DEVERR_PROBS and gives token -1.  vocab_size <= 2^20, else PA_ERR_UNSUPPORTED.
+ */
+int pa_verify_tree(const int32_t *tokens, const int32_t *parents, const int32_t *query_start_loc,
+                   int32_t num_seqs, int32_t num_tokens, const void *target_probs, int64_t target_stride,
+                   const void *draft_probs, int64_t draft_stride, int32_t vocab_size, int32_t dtype,
+                   const float *accept_uniforms, const float *sample_uniforms, int32_t *accepted_lens,
+                   int32_t *path, int32_t *next_tokens, void *stream);
+
+/*
+ * Commit of the accepted paths: in every layer's pools the K and V rows of node path[i]
+ * move to the place of node i, i < accepted_lens[s]; the length becomes
+ * context_lens[s] - n_s + accepted_lens[s]; and the blocks behind it go back to the ring
+ * of pa_plan_step, behind its last free entry, sequence after sequence.
+ *   k_caches, v_caches  HOST arrays of num_layers device pool pointers (1 <=
+ *                     num_layers <= 256), all shaped by `cache`
+ *   path              device, int32 [num_tokens]: as pa_verify_tree's, entries from the
+ *                     sequence's first row on, 0 <= path[0] < path[1] < ... < n_s
+ *   accepted_lens     device, int32 [num_seqs], 0 .. n_s (0: no node stays)
+ *   context_lens_out  device, int32 [num_seqs].  May be context_lens (one launch more)
+ *   block_tables      device, int32 [num_seqs][max_blocks_per_seq]; not written.  The
+ *                     blocks of the nodes belong to one sequence each
+ *   free_ring, free_state, free_state_out   as pa_plan_step's; free_ring NULL: no blocks
+ *                     are given back (a host manager does), the others are not used
+ * A sequence with bad lengths (PA_DEVERR_CONTEXT_LEN) or a bad path (PA_DEVERR_TREE)
+ * stays as it is.  A ring without room, or a free_state out of range, sets PA_DEVERR_STEP
+ * and no block is given back.  A bad block id sets PA_DEVERR_BLOCK_ID, and rows from or
+ * to it are not moved.  num_seqs <= 16384, ring_size below 2^30 - 1, else
+ * PA_ERR_UNSUPPORTED.
+ */
+int pa_commit_tree(void *const *k_caches, void *const *v_caches, int32_t num_layers, const pa_cache_desc *cache,
+                   const int32_t *query_start_loc, int32_t num_seqs, int32_t num_tokens,
+                   const int32_t *path, const int32_t *accepted_lens, const int32_t *context_lens,
+                   int32_t *context_lens_out, const int32_t *block_tables, int32_t max_blocks_per_seq,
+                   int32_t *free_ring, int32_t ring_size, const int32_t *free_state,
+                   int32_t *free_state_out, void *stream);
 
 /*
  * Copy-on-write block copy, one launch for all pairs and layers.  For every

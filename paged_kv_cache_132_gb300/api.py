@@ -396,6 +396,228 @@ def prompt_attention(query: torch.Tensor, key: torch.Tensor, value: torch.Tensor
     return out
 
 
+class TreePlan(NamedTuple):
+    """What plan_tree makes (device tensors)."""
+    positions: torch.Tensor  # int32 [T], -1 for rows of no sequence
+    tree_mask: torch.Tensor  # int64 [T][ceil(max_nodes / 64)]: bit j of a row, node j of its sequence
+
+
+def plan_tree(parents: torch.Tensor, query_start_loc: torch.Tensor, context_lens: torch.Tensor, max_nodes: int, *,
+              out: Optional[TreePlan] = None, stream: Optional[torch.cuda.Stream] = None) -> TreePlan:
+    """Positions and ancestor masks of drafted trees.
+
+    Sequence s owns rows query_start_loc[s] .. query_start_loc[s+1]-1, the last
+    ones of its context_lens[s] cached tokens (plan_step with new_lens[s] nodes);
+    ``parents`` int32 [T] holds each node's parent as an index in its sequence,
+    less than its own (-1: none).  ``max_nodes`` is a host-side upper bound of the
+    nodes of a sequence.  Positions are the depths behind the cached tokens; they
+    and the slots of plan_step go to rotary_and_cache, the masks to tree_attention."""
+    lib = native.load()
+    t, i32 = parents.numel(), torch.int32
+    _require(max_nodes >= 1, "max_nodes must be positive")
+    words = (max_nodes + 63) // 64
+    _require(parents.dtype is i32 and parents.shape == (t,) and parents.is_contiguous(), "parents is int32 [T]")
+    _require(context_lens.dtype is i32 and context_lens.dim() == 1 and context_lens.is_contiguous(),
+             "context_lens is int32 [num_seqs]")
+    s = context_lens.numel()
+    _require(query_start_loc.dtype is i32 and query_start_loc.shape == (s + 1,) and query_start_loc.is_contiguous(),
+             "query_start_loc is int32 [num_seqs + 1]")
+    if out is None:
+        out = TreePlan(_empty((t,), i32, parents.device, stream),
+                       _empty((t, words), torch.int64, parents.device, stream))
+    _require(out[0].dtype is i32 and out[0].shape == (t,) and out[0].is_contiguous()
+             and out[1].dtype is torch.int64 and out[1].shape == (t, words) and out[1].is_contiguous(),
+             "out is (positions int32 [T], tree_mask int64 [T][words])")
+    _require_here(parents, query_start_loc, context_lens, *out)
+    _raise(lib.pa_plan_tree(parents.data_ptr(), query_start_loc.data_ptr(), context_lens.data_ptr(), s, t,
+                            out[0].data_ptr(), out[1].data_ptr(), words, _stream_ptr(stream)), "pa_plan_tree")
+    return out
+
+
+def tree_attention_workspace_size(num_tokens: int, mask_words: int, num_heads: int, num_kv_heads: int,
+                                  head_dim: int) -> int:
+    return int(native.load().pa_tree_attention_workspace_size(num_tokens, mask_words, num_heads, num_kv_heads,
+                                                              head_dim))
+
+
+def tree_attention(query: torch.Tensor, query_start_loc: torch.Tensor, tree_mask: torch.Tensor,
+                   k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
+                   context_lens: torch.Tensor, scale: float, *, out: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None,
+                   stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Attention of the nodes of drafted trees over the paged cache; returns
+    out [T][H][d] in the pools' type (f16 or bf16).
+
+    Sequence s owns rows query_start_loc[s] .. query_start_loc[s+1]-1 of query
+    [T][H][d], the last n_s of its context_lens[s] cached tokens, their K/V in the
+    pools.  A row attends to every position before its tree and to the nodes whose
+    bit of its row of ``tree_mask`` (plan_tree's, or any other mask; int64
+    [T][words]) is set; to nothing: 0.  The query may be a slice of a fused
+    projection's rows.  Rows outside every sequence are not written."""
+    lib = native.load()
+    _require(query.dim() == 3, "query is [num_tokens][num_heads][head_dim]")
+    t, h, d = query.shape
+    desc = cache_desc(k_cache)
+    dtype = k_cache.dtype
+    _require(k_cache.shape == v_cache.shape and v_cache.dtype is dtype and k_cache.is_contiguous()
+             and v_cache.is_contiguous(), "K and V pools must match and be contiguous")
+    _require(query.dtype is dtype and d == desc.head_dim, "query dtype/head_dim must match the pools")
+    i32 = torch.int32
+    _require(block_tables.dtype is i32 and block_tables.dim() == 2 and block_tables.is_contiguous(),
+             "block_tables is int32 [num_seqs][max_blocks]")
+    s = block_tables.shape[0]
+    _require(context_lens.dtype is i32 and context_lens.shape == (s,) and context_lens.is_contiguous(),
+             "context_lens is int32 [num_seqs]")
+    _require(query_start_loc.dtype is i32 and query_start_loc.shape == (s + 1,) and query_start_loc.is_contiguous(),
+             "query_start_loc is int32 [num_seqs + 1]")
+    _require(tree_mask.dtype is torch.int64 and tree_mask.dim() == 2 and tree_mask.shape[0] == t
+             and tree_mask.is_contiguous(), "tree_mask is int64 [num_tokens][words]")
+    if out is None:
+        out = _empty((t, h, d), dtype, query.device, stream)
+    _require(out.shape == query.shape and out.dtype is dtype and out.is_contiguous(),
+             "out is contiguous [num_tokens][num_heads][head_dim] of the pools' dtype")
+    words, hkv = tree_mask.shape[1], desc.num_kv_heads
+    if workspace is None:
+        need = lib.pa_tree_attention_workspace_size(t, words, h, hkv, d)
+        workspace = _empty((max(need, 256),), torch.uint8, query.device, stream)
+    _require(workspace.dtype is torch.uint8 and workspace.is_contiguous(), "workspace is bytes")
+    _require_here(query, query_start_loc, tree_mask, k_cache, v_cache, block_tables, context_lens, out, workspace)
+    _raise(lib.pa_tree_attention(out.data_ptr(), query.data_ptr(), _token_stride(query, "query"),
+                                 query_start_loc.data_ptr(), t, tree_mask.data_ptr(), words, k_cache.data_ptr(),
+                                 v_cache.data_ptr(), ctypes.byref(desc), block_tables.data_ptr(),
+                                 block_tables.shape[1], context_lens.data_ptr(), s, h, hkv, float(scale),
+                                 workspace.data_ptr(), workspace.numel(), _stream_ptr(stream)),
+           "pa_tree_attention")
+    return out
+
+
+class TreeVerdict(NamedTuple):
+    """What verify_tree makes (device tensors)."""
+    accepted_lens: torch.Tensor  # int32 [S] accepted nodes, node 0 among them
+    path: torch.Tensor           # int32 [T] each sequence's accepted nodes from its first row on, then -1
+    next_tokens: torch.Tensor    # int32 [S]
+
+
+def _row_stride(t: torch.Tensor, name: str) -> int:
+    """Elements from one row of probabilities to the next; a row is contiguous."""
+    rows, width = t.shape
+    _require(width == 1 or t.stride(1) == 1, f"{name}: a row must be contiguous")
+    stride = t.stride(0) if rows > 1 else width
+    _require(stride >= width, f"{name}: rows must not overlap")
+    return stride
+
+
+def verify_tree(tokens: torch.Tensor, parents: torch.Tensor, query_start_loc: torch.Tensor,
+                target_probs: torch.Tensor, draft_probs: Optional[torch.Tensor], accept_uniforms: torch.Tensor,
+                sample_uniforms: torch.Tensor, *, out: Optional[TreeVerdict] = None,
+                stream: Optional[torch.cuda.Stream] = None) -> TreeVerdict:
+    """Which nodes of drafted trees the target accepts, and the token that follows.
+
+    ``target_probs`` and ``draft_probs`` [T][vocab] (f32, f16 or bf16; rows may be
+    padded): row i is the distribution of the token after node i, the draft's the
+    one that i's children were drawn from independently; None for tokens that were
+    not drawn (a lookup's).  ``accept_uniforms`` [T] and ``sample_uniforms`` [S]
+    float32 in [0, 1).  Children are tried in order, a refused one leaves the
+    residual distribution to the next, and the last token is drawn from what is
+    left: the accepted tokens are distributed as the target's own."""
+    lib = native.load()
+    t, i32, f32 = tokens.numel(), torch.int32, torch.float32
+    _require(tokens.dtype is i32 and tokens.shape == (t,) and tokens.is_contiguous() and parents.dtype is i32
+             and parents.shape == (t,) and parents.is_contiguous(), "tokens and parents are int32 [T]")
+    _require(query_start_loc.dtype is i32 and query_start_loc.dim() == 1 and query_start_loc.numel() > 0
+             and query_start_loc.is_contiguous(), "query_start_loc is int32 [num_seqs + 1]")
+    s = query_start_loc.numel() - 1
+    _require(target_probs.dim() == 2 and target_probs.shape[0] == t and target_probs.dtype in DTYPE_CODE,
+             "target_probs is [T][vocab] of f32, f16 or bf16")
+    _require(draft_probs is None or (draft_probs.shape == target_probs.shape
+                                     and draft_probs.dtype is target_probs.dtype),
+             "draft_probs is like target_probs")
+    _require(accept_uniforms.dtype is f32 and accept_uniforms.shape == (t,) and accept_uniforms.is_contiguous()
+             and sample_uniforms.dtype is f32 and sample_uniforms.shape == (s,) and sample_uniforms.is_contiguous(),
+             "accept_uniforms is float32 [T], sample_uniforms float32 [num_seqs]")
+    if out is None:
+        dev = tokens.device
+        out = TreeVerdict(_empty((s,), i32, dev, stream), _empty((t,), i32, dev, stream),
+                          _empty((s,), i32, dev, stream))
+    for x, n in zip(out, (s, t, s)):
+        _require(x.dtype is i32 and x.shape == (n,) and x.is_contiguous(),
+                 "out is (accepted_lens int32 [S], path int32 [T], next_tokens int32 [S])")
+    _require_here(tokens, parents, query_start_loc, target_probs, accept_uniforms, sample_uniforms, *out)
+    draft_ptr, draft_stride = None, 0
+    if draft_probs is not None:
+        _require_here(draft_probs)
+        draft_ptr, draft_stride = draft_probs.data_ptr(), _row_stride(draft_probs, "draft_probs")
+    _raise(lib.pa_verify_tree(tokens.data_ptr(), parents.data_ptr(), query_start_loc.data_ptr(), s, t,
+                              target_probs.data_ptr(), _row_stride(target_probs, "target_probs"), draft_ptr,
+                              draft_stride, target_probs.shape[1], DTYPE_CODE[target_probs.dtype],
+                              accept_uniforms.data_ptr(), sample_uniforms.data_ptr(), out[0].data_ptr(),
+                              out[1].data_ptr(), out[2].data_ptr(), _stream_ptr(stream)), "pa_verify_tree")
+    return out
+
+
+class TreeCommit(NamedTuple):
+    """What commit_tree makes (device tensors)."""
+    context_lens: torch.Tensor          # int32 [S] after the step
+    free_state: Optional[torch.Tensor]  # int32 [2]; None without a ring
+
+
+def commit_tree(k_caches: Sequence[torch.Tensor], v_caches: Sequence[torch.Tensor], query_start_loc: torch.Tensor,
+                path: torch.Tensor, accepted_lens: torch.Tensor, context_lens: torch.Tensor,
+                block_tables: torch.Tensor, *, free_ring: Optional[torch.Tensor] = None,
+                free_state: Optional[torch.Tensor] = None, out: Optional[TreeCommit] = None,
+                stream: Optional[torch.cuda.Stream] = None) -> TreeCommit:
+    """Keep the accepted paths of drafted trees: move their K/V rows together in
+    every layer's pools, cut the lengths to them, and give the blocks behind back to
+    plan_step's ring (``free_ring`` and ``free_state``; None: the host's manager
+    keeps the blocks).  ``path`` and ``accepted_lens`` are verify_tree's.  ``out`` may
+    reuse buffers, context_lens and free_state among them."""
+    lib = native.load()
+    i32 = torch.int32
+    _require(len(k_caches) == len(v_caches) and len(k_caches) > 0, "one K and one V pool per layer")
+    pools = [*k_caches, *v_caches]
+    desc, first = cache_desc(pools[0]), pools[0]
+    for x in pools:
+        _require(x.shape == first.shape and x.dtype is first.dtype and x.is_contiguous(),
+                 "all pools must match and be contiguous")
+    s, t = context_lens.numel(), path.numel()
+    _require(context_lens.dtype is i32 and context_lens.shape == (s,) and context_lens.is_contiguous()
+             and accepted_lens.dtype is i32 and accepted_lens.shape == (s,) and accepted_lens.is_contiguous(),
+             "context_lens and accepted_lens are int32 [num_seqs]")
+    _require(path.dtype is i32 and path.shape == (t,) and path.is_contiguous(), "path is int32 [T]")
+    _require(query_start_loc.dtype is i32 and query_start_loc.shape == (s + 1,) and query_start_loc.is_contiguous(),
+             "query_start_loc is int32 [num_seqs + 1]")
+    _require(block_tables.dtype is i32 and block_tables.dim() == 2 and block_tables.shape[0] == s
+             and block_tables.is_contiguous(), "block_tables is int32 [num_seqs][max_blocks]")
+    _require((free_ring is None) == (free_state is None), "free_ring and free_state come together")
+    if free_ring is not None:
+        _require(free_ring.dtype is i32 and free_ring.dim() == 1 and free_ring.is_contiguous()
+                 and free_state.dtype is i32 and free_state.shape == (2,) and free_state.is_contiguous(),
+                 "free_ring is int32 [ring_size], free_state int32 [2]")
+        _require_here(free_ring, free_state)
+    if out is None:
+        dev = context_lens.device
+        out = TreeCommit(_empty((s,), i32, dev, stream),
+                         None if free_ring is None else _empty((2,), i32, dev, stream))
+    _require(out[0].dtype is i32 and out[0].shape == (s,) and out[0].is_contiguous(),
+             "out is (context_lens int32 [S], free_state int32 [2] or None)")
+    ring_ptr, ring_size, state_ptr, state_out = None, 0, None, None
+    if free_ring is not None:
+        _require(out[1] is not None and out[1].dtype is i32 and out[1].shape == (2,) and out[1].is_contiguous(),
+                 "out is (context_lens int32 [S], free_state int32 [2])")
+        _require_here(out[1])
+        ring_ptr, ring_size, state_ptr, state_out = (free_ring.data_ptr(), free_ring.numel(), free_state.data_ptr(),
+                                                     out[1].data_ptr())
+    _require_here(*pools, query_start_loc, path, accepted_lens, context_lens, block_tables, out[0])
+    n = len(k_caches)
+    kp = (ctypes.c_void_p * n)(*[x.data_ptr() for x in k_caches])
+    vp = (ctypes.c_void_p * n)(*[x.data_ptr() for x in v_caches])
+    _raise(lib.pa_commit_tree(kp, vp, n, ctypes.byref(desc), query_start_loc.data_ptr(), s, t, path.data_ptr(),
+                              accepted_lens.data_ptr(), context_lens.data_ptr(), out[0].data_ptr(),
+                              block_tables.data_ptr(), block_tables.shape[1], ring_ptr, ring_size, state_ptr,
+                              state_out, _stream_ptr(stream)), "pa_commit_tree")
+    return out
+
+
 def copy_blocks(k_caches: Sequence[torch.Tensor], v_caches: Sequence[torch.Tensor], src_dst_pairs: torch.Tensor,
                 stream: Optional[torch.cuda.Stream] = None) -> None:
     """Copy-on-write: copy K and V block pairs[i][0] -> pairs[i][1] in every layer."""

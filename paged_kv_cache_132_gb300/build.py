@@ -18,7 +18,8 @@ LIB_DIR = os.path.join(HERE, "lib")
 LIB_PATH = os.path.join(LIB_DIR, "libpa.so")
 SOURCES = ["pa_api.cu", "cache_ops.cu", "checks.cu", "decode.cu", "decode_f32.cu", "decode_simt_f16.cu", "decode_simt_bf16.cu",
            "decode_mma_f16.cu", "decode_mma_bf16.cu", "pa_noalloc.cu", "prefill.cu", "prefill_f16.cu",
-           "prefill_bf16.cu", "rotary.cu", "step_plan.cu", "prompt.cu", "prompt_f16.cu", "prompt_bf16.cu"]
+           "prefill_bf16.cu", "rotary.cu", "step_plan.cu", "prompt.cu", "prompt_f16.cu", "prompt_bf16.cu",
+           "pa_tree.cu", "tree_step.cu", "tree_verify.cu", "tree_attn.cu", "tree_attn_f16.cu", "tree_attn_bf16.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-lineinfo", "-O3", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
                      "-I", INCLUDE]

@@ -24,6 +24,7 @@
 #include <mutex>
 
 #include "../../include/pa.h"
+#include "host.h"
 #include "kernels.h"
 
 namespace {
@@ -194,6 +195,27 @@ bool encode_pool_map(CUtensorMap* map, const void* base, int dtype, const pa::Po
     return r == CUDA_SUCCESS;
 }
 
+// The pool's rows in groups of eight, as a 4-D tensor {64, 8 rows, d / 64 slabs,
+// groups}: one box = one (block, head) tile, the slabs of 8 rows side by side in shared
+// memory (the tree attention's K and V tiles).
+bool encode_group_map(CUtensorMap* map, const void* base, int dtype, const pa::PoolShape& shape) {
+    const int64_t rows = shape.num_blocks * shape.num_kv_heads * shape.block_size;
+    if (rows <= 0 || rows >= (1LL << 31) || shape.head_dim % 64 != 0 || shape.block_size % 8 != 0) return false;
+    PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+    if (!encode) return false;
+    const CUtensorMapDataType type =
+        dtype == PA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    std::memset(map, 0, sizeof(*map));
+    const cuuint64_t row = (cuuint64_t)shape.head_dim * 2;
+    const cuuint64_t dims[4] = {64, 8, (cuuint64_t)shape.head_dim / 64, (cuuint64_t)rows / 8};
+    const cuuint64_t strides[3] = {row, 128, 8 * row};
+    const cuuint32_t box[4] = {64, 8, (cuuint32_t)shape.head_dim / 64, (cuuint32_t)shape.block_size / 8};
+    const cuuint32_t elem_strides[4] = {1, 1, 1, 1};
+    return encode(map, type, 4, const_cast<void*>(base), dims, strides, box, elem_strides,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Rows [num_tokens][num_heads][d] of 16-bit elements, `token_stride` elements
 // from token to token, as a 3-D tensor {d, heads, tokens}; a box is 64 elements
 // x box_heads heads x box_tokens tokens, 128 bytes per (token, head) row.
@@ -221,7 +243,7 @@ bool encode_rows_map(CUtensorMap* map, const void* base, int dtype, int num_toke
 // activations have a cache of their own: new ones come with every call, and would
 // put the pools' maps out, which stay for the life of a server.
 struct MapKey {
-    int kind;  // 0: pool, 2-D view; 1: pool, decode's view; 2: rows of tokens
+    int kind;  // 0: pool, 2-D view; 1: pool, decode's view; 2: rows of tokens; 3: pool, groups of rows
     int dtype;
     const void* base;
     int64_t a, b, c, d, e, f;
@@ -260,6 +282,16 @@ const CUtensorMap* pool_map(const void* base, int dtype, const pa::PoolShape& sh
     if (const CUtensorMap* m = t_pool_maps.find(key)) return m;
     MapSlot& slot = t_pool_maps.take();
     if (!encode_pool_map(&slot.map, base, dtype, shape, interleave)) return nullptr;
+    slot.key = key;
+    slot.valid = true;
+    return &slot.map;
+}
+
+const CUtensorMap* group_map(const void* base, int dtype, const pa::PoolShape& shape) {
+    const MapKey key{3, dtype, base, shape.num_blocks, shape.num_kv_heads, shape.block_size, shape.head_dim, 0, 0};
+    if (const CUtensorMap* m = t_pool_maps.find(key)) return m;
+    MapSlot& slot = t_pool_maps.take();
+    if (!encode_group_map(&slot.map, base, dtype, shape)) return nullptr;
     slot.key = key;
     slot.valid = true;
     return &slot.map;
@@ -305,6 +337,25 @@ int decode_partition(int64_t num_seqs, int num_kv_heads, int max_context_len, in
 size_t decode_workspace_bytes(int num_seqs, int num_heads, int max_context_len, int partition, int head_dim) {
     return decode_workspace_layout(num_seqs, num_heads, max_parts_for(max_context_len, partition), head_dim).total;
 }
+
+namespace host {
+int elem_bytes(int dtype) { return ::elem_bytes(dtype); }
+bool aligned(const void* p, uintptr_t a) { return ::aligned(p, a); }
+int check_cache(const pa_cache_desc* c, PoolShape* shape) { return ::check_cache(c, shape); }
+int current_device() { return ::current_device(); }
+int* error_word(int dev) { return ::error_word(dev); }
+int sm_count(int dev) { return ::sm_count(dev); }
+int option(int id) { return ::option(id); }
+unsigned long long wait_limit_ns() { return ::wait_limit_ns(); }
+int status_of(cudaError_t e) { return ::status_of(e); }
+const CUtensorMap* rows_map(const void* base, int dtype, int num_tokens, int num_heads, int head_dim,
+                            int64_t token_stride, int box_heads, int box_tokens) {
+    return ::rows_map(base, dtype, num_tokens, num_heads, head_dim, token_stride, box_heads, box_tokens);
+}
+const CUtensorMap* group_map(const void* base, int dtype, const PoolShape& shape) {
+    return ::group_map(base, dtype, shape);
+}
+}  // namespace host
 
 }  // namespace pa
 

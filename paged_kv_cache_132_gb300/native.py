@@ -20,6 +20,8 @@ PA_F32, PA_F16, PA_BF16 = 0, 1, 2
 DEVERR_BLOCK_ID, DEVERR_SLOT, DEVERR_CONTEXT_LEN, DEVERR_COPY_PAIR, DEVERR_TIMEOUT = 0x1, 0x2, 0x4, 0x8, 0x10
 DEVERR_DUP_SLOT, DEVERR_PAIR_CONFLICT = 0x20, 0x40  # checked mode only
 DEVERR_POSITION, DEVERR_STEP = 0x80, 0x100
+DEVERR_TREE, DEVERR_PROBS = 0x200, 0x400
+MAX_TREE_NODES = 1024  # PA_MAX_TREE_NODES
 OPT_DEBUG_CHECKS, OPT_DECODE_KERNEL, OPT_DROP_FIRST_FILL = 0, 1, 2  # pa_option
 NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024  # PA_NOALLOC_SCRATCH_BYTES
 
@@ -79,6 +81,14 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                                             ctypes.c_float, vp, sz, vp]
         lib.pa_prompt_attention_workspace_size.argtypes = [i32, i32, i32, i32]
         lib.pa_prompt_attention_workspace_size.restype = sz
+        lib.pa_plan_tree.argtypes = [vp, vp, vp, i32, i32, vp, vp, i32, vp]
+        lib.pa_tree_attention_workspace_size.argtypes = [i32, i32, i32, i32, i32]
+        lib.pa_tree_attention_workspace_size.restype = sz
+        lib.pa_tree_attention.argtypes = [vp, vp, i64, vp, i32, vp, i32, vp, vp, desc, vp, i32, vp, i32, i32, i32,
+                                          ctypes.c_float, vp, sz, vp]
+        lib.pa_verify_tree.argtypes = [vp, vp, vp, i32, i32, vp, i64, vp, i64, i32, i32, vp, vp, vp, vp, vp, vp]
+        lib.pa_commit_tree.argtypes = [ctypes.POINTER(vp), ctypes.POINTER(vp), i32, desc, vp, i32, i32, vp, vp, vp, vp,
+                                       vp, i32, vp, i32, vp, vp, vp]
         lib.pa_get_device_error.argtypes = [vp, ctypes.POINTER(i32)]
         lib.pa_status_string.argtypes = [ctypes.c_int]
         lib.pa_status_string.restype = ctypes.c_char_p
@@ -86,8 +96,9 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.pa_set_option.argtypes = [ctypes.c_int, ctypes.c_int]
         lib.pa_get_option.argtypes = [ctypes.c_int]
         for name in ("pa_reshape_and_cache", "pa_decode", "pa_decode_noalloc", "pa_copy_blocks",
-                     "pa_swap_blocks", "pa_prefill", "pa_prompt_attention", "pa_rotary_and_cache", "pa_plan_step", "pa_get_device_error", "pa_abi_version", "pa_set_option",
-                     "pa_get_option"):
+                     "pa_swap_blocks", "pa_prefill", "pa_prompt_attention", "pa_rotary_and_cache", "pa_plan_step",
+                     "pa_plan_tree", "pa_tree_attention", "pa_verify_tree", "pa_commit_tree", "pa_get_device_error",
+                     "pa_abi_version", "pa_set_option", "pa_get_option"):
             getattr(lib, name).restype = ctypes.c_int
         _lib = lib
         return lib
