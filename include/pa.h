@@ -516,7 +516,7 @@ int pa_tree_attention(void *out, const void *query, int64_t query_stride, const 
  *   path              device, int32 [num_tokens]: from each sequence's first row on the
  *                     accepted nodes, then -1; other rows are not written
  *   next_tokens       device, int32 [num_seqs]
- * Sums are exact to 2^-52 a weight, whatever the order.  A sequence without nodes or
+ * Sums are exact to 2^-56 a weight, whatever the order.  A sequence without nodes or
  * with bad lengths gets accepted length 0 and token -1; a row without any weight sets
  * PA_DEVERR_PROBS and gives token -1.  vocab_size <= 2^20, else PA_ERR_UNSUPPORTED.
  */

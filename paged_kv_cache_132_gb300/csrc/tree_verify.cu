@@ -15,11 +15,14 @@
 // rows of a draft (tokens from a lookup, say) q is 1 at the child and 0 elsewhere: x is
 // accepted if u s < p(x), and a refusal takes p(x) out of s and of the row.
 //
-// Weights are whole numbers: p and q in units of 2^-52 (exact from 2^-29 up, cut below),
-// added in 64 bits.  A sum is then the same in any order, so the split of a row over
-// threads and CTAs changes no token, and no token on a border of the cumulative weights
-// is missed by a rounding: binary32 sums move the borders of 128 000 tokens by 2^-24,
-// binary64 additions run at a sixtieth of the rate of integer ones.
+// Weights are added as whole numbers, in units of 2^-56.  A sum is then the same in any
+// order, so the split of a row over threads and CTAs changes no token, and no token on a
+// border of the cumulative weights is missed by a rounding: binary32 sums move the borders
+// of 128 000 tokens by 2^-24, binary64 additions run at a sixtieth of the rate.  A weight
+// is d + e, the difference in binary32 and its rounding error (exact: e = (p - d) - q for
+// p >= q), and falls into three whole numbers by additions alone: d + 2 has its multiple
+// of 2^-22 in the low bits, what is left its multiples of 2^-44 and then of 2^-56.  A
+// lane adds the words up and takes the constants out once per segment.
 //
 // A cluster of CTAs per sequence, one CTA for large batches, shares the row's segments
 // of 512 entries.  All its CTAs walk the tree alike (one warp, from probabilities of the
@@ -54,30 +57,60 @@ __device__ inline float as_float(__nv_bfloat16 x) { return __bfloat162float(x); 
 // A probability: NaN and negative entries count as 0, those above 1 as 1.
 __device__ inline float clean(float x) { return fminf(fmaxf(x, 0.f), 1.f); }
 
-// x in [0, 1] in units of 2^-52: the 24-bit significand, shifted.
-__device__ inline u64 fixed52(float x) {
-    const uint32_t b = __float_as_uint(clean(x));
-    const uint32_t m = (b & 0x7fffffu) | 0x800000u;
-    const int sh = (int)(b >> 23) - (127 + 23 - 52);  // -98 .. 29
-    const uint32_t lo = sh >= 0 ? m << sh : m >> min(-sh, 31);
-    const uint32_t hi = __funnelshift_l(m, 0u, max(sh, 0));
-    return ((u64)hi << 32) | lo;
-}
-// Sums of weights: rows that add up to 4096 and more (no probabilities) stay at the end.
+// Sum of weights d + e, d in [0, 1], |e| <= 2^-24, in units of 2^-56.
+struct Sum {
+    static constexpr float A = 2.f;               // [2, 4): steps of 2^-22
+    static constexpr float B = 0x1.8p-21f;        // steps of 2^-44, +- 2^-22
+    static constexpr float C = 0x1.8p-33f;        // steps of 2^-56, +- 2^-34
+    uint32_t a = 0, b = 0, c = 0;
+    int count = 0;
+    __device__ inline void add(float d, float e) {
+        const float x = __fadd_rn(d, A);
+        const float r = __fadd_rn(__fsub_rn(d, __fsub_rn(x, A)), e);
+        const float y = __fadd_rn(r, B);
+        const float z = __fadd_rn(__fsub_rn(r, __fsub_rn(y, B)), C);
+        a += __float_as_uint(x);
+        b += __float_as_uint(y);
+        c += __float_as_uint(z);
+        ++count;
+    }
+    __device__ inline u64 value() const {
+        const int64_t hi = (int32_t)(a - count * __float_as_uint(A)), mid = (int32_t)(b - count * __float_as_uint(B)),
+                      lo = (int32_t)(c - count * __float_as_uint(C));
+        const int64_t v = hi * (1LL << 34) + mid * (1LL << 12) + lo;
+        return v > 0 ? (u64)v : 0;
+    }
+};
+constexpr double kUnit = 0x1p-56;
+// Rows that add up to 256 and more (no probabilities) stay at the end.
 __device__ inline u64 add_sat(u64 a, u64 b) {
     const u64 c = a + b;
     return c < a ? ~0ull : c;
 }
 
-// max(p - c q, 0); c in units of 2^-53, below 2^11.
+// max(p - c q, 0), c = hi + lo.
 struct Weights {
-    bool use_q, c_is_1;
-    u64 c;
-    __device__ inline u64 operator()(float p, float q) const {
-        const u64 a = fixed52(p);
-        if (!use_q) return a;
-        const u64 b = c_is_1 ? fixed52(q) : __umul64hi(fixed52(q) << 11, c);
-        return a > b ? a - b : 0;
+    bool use_q;
+    float hi, lo;  // hi = 1 and lo = 0 after the first refusal
+    __device__ inline void add(Sum& sum, float p, float q) const {
+        p = clean(p);
+        if (!use_q) {
+            sum.add(p, 0.f);
+        } else if (hi == 1.f && lo == 0.f) {
+            const float b = fminf(fmaxf(q, 0.f), p);
+            const float d = __fsub_rn(p, b);
+            sum.add(d, __fsub_rn(__fsub_rn(p, d), b));
+        } else {
+            const float x = clean(q), b = __fmul_rn(x, hi);
+            const float d = __fsub_rn(p, b);
+            const float e = __fsub_rn(__fsub_rn(__fsub_rn(p, d), b), __fmaf_rn(x, lo, __fmaf_rn(x, hi, -b)));
+            if (d > 0.f) sum.add(d, fmaxf(e, -d));
+        }
+    }
+    __device__ inline u64 one(float p, float q) const {
+        Sum sum;
+        add(sum, p, q);
+        return sum.value();
     }
 };
 
@@ -93,14 +126,15 @@ struct Row {
 
 // N entries of a row from `e` on (a multiple of N before the skew); 0 outside it.
 template <typename T, int N>
-__device__ inline void load_entries(const Row<T>& r, int skew, int e, int vocab, float (&x)[N]) {
+__device__ inline uint4 load_vector(const Row<T>& r, int skew, int e, int vocab) {
     static_assert(N * sizeof(T) == 16, "one vector");
-    if (skew == r.skew && e >= 0 && e + N <= vocab) {
-        unpack16(__ldg(reinterpret_cast<const uint4*>(r.at + e)), x, T());
-    } else {
+    if (skew == r.skew && e >= 0 && e + N <= vocab) return __ldg(reinterpret_cast<const uint4*>(r.at + e));
+    T x[N];
 #pragma unroll
-        for (int k = 0; k < N; ++k) x[k] = e + k >= 0 && e + k < vocab ? as_float(r.at[e + k]) : 0.f;
-    }
+    for (int k = 0; k < N; ++k) x[k] = e + k >= 0 && e + k < vocab ? r.at[e + k] : T(0.f);
+    uint4 w;
+    memcpy(&w, x, 16);
+    return w;
 }
 
 struct Shared {
@@ -127,31 +161,45 @@ struct Verify {
     __device__ inline int segments(int skew) const { return (skew + p.vocab + kSegment - 1) / kSegment; }
     __device__ inline int per_cta(int skew) const { return (segments(skew) + ranks - 1) / ranks; }
 
-    // Sums of the weights of row `node` by segment, and of all this CTA's.
-    __device__ void sums(int node, const Weights& w) {
+    // Sums of the weights of row `node` by segment, and of all this CTA's.  A warp has
+    // eight vectors of every lane in flight: one to four segments.
+    template <bool USE_Q>
+    __device__ void sums_of(int node, const Weights& w) {
         constexpr int N = 16 / (int)sizeof(T), V = kSegment / (32 * N);  // entries of a vector, vectors of a lane
+        constexpr int SEGS = 8 / (V * (USE_Q ? 2 : 1));
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
         const Row<T> a(p.target, (row0 + node) * p.target_stride);
-        const Row<T> b(w.use_q ? p.draft : p.target, (row0 + node) * (w.use_q ? p.draft_stride : p.target_stride));
+        const Row<T> b(USE_Q ? p.draft : p.target, (row0 + node) * (USE_Q ? p.draft_stride : p.target_stride));
         const int each = per_cta(a.skew), s0 = rank * each, s1 = min(s0 + each, segments(a.skew));
         u64 mine = 0;
-        for (int s = s0 + warp; s < s1; s += kWarps) {
-            float x[V][N], y[V][N];
+        for (int s = s0 + warp * SEGS; s < s1; s += kWarps * SEGS) {
+            uint4 x[SEGS * V], y[SEGS * V];
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
+            for (int v = 0; v < SEGS * V; ++v) {
                 const int e = s * kSegment + (v * 32 + lane) * N - a.skew;
-                load_entries<T, N>(a, a.skew, e, p.vocab, x[v]);
-                if (w.use_q) load_entries<T, N>(b, a.skew, e, p.vocab, y[v]);
+                x[v] = load_vector<T, N>(a, a.skew, e, p.vocab);
+                if (USE_Q) y[v] = load_vector<T, N>(b, a.skew, e, p.vocab);
             }
-            u64 sum = 0;
 #pragma unroll
-            for (int v = 0; v < V; ++v)
+            for (int g = 0; g < SEGS; ++g) {
+                Sum lane_sum;
 #pragma unroll
-                for (int k = 0; k < N; ++k) sum += w(x[v][k], y[v][k]);
+                for (int v = g * V; v < (g + 1) * V; ++v) {
+                    float f[N], h[N];
+                    unpack16(x[v], f, T());
+                    if (USE_Q) unpack16(y[v], h, T());
 #pragma unroll
-            for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);  // below 2^62
-            if (lane == 0) sm.segment[s - s0] = sum;
-            mine = add_sat(mine, sum);
+                    for (int k = 0; k < N; ++k) w.add(lane_sum, f[k], USE_Q ? h[k] : 0.f);
+                }
+                u64 sum = lane_sum.value();
+#pragma unroll
+                for (int d = 16; d >= 1; d >>= 1) sum = add_sat(sum, __shfl_xor_sync(kAll, sum, d));
+                // past the CTA's last segment: the next one's, or nothing
+                if (s + g < s1) {
+                    if (lane == 0) sm.segment[s + g - s0] = sum;
+                    mine = add_sat(mine, sum);
+                }
+            }
         }
         if (lane == 0) sm.warp_sum[warp] = mine;
         __syncthreads();
@@ -161,6 +209,14 @@ struct Verify {
             sm.total = t;
         }
         __syncthreads();
+    }
+    __device__ void sums(int node, const Weights& w) {
+        if (!w.use_q)
+            sums_of<false>(node, w);
+        else if (w.hi == 1.f && w.lo == 0.f)
+            sums_of<true>(node, Weights{true, 1.f, 0.f});  // without the products
+        else
+            sums_of<true>(node, w);
     }
 
     // Is x among the tokens refused at the last accepted node?  (warp)
@@ -201,8 +257,8 @@ struct Verify {
         for (int v = 0; v < V && token < 0; ++v) {
             const int e = (s0 + seg) * kSegment + (v * 32 + lane) * N - a.skew;
             float x[N], y[N];
-            load_entries<T, N>(a, a.skew, e, p.vocab, x);
-            if (w.use_q) load_entries<T, N>(b, a.skew, e, p.vocab, y);
+            unpack16(load_vector<T, N>(a, a.skew, e, p.vocab), x, T());
+            unpack16(load_vector<T, N>(b, a.skew, e, p.vocab), y, T());
             for (int k = 0; k < sm.num_refused; ++k) {
                 const int gone = sm.refused[k] - e;
 #pragma unroll
@@ -211,7 +267,7 @@ struct Verify {
             }
             u64 sum = 0;
 #pragma unroll
-            for (int k = 0; k < N; ++k) sum += w(x[k], y[k]);
+            for (int k = 0; k < N; ++k) sum += w.one(x[k], y[k]);
             u64 below = sum;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
@@ -225,7 +281,7 @@ struct Verify {
                     u64 cum = below - sum;
 #pragma unroll
                     for (int k = 0; k < N; ++k) {
-                        cum += w(x[k], y[k]);
+                        cum += w.one(x[k], y[k]);
                         if (token < 0 && cum > left) token = e + k;
                     }
                 }
@@ -239,7 +295,7 @@ struct Verify {
 };
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) tree_verify_kernel(const __grid_constant__ TreeVerifyParams p) {
+__global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(const __grid_constant__ TreeVerifyParams p) {
     __shared__ Shared sm;
     const cg::cluster_group cluster = cg::this_cluster();
     const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -283,7 +339,8 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(const __grid_cons
     bool spent = false;    // nothing is left of the target's row: the token comes from the row itself
     u64 own = 0, before = 0, total = 0;
     auto weights = [&](bool use_q, double factor) {
-        return Weights{use_q, factor == 1., use_q ? (u64)__double2ull_rn(fmin(factor, 2047.) * 9007199254740992.) : 0};
+        const float hi = (float)factor;
+        return Weights{use_q, hi, (float)(factor - hi)};
     };
     // The sums of the whole row: this CTA's, those of the CTAs before it, of all.
     auto share = [&] {
@@ -357,9 +414,9 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(const __grid_cons
                     for (int k = 0; k < sm.num_refused; ++k) {
                         const int x = sm.refused[k], seg = (x + a.skew) / kSegment - s0;
                         if (seg < 0 || seg >= each) continue;
-                        const u64 gone = fixed52(as_float(a.at[x]));
-                        sm.segment[seg] -= gone;
-                        sm.total = sm.total == ~0ull ? sm.total : sm.total - gone;
+                        const u64 gone = Weights{false, 0.f, 0.f}.one(as_float(a.at[x]), 0.f);
+                        sm.segment[seg] -= min(gone, sm.segment[seg]);
+                        sm.total = sm.total == ~0ull ? sm.total : sm.total - min(gone, sm.total);
                     }
                 __syncthreads();
             }
@@ -389,7 +446,7 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(const __grid_cons
             return;
         }
         // A refusal's sum.
-        sum = (double)total * 0x1p-52;
+        sum = (double)total * kUnit;
         spent = total == 0;
         __syncthreads();
     }

@@ -1,5 +1,5 @@
 """Verification of drafted trees against its rules in 64 bits, token for token: the
-sums of weights are exact to 2^-52 a weight, so a token differs only where a random
+sums of weights are exact to 2^-52 a weight and better, so a token differs only where a random
 number falls that close to a border."""
 import math
 import random
