@@ -20,9 +20,11 @@
 // border of the cumulative weights is missed by a rounding: binary32 sums move the borders
 // of 128 000 tokens by 2^-24, binary64 additions run at a sixtieth of the rate.  A weight
 // is d + e, the difference in binary32 and its rounding error (exact: e = (p - d) - q for
-// p >= q), and falls into three whole numbers by additions alone: d + 2 has its multiple
-// of 2^-22 in the low bits, what is left its multiples of 2^-44 and then of 2^-56.  A
-// lane adds the words up and takes the constants out once per segment.
+// p >= q), and falls into two whole numbers by additions alone: d + 1 has its multiple of
+// 2^-23 in the low bits, what is left of it its multiple of 2^-45.  A lane adds those
+// words, and what is left then (2^-46 and less) in binary32, over its 16 entries of a
+// segment, and takes the constants out once; which entries are a lane's goes by the row
+// alone.  Two entries go through the additions of one instruction.
 //
 // A cluster of CTAs per sequence, one CTA for large batches, shares the row's segments
 // of 512 entries.  All its CTAs walk the tree alike (one warp, from probabilities of the
@@ -34,6 +36,7 @@
 #include <cooperative_groups.h>
 #include <type_traits>
 
+#include "attn_common.cuh"
 #include "common.cuh"
 #include "tree.h"
 
@@ -47,6 +50,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kNodes = 1024;        // PA_MAX_TREE_NODES
 constexpr int kSegment = 512;       // entries of a segment: 16 a lane
 constexpr int kSegments = kMaxVocab / kSegment + 1;
+constexpr int kRanks = 8;            // CTAs of a cluster at most
 constexpr unsigned kAll = 0xffffffffu;
 using u64 = unsigned long long;
 
@@ -55,29 +59,33 @@ __device__ inline float as_float(__half x) { return __half2float(x); }
 __device__ inline float as_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 
 // A probability: NaN and negative entries count as 0, those above 1 as 1.
-__device__ inline float clean(float x) { return fminf(fmaxf(x, 0.f), 1.f); }
+__device__ inline float clean(float x) { return __saturatef(x); }
 
-// Sum of weights d + e, d in [0, 1], |e| <= 2^-24, in units of 2^-56.
+// Sum of up to 16 weights d + e, d in [0, 1], |e| <= 2^-24, in units of 2^-56.
 struct Sum {
-    static constexpr float A = 2.f;               // [2, 4): steps of 2^-22
-    static constexpr float B = 0x1.8p-21f;        // steps of 2^-44, +- 2^-22
-    static constexpr float C = 0x1.8p-33f;        // steps of 2^-56, +- 2^-34
-    uint32_t a = 0, b = 0, c = 0;
+    static constexpr float A = 1.f;         // [1, 2]: steps of 2^-23
+    static constexpr float B = 0x1.8p-22f;  // steps of 2^-45, +- 2^-23
+    uint32_t a = 0, b = 0;
+    float rest0 = 0.f, rest1 = 0.f;
     int count = 0;
-    __device__ inline void add(float d, float e) {
-        const float x = __fadd_rn(d, A);
-        const float r = __fadd_rn(__fsub_rn(d, __fsub_rn(x, A)), e);
-        const float y = __fadd_rn(r, B);
-        const float z = __fadd_rn(__fsub_rn(r, __fsub_rn(y, B)), C);
-        a += __float_as_uint(x);
-        b += __float_as_uint(y);
-        c += __float_as_uint(z);
-        ++count;
+    __device__ inline void add2(float d0, float d1, float e0, float e1) {
+        float x0 = d0, x1 = d1;
+        add2_rn(x0, x1, A, A);
+        a += __float_as_uint(x0) + __float_as_uint(x1);
+        add2_rn(x0, x1, -A, -A);
+        sub2_rn(d0, d1, x0, x1);
+        add2_rn(d0, d1, e0, e1);
+        x0 = d0, x1 = d1;
+        add2_rn(x0, x1, B, B);
+        b += __float_as_uint(x0) + __float_as_uint(x1);
+        add2_rn(x0, x1, -B, -B);
+        sub2_rn(d0, d1, x0, x1);
+        add2_rn(rest0, rest1, d0, d1);
+        count += 2;
     }
     __device__ inline u64 value() const {
-        const int64_t hi = (int32_t)(a - count * __float_as_uint(A)), mid = (int32_t)(b - count * __float_as_uint(B)),
-                      lo = (int32_t)(c - count * __float_as_uint(C));
-        const int64_t v = hi * (1LL << 34) + mid * (1LL << 12) + lo;
+        const int64_t hi = (int32_t)(a - count * __float_as_uint(A)), mid = (int32_t)(b - count * __float_as_uint(B));
+        const int64_t v = hi * (1LL << 33) + mid * (1LL << 11) + __float2int_rn((rest0 + rest1) * 0x1p56f);
         return v > 0 ? (u64)v : 0;
     }
 };
@@ -88,28 +96,48 @@ __device__ inline u64 add_sat(u64 a, u64 b) {
     return c < a ? ~0ull : c;
 }
 
+// Sum over the lanes, each below 2^61, by three 32-bit ones of 27 bits.
+__device__ inline u64 sum_of_lanes(u64 x) {
+    const uint32_t a = __reduce_add_sync(kAll, (uint32_t)x & 0x7ffffffu);
+    const uint32_t b = __reduce_add_sync(kAll, (uint32_t)(x >> 27) & 0x7ffffffu);
+    const uint32_t c = __reduce_add_sync(kAll, (uint32_t)(x >> 54));
+    return c < 960 ? ((u64)c << 54) + ((u64)b << 27) + a : ~0ull;
+}
+
 // max(p - c q, 0), c = hi + lo.
+enum Kind { kRow, kDifference, kGeneral };  // c = 0, 1, any
 struct Weights {
-    bool use_q;
-    float hi, lo;  // hi = 1 and lo = 0 after the first refusal
-    __device__ inline void add(Sum& sum, float p, float q) const {
-        p = clean(p);
-        if (!use_q) {
-            sum.add(p, 0.f);
-        } else if (hi == 1.f && lo == 0.f) {
-            const float b = fminf(fmaxf(q, 0.f), p);
-            const float d = __fsub_rn(p, b);
-            sum.add(d, __fsub_rn(__fsub_rn(p, d), b));
+    Kind kind;
+    float hi, lo;
+    // d + e of one entry, d in the place of p.
+    __device__ inline void general(float& p, float q, float& e) const {
+        const float x = clean(q), b = __fmul_rn(x, hi), d = __fsub_rn(p, b);
+        e = __fsub_rn(__fsub_rn(__fsub_rn(p, d), b), __fmaf_rn(x, lo, __fmaf_rn(x, hi, -b)));
+        e = d > 0.f ? fmaxf(e, -d) : 0.f;
+        p = fmaxf(d, 0.f);
+    }
+    template <Kind KIND>
+    __device__ inline void add2(Sum& sum, float p0, float p1, float q0, float q1) const {
+        p0 = clean(p0), p1 = clean(p1);
+        if constexpr (KIND == kRow) {
+            sum.add2(p0, p1, 0.f, 0.f);
+        } else if constexpr (KIND == kDifference) {
+            q0 = fminf(clean(q0), p0), q1 = fminf(clean(q1), p1);
+            float d0 = p0, d1 = p1;
+            sub2_rn(d0, d1, q0, q1);
+            sub2_rn(p0, p1, d0, d1);
+            sub2_rn(p0, p1, q0, q1);
+            sum.add2(d0, d1, p0, p1);
         } else {
-            const float x = clean(q), b = __fmul_rn(x, hi);
-            const float d = __fsub_rn(p, b);
-            const float e = __fsub_rn(__fsub_rn(__fsub_rn(p, d), b), __fmaf_rn(x, lo, __fmaf_rn(x, hi, -b)));
-            if (d > 0.f) sum.add(d, fmaxf(e, -d));
+            float e0, e1;
+            general(p0, q0, e0);
+            general(p1, q1, e1);
+            sum.add2(p0, p1, e0, e1);
         }
     }
     __device__ inline u64 one(float p, float q) const {
-        Sum sum;
-        add(sum, p, q);
+        Sum sum;  // the general form has the same d and e for c = 0 and 1
+        add2<kGeneral>(sum, p, 0.f, q, 0.f);
         return sum.value();
     }
 };
@@ -124,31 +152,57 @@ struct Row {
     }
 };
 
-// N entries of a row from `e` on (a multiple of N before the skew); 0 outside it.
+// Vector v of COUNT, 32 lanes x N entries apart, from entry `e` of the row on.
+template <typename T, int N, int COUNT>
+__device__ inline void load_inside(const Row<T>& r, int e, uint4 (&x)[COUNT]) {
+#pragma unroll
+    for (int v = 0; v < COUNT; ++v) x[v] = __ldg(reinterpret_cast<const uint4*>(r.at + e) + v * 32);
+}
+// N entries one by one, 0 outside the row.
 template <typename T, int N>
-__device__ inline uint4 load_vector(const Row<T>& r, int skew, int e, int vocab) {
-    static_assert(N * sizeof(T) == 16, "one vector");
-    if (skew == r.skew && e >= 0 && e + N <= vocab) return __ldg(reinterpret_cast<const uint4*>(r.at + e));
+__device__ __noinline__ uint4 load_entries(const T* at, int e, int vocab) {
     T x[N];
 #pragma unroll
-    for (int k = 0; k < N; ++k) x[k] = e + k >= 0 && e + k < vocab ? r.at[e + k] : T(0.f);
+    for (int k = 0; k < N; ++k) x[k] = e + k >= 0 && e + k < vocab ? at[e + k] : T(0.f);
     uint4 w;
     memcpy(&w, x, 16);
     return w;
+}
+// The same at a row's ends, or with another skew than the vectors': all vectors inside
+// the row first, together, then what lies across its ends.
+template <typename T, int N, int COUNT>
+__device__ inline void load_edge(const Row<T>& r, int skew, int e, int vocab, uint4 (&x)[COUNT]) {
+    static_assert(N * sizeof(T) == 16, "one vector");
+    bool across = false;
+#pragma unroll
+    for (int v = 0; v < COUNT; ++v) {
+        const int at = e + v * 32 * N;
+        const bool whole = skew == r.skew && at >= 0 && at + N <= vocab;
+        x[v] = make_uint4(0u, 0u, 0u, 0u);
+        if (whole) x[v] = __ldg(reinterpret_cast<const uint4*>(r.at + at));
+        across |= !whole && at + N > 0 && at < vocab;
+    }
+    if (!__any_sync(kAll, across)) return;
+#pragma unroll
+    for (int v = 0; v < COUNT; ++v) {
+        const int at = e + v * 32 * N;
+        if (at + N > 0 && at < vocab && !(skew == r.skew && at >= 0 && at + N <= vocab))
+            x[v] = load_entries<T, N>(r.at, at, vocab);
+    }
 }
 
 struct Shared {
     int parent[kNodes], token[kNodes];
     float p[kNodes], q[kNodes], u[kNodes];
-    int refused[kNodes];    // tokens refused at the last accepted node (no draft)
+    bool first[kNodes];        // accepted with c = 0, s = 1
+    int refused[kNodes];       // tokens refused at the last accepted node (no draft)
     u64 segment[kSegments];
     u64 warp_sum[kWarps];
-    u64 total;              // of this CTA's segments (read by the cluster)
-    int go;                 // what comes next: 0 the token, 1 a sum
+    u64 totals[2][kRanks];     // of every CTA's segments, by the parity of the sums' number
+    int go;                    // what comes next: 0 the token, 1 a sum
     int now, num_refused;
     double c;
-    int again;              // the last sum is not the one that the token needs
-    int use_q;
+    int again;                 // the last sum is not the one that the token needs
 };
 
 template <typename T>
@@ -161,62 +215,100 @@ struct Verify {
     __device__ inline int segments(int skew) const { return (skew + p.vocab + kSegment - 1) / kSegment; }
     __device__ inline int per_cta(int skew) const { return (segments(skew) + ranks - 1) / ranks; }
 
-    // Sums of the weights of row `node` by segment, and of all this CTA's.  A warp has
-    // eight vectors of every lane in flight: one to four segments.
-    template <bool USE_Q>
+    // Do segments [s, end) lie in the rows, on vectors of both?
+    __device__ inline bool inside(const Row<T>& a, const Row<T>& b, int s, int end) const {
+        return a.skew == b.skew && s * kSegment >= a.skew && end * kSegment - a.skew <= p.vocab;
+    }
+
+    // Entries e .. e + N - 1 without the refused tokens among them.
+    template <int N>
+    __device__ inline void take_out(float (&x)[N], int e, int num_refused) const {
+        for (int k = 0; k < num_refused; ++k) {
+            const int gone = sm.refused[k] - e;
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                if (j == gone) x[j] = 0.f;
+        }
+    }
+
+    // Sums of the weights of row `node` by segment, and of this warp's.
+    template <Kind KIND>
     __device__ void sums_of(int node, const Weights& w) {
+        constexpr bool USE_Q = KIND != kRow;
         constexpr int N = 16 / (int)sizeof(T), V = kSegment / (32 * N);  // entries of a vector, vectors of a lane
-        constexpr int SEGS = 8 / (V * (USE_Q ? 2 : 1));
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
         const Row<T> a(p.target, (row0 + node) * p.target_stride);
         const Row<T> b(USE_Q ? p.draft : p.target, (row0 + node) * (USE_Q ? p.draft_stride : p.target_stride));
         const int each = per_cta(a.skew), s0 = rank * each, s1 = min(s0 + each, segments(a.skew));
+        const int num_refused = sm.num_refused;
         u64 mine = 0;
-        for (int s = s0 + warp * SEGS; s < s1; s += kWarps * SEGS) {
-            uint4 x[SEGS * V], y[SEGS * V];
-#pragma unroll
-            for (int v = 0; v < SEGS * V; ++v) {
-                const int e = s * kSegment + (v * 32 + lane) * N - a.skew;
-                x[v] = load_vector<T, N>(a, a.skew, e, p.vocab);
-                if (USE_Q) y[v] = load_vector<T, N>(b, a.skew, e, p.vocab);
+#pragma unroll 1
+        for (int s = s0 + warp; s < s1; s += kWarps) {
+            uint4 x[V], y[V];
+            const int e0 = s * kSegment + lane * N - a.skew;
+            if (inside(a, b, s, s + 1)) {
+                load_inside<T, N>(a, e0, x);
+                if (USE_Q) load_inside<T, N>(b, e0, y);
+            } else {
+                load_edge<T, N>(a, a.skew, e0, p.vocab, x);
+                if (USE_Q) load_edge<T, N>(b, a.skew, e0, p.vocab, y);
             }
+            // Refused tokens in this segment (rarely one)?
+            bool some_gone = false;
+            for (int k = 0; k < num_refused; ++k) some_gone |= (sm.refused[k] + a.skew) / kSegment == s;
+            Sum lane_sum;
 #pragma unroll
-            for (int g = 0; g < SEGS; ++g) {
-                Sum lane_sum;
+            for (int v = 0; v < V; ++v) {
+                float f[N], h[N];
+                unpack16(x[v], f, T());
+                if (USE_Q)
+                    unpack16(y[v], h, T());
+                else if (some_gone)
+                    take_out(f, e0 + v * 32 * N, num_refused);
 #pragma unroll
-                for (int v = g * V; v < (g + 1) * V; ++v) {
-                    float f[N], h[N];
-                    unpack16(x[v], f, T());
-                    if (USE_Q) unpack16(y[v], h, T());
-#pragma unroll
-                    for (int k = 0; k < N; ++k) w.add(lane_sum, f[k], USE_Q ? h[k] : 0.f);
-                }
-                u64 sum = lane_sum.value();
-#pragma unroll
-                for (int d = 16; d >= 1; d >>= 1) sum = add_sat(sum, __shfl_xor_sync(kAll, sum, d));
-                // past the CTA's last segment: the next one's, or nothing
-                if (s + g < s1) {
-                    if (lane == 0) sm.segment[s + g - s0] = sum;
-                    mine = add_sat(mine, sum);
-                }
+                for (int k = 0; k < N; k += 2)
+                    w.template add2<KIND>(lane_sum, f[k], f[k + 1], USE_Q ? h[k] : 0.f, USE_Q ? h[k + 1] : 0.f);
             }
+            const u64 sum = sum_of_lanes(lane_sum.value());
+            if (lane == 0) sm.segment[s - s0] = sum;
+            mine = add_sat(mine, sum);
         }
         if (lane == 0) sm.warp_sum[warp] = mine;
         __syncthreads();
-        if (threadIdx.x == 0) {
-            u64 t = 0;
-            for (int k = 0; k < kWarps; ++k) t = add_sat(t, sm.warp_sum[k]);
-            sm.total = t;
-        }
-        __syncthreads();
     }
     __device__ void sums(int node, const Weights& w) {
-        if (!w.use_q)
-            sums_of<false>(node, w);
-        else if (w.hi == 1.f && w.lo == 0.f)
-            sums_of<true>(node, Weights{true, 1.f, 0.f});  // without the products
+        if (w.kind == kRow)
+            sums_of<kRow>(node, w);
+        else if (w.kind == kDifference)
+            sums_of<kDifference>(node, w);
         else
-            sums_of<true>(node, w);
+            sums_of<kGeneral>(node, w);
+    }
+
+    // The sum of the whole row; this CTA's and those of the CTAs before it.  Every CTA
+    // writes its own to all of them, so that none reads another's memory behind the
+    // cluster's barrier; the next sums go to the other half of the array.
+    __device__ u64 share(const cg::cluster_group& cluster, int number, u64& own, u64& before) {
+        u64* const totals = sm.totals[number & 1];
+        if (threadIdx.x < 32) {
+            u64 t = threadIdx.x < kWarps ? sm.warp_sum[threadIdx.x] : 0;
+#pragma unroll
+            for (int d = kWarps / 2; d >= 1; d >>= 1) t = add_sat(t, __shfl_xor_sync(kAll, t, d));
+            t = __shfl_sync(kAll, t, 0);
+            if ((int)threadIdx.x < ranks) *cluster.map_shared_rank(&totals[rank], (int)threadIdx.x) = t;
+        }
+        if (ranks > 1)
+            cluster.sync();
+        else
+            __syncthreads();
+        u64 total = 0;
+        own = totals[rank];
+        before = 0;
+        for (int r = 0; r < ranks; ++r) {
+            if (r < rank) before = add_sat(before, totals[r]);
+            total = add_sat(total, totals[r]);
+        }
+        return total;
     }
 
     // Is x among the tokens refused at the last accepted node?  (warp)
@@ -226,71 +318,86 @@ struct Verify {
         return __any_sync(kAll, there);
     }
 
+    // Inclusive sums over the lanes.
+    static __device__ inline u64 scan(u64 x, int lane) {
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const u64 up = __shfl_up_sync(kAll, x, d);
+            if (lane >= d) x = add_sat(x, up);
+        }
+        return x;
+    }
+
     // The first entry of the CTA's segments whose cumulative weight exceeds `left`, by
-    // one warp; entries of refused tokens weigh nothing.
+    // one warp.  (The whole numbers of an entry or a vector may differ from a segment's by
+    // its last units: where they leave `left` beyond them all, the last entry with a weight.)
     __device__ int find(int node, const Weights& w, u64 left, int lane) {
         constexpr int N = 16 / (int)sizeof(T), V = kSegment / (32 * N);
+        const bool use_q = w.kind != kRow;
         const Row<T> a(p.target, (row0 + node) * p.target_stride);
-        const Row<T> b(w.use_q ? p.draft : p.target, (row0 + node) * (w.use_q ? p.draft_stride : p.target_stride));
+        const Row<T> b(use_q ? p.draft : p.target, (row0 + node) * (use_q ? p.draft_stride : p.target_stride));
         const int each = per_cta(a.skew), s0 = rank * each, count = min(each, segments(a.skew) - s0);
-        // this lane's segments, then the one that passes `left`
+        // The segment: a lane has some, the one that passes `left` goes through its own.
         const int share = (count + 31) / 32, k0 = lane * share, k1 = min(k0 + share, count);
         u64 mine = 0;
         for (int k = k0; k < k1; ++k) mine = add_sat(mine, sm.segment[k]);
-        u64 incl = mine;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const u64 up = __shfl_up_sync(kAll, incl, d);
-            if (lane >= d) incl = add_sat(incl, up);
-        }
-        const unsigned past = __ballot_sync(kAll, incl > left);
+        u64 incl = scan(mine, lane);
+        unsigned past = __ballot_sync(kAll, incl > left);
         if (past == 0) return -1;
-        const int owner = __ffs(past) - 1;
-        int seg = 0;
-        if (lane == owner) {
-            left -= incl - mine;
-            for (seg = k0; seg < k1 - 1 && sm.segment[seg] <= left; ++seg) left -= sm.segment[seg];
-        }
+        int owner = __ffs(past) - 1, seg = k0;
+        left -= __shfl_sync(kAll, incl - mine, owner);
+        if (lane == owner)
+            for (; seg < k1 - 1 && sm.segment[seg] <= left; ++seg) left -= sm.segment[seg];
         seg = __shfl_sync(kAll, seg, owner);
         left = __shfl_sync(kAll, left, owner);
-        int token = -1;
-        for (int v = 0; v < V && token < 0; ++v) {
-            const int e = (s0 + seg) * kSegment + (v * 32 + lane) * N - a.skew;
-            float x[N], y[N];
-            unpack16(load_vector<T, N>(a, a.skew, e, p.vocab), x, T());
-            unpack16(load_vector<T, N>(b, a.skew, e, p.vocab), y, T());
-            for (int k = 0; k < sm.num_refused; ++k) {
-                const int gone = sm.refused[k] - e;
-#pragma unroll
-                for (int j = 0; j < N; ++j)
-                    if (j == gone) x[j] = 0.f;
-            }
-            u64 sum = 0;
-#pragma unroll
-            for (int k = 0; k < N; ++k) sum += w.one(x[k], y[k]);
-            u64 below = sum;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const u64 up = __shfl_up_sync(kAll, below, d);
-                if (lane >= d) below += up;
-            }
-            const unsigned over = __ballot_sync(kAll, below > left);
-            if (over) {
-                const int at = __ffs(over) - 1;
-                if (lane == at) {
-                    u64 cum = below - sum;
-#pragma unroll
-                    for (int k = 0; k < N; ++k) {
-                        cum += w.one(x[k], y[k]);
-                        if (token < 0 && cum > left) token = e + k;
-                    }
-                }
-                token = __shfl_sync(kAll, token, at);
-            } else {
-                left -= __shfl_sync(kAll, below, 31);
-            }
+        // The vector, then the entry.
+        const int e0 = (s0 + seg) * kSegment + lane * N - a.skew;
+        uint4 x[V], y[V];
+        if (inside(a, b, s0 + seg, s0 + seg + 1)) {
+            load_inside<T, N>(a, e0, x);
+            load_inside<T, N>(b, e0, y);  // not used without a q
+        } else {
+            load_edge<T, N>(a, a.skew, e0, p.vocab, x);
+            load_edge<T, N>(b, a.skew, e0, p.vocab, y);
         }
-        return token;
+        int v = 0;
+        u64 sum = 0;
+#pragma unroll 1
+        for (;; ++v) {
+            uint4 xv = x[0], yv = y[0];
+#pragma unroll
+            for (int k = 1; k < V; ++k)
+                if (k == v) xv = x[k], yv = y[k];
+            float f[N], h[N];
+            unpack16(xv, f, T());
+            unpack16(yv, h, T());
+            take_out(f, e0 + v * 32 * N, sm.num_refused);
+            Sum lane_sum;
+#pragma unroll
+            for (int k = 0; k < N; k += 2) w.template add2<kGeneral>(lane_sum, f[k], f[k + 1], h[k], h[k + 1]);
+            sum = lane_sum.value();
+            const u64 all = sum_of_lanes(sum);
+            if (v == V - 1 || all > left) break;
+            left -= all;
+        }
+        incl = scan(sum, lane);
+        past = __ballot_sync(kAll, incl > left);
+        const unsigned some = __ballot_sync(kAll, sum > 0);
+        if (some == 0) return -1;  // (a segment whose weight is a rounding)
+        owner = past ? __ffs(past) - 1 : 31 - __clz(some);
+        left -= min(left, __shfl_sync(kAll, incl - sum, owner));
+        // Its entries, a lane to each.
+        const int e = (s0 + seg) * kSegment + (v * 32 + owner) * N - a.skew + lane;
+        float f[1] = {0.f}, h = 0.f;
+        if (lane < N && e >= 0 && e < p.vocab) {
+            f[0] = as_float(a.at[e]);
+            if (use_q) h = as_float(b.at[e]);
+            take_out(f, e, sm.num_refused);
+        }
+        const u64 one = w.one(f[0], h);
+        past = __ballot_sync(kAll, scan(one, lane) > left);
+        const unsigned heavy = __ballot_sync(kAll, one > 0);
+        return __shfl_sync(kAll, e, past ? __ffs(past) - 1 : heavy ? 31 - __clz(heavy) : 0);
     }
 };
 
@@ -311,6 +418,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(const __grid_c
         }
         return;
     }
+    if (ranks > 1) cluster.barrier_arrive();  // waited for before the first sum is shared
     const bool drafted = p.draft != nullptr;
     bool bad = false;
     for (int i = tid; i < n; i += kThreads) {
@@ -322,9 +430,14 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(const __grid_c
         sm.parent[i] = tried ? up : -1;
         sm.token[i] = x;
         if (tried) {
-            sm.p[i] = clean(as_float(static_cast<const T*>(p.target)[(row0 + up) * p.target_stride + x]));
-            sm.q[i] = drafted ? clean(as_float(static_cast<const T*>(p.draft)[(row0 + up) * p.draft_stride + x])) : 1.f;
-            sm.u[i] = p.accept_uniforms[row0 + i];
+            const float a = clean(as_float(static_cast<const T*>(p.target)[(row0 + up) * p.target_stride + x]));
+            const float b = drafted ? clean(as_float(static_cast<const T*>(p.draft)[(row0 + up) * p.draft_stride + x])) : 1.f;
+            const float u = p.accept_uniforms[row0 + i];
+            sm.p[i] = a;
+            sm.q[i] = b;
+            sm.u[i] = u;
+            // Exact, and off the walk's chain of dependent steps: binary64 takes long.
+            sm.first[i] = (double)u * (double)b < (double)a;
         }
         if (rank == 0) p.path[row0 + i] = i == 0 ? 0 : -1;
     }
@@ -335,24 +448,12 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(const __grid_c
     Verify<T> v{p, sm, row0, rank, ranks};
     // Walk (warp 0): c, s of the last accepted node, the next node to look at.
     double c = 0., sum = 1.;
-    int now = 0, from = 1, count = 1;
-    bool spent = false;    // nothing is left of the target's row: the token comes from the row itself
+    int now = 0, from = 1, count = 1, number = 0;
+    bool spent = false;  // nothing is left of the target's row: the token comes from the row itself
     u64 own = 0, before = 0, total = 0;
-    auto weights = [&](bool use_q, double factor) {
-        const float hi = (float)factor;
-        return Weights{use_q, hi, (float)(factor - hi)};
-    };
-    // The sums of the whole row: this CTA's, those of the CTAs before it, of all.
-    auto share = [&] {
-        cluster.sync();
-        own = sm.total;
-        before = total = 0;
-        for (int r = 0; r < ranks; ++r) {
-            const u64 t = *cluster.map_shared_rank(&sm.total, r);
-            if (r < rank) before = add_sat(before, t);
-            total = add_sat(total, t);
-        }
-        cluster.sync();
+    auto shared_sum = [&] {
+        if (ranks > 1 && number == 0) cluster.barrier_wait();  // every CTA of the cluster has begun
+        total = v.share(cluster, number++, own, before);
     };
     while (true) {
         if (tid < 32) {
@@ -368,11 +469,20 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(const __grid_c
                 }
                 if (i >= n) break;
                 from = i + 1;
-                const double u = sm.u[i], q = sm.q[i];
-                double w = fmax(sm.p[i] - c * q, 0.);
+                const bool plain = c == 0. && sum == 1.;
                 const int x = sm.token[i];
-                if (!drafted) w = v.refused(x, lane) ? 0. : sm.p[i];
-                if (u * q * sum < w) {
+                bool accept;
+                double w = 0.;
+                if (drafted) {
+                    accept = plain ? sm.first[i] : (double)sm.u[i] * sm.q[i] * sum < fmax(sm.p[i] - c * sm.q[i], 0.);
+                } else if (plain && sm.num_refused == 0) {
+                    accept = sm.first[i];
+                    w = sm.p[i];
+                } else {
+                    w = v.refused(x, lane) ? 0. : sm.p[i];
+                    accept = (double)sm.u[i] * sum < w;
+                }
+                if (accept) {
                     if (lane == 0) {
                         if (rank == 0) p.path[row0 + count] = i;
                         sm.num_refused = 0;
@@ -401,32 +511,20 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(const __grid_c
         __syncthreads();
         const bool token = !sm.go;
         // Weights of the token: those of the last sum, or the target's row.
-        const bool use_q = sm.go || !sm.again;
         const int node = sm.now;
-        const Weights w = weights(use_q, sm.c);
+        const double factor = sm.go || !sm.again ? sm.c : 0.;
+        const float hi = (float)factor;
+        const Weights w{factor == 0. ? kRow : factor == 1. ? kDifference : kGeneral, hi, (float)(factor - hi)};
         if (sm.again) {
             v.sums(node, w);
-            if (token && sm.num_refused > 0) {
-                // Take the refused tokens out; if nothing else is left, they are not.
-                const Row<T> a(p.target, (int64_t)(row0 + node) * p.target_stride);
-                const int each = v.per_cta(a.skew), s0 = rank * each;
-                if (tid == 0)
-                    for (int k = 0; k < sm.num_refused; ++k) {
-                        const int x = sm.refused[k], seg = (x + a.skew) / kSegment - s0;
-                        if (seg < 0 || seg >= each) continue;
-                        const u64 gone = Weights{false, 0.f, 0.f}.one(as_float(a.at[x]), 0.f);
-                        sm.segment[seg] -= min(gone, sm.segment[seg]);
-                        sm.total = sm.total == ~0ull ? sm.total : sm.total - min(gone, sm.total);
-                    }
-                __syncthreads();
-            }
-            share();
-            if (token && sm.num_refused > 0 && total == 0) {
+            shared_sum();
+            if (token && total == 0 && sm.num_refused > 0) {
+                // Nothing but refused tokens: the row itself.
                 __syncthreads();
                 if (tid == 0) sm.num_refused = 0;
                 __syncthreads();
                 v.sums(node, w);
-                share();
+                shared_sum();
             }
         }
         if (token) {
