@@ -109,9 +109,10 @@ int pa_tree_attention(void* out, const void* query, int64_t query_stride, const 
     p.row_cap = pa::tree_row_cap(nodes, group);
     p.wait_limit_ns = wait_limit_ns();
     p.debug_flags = option(PA_OPT_DROP_FIRST_FILL) ? pa::kDebugDropFirstFill : 0;
-    // The longest list of K/V tiles these tables allow; its numbers stay 32-bit.
-    const double tiles = (double)num_seqs * p.max_pairs * num_kv_heads * (double)((p.ctx_cap + 127LL) / 128);
-    if (tiles > 1073741824.) return PA_ERR_UNSUPPORTED;
+    // The longest list of K/V tiles these tables allow; its half tiles stay 32-bit numbers.
+    const double items = (double)num_seqs * p.max_pairs * num_kv_heads;
+    const double tiles = items * (double)((p.ctx_cap + 127LL) / 128);
+    if (2. * tiles + 2. * items > 2147483647.) return PA_ERR_UNSUPPORTED;
     const pa::TreeWorkspaceLayout lay = pa::tree_workspace_layout(p.row_cap, shape.head_dim);
     if (!aligned(workspace, 256) || workspace_bytes < lay.total) return PA_ERR_WORKSPACE;
     char* ws = static_cast<char*>(workspace);

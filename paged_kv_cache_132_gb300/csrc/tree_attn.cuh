@@ -13,10 +13,13 @@
 // of 128 positions.  The K/V tiles of all items stand in one list (pairs of query
 // tiles outermost, so that what reads the same keys runs at the same time; then
 // sequences, KV heads, tiles), and each CTA -- one per SM -- takes an equal,
-// contiguous piece of it.  So every SM reads the same number of bytes whatever
-// the lengths, and only an item that lies across a border between CTAs is computed
-// in parts: at most two per CTA, which the reduce kernel joins.  The list is
-// never written: each CTA finds its piece by a prefix sum over the lengths.
+// contiguous piece of it.  So every SM has the same work whatever the lengths, and
+// only an item that lies across a border between CTAs is computed in parts: at most
+// two per CTA, which the reduce kernel joins.  The list is never written: each CTA
+// finds its piece by a prefix sum over the lengths.  Pieces are counted in half tiles,
+// and an item begins with LEAD of them for what it costs beside its tiles (0.75 us,
+// against 1.45 us for a tile of 64 KiB: 64 sequences of 16 to 8192 tokens, 8 KV heads,
+// ended between 76 and 90 us by the CTA without it).
 //
 // Per K/V tile j and query tile:
 //   S  = Q K_j^T      tcgen05.mma M=128 N=128 K=d, into TMEM
@@ -74,6 +77,7 @@ struct TreeShape {
     static constexpr int TILE = 16 * GROUP;      // bytes of a K or V tile
     static constexpr int NSLOT = D == 128 ? 5 : 8;  // K/V ring: K_0, V_0, K_1, V_1, ... one tile per slot
     static constexpr int NITEM = 4;              // items announced ahead of their last reader
+    static constexpr int LEAD = D == 128 ? 1 : 2;  // an item's cost beside its tiles, in half tiles
     static constexpr int SOFTMAX_WARPS = 4;      // per chain
     static constexpr int LOAD_WARP = 2;
     static constexpr int CHECK_WARP = 3;
@@ -96,7 +100,8 @@ struct TreeShape {
         int4 item[NITEM][2];        // {first row, nodes (0: no more work), ctx, KV head}, {pair, tiles from, to, sequence}
         int last_dirty;             // latest item with non-finite values among its nodes
         int scratch[16];            // sums over the warps
-        int start[3];               // where this CTA's piece begins: pair, sequence, tile of the sequence
+        int start[3];               // where this CTA's piece begins: pair, sequence, half tile of the sequence
+        int start_seq[3];           // that sequence's first row, nodes, ctx
         uint64_t item_full[NITEM];  // announced (load warp)
         uint64_t item_empty[NITEM]; // read by every role
         // Who waits for a barrier waits for each of its phases in turn: a parity does not
@@ -223,44 +228,68 @@ __device__ inline int tree_block_scan(int x, int* scratch, int& total) {
     return incl - x + tree_warp_sum(lane < warp ? w : 0);
 }
 
-// The piece [lo, hi) of the list; sm.start is where it begins.  Counts stay below
-// 2^31 (the host checks the largest list).
+// Half tiles of an item, and the tiles that begin before half tile `at` of it.
 template <class Shape>
-__device__ __forceinline__ int2 tree_piece(const TreeAttnParams& p, typename Shape::Smem& sm) {
+__device__ __forceinline__ int tree_item_length(int tiles) { return 2 * tiles + Shape::LEAD; }
+template <class Shape>
+__device__ __forceinline__ int tree_tiles_before(int at) {
+    return at <= Shape::LEAD ? 0 : (at - Shape::LEAD + 1) >> 1;
+}
+
+// The list's length, the CTAs that share it (two half tiles each at least, so that a
+// piece within an item has a tile), and this CTA's piece [lo, hi); sm.start is where
+// it begins.  Counts stay below 2^31 (the host checks the longest list).
+struct TreePiece {
+    int lo, hi, total, ctas;
+    // The CTA that has half tile `at` of the list.
+    __device__ __forceinline__ int cta_of(int at) const { return (int)((((long long)at + 1) * ctas - 1) / total); }
+};
+template <class Shape>
+__device__ __forceinline__ TreePiece tree_piece(const TreeAttnParams& p, typename Shape::Smem& sm) {
     int mine = 0;
     TreeSeq q = tree_seq(p, threadIdx.x, blockIdx.x == 0);
     for (int s = threadIdx.x;; q = tree_seq(p, s, blockIdx.x == 0)) {
-        mine += q.tiles * q.pairs;
+        if (q.tiles) mine += tree_item_length<Shape>(q.tiles) * q.pairs;
         s += Shape::THREADS;
         if (s - (int)threadIdx.x >= p.num_seqs) break;
     }
     // one loop turn: q is still this thread's only sequence
     const bool single = p.num_seqs <= Shape::THREADS;
-    int total;
-    tree_block_scan(mine, sm.scratch, total);
-    total *= p.num_kv_heads;
-    const int chunk = (total + p.ctas - 1) / p.ctas;
-    const int lo = min((int)min((long long)blockIdx.x * chunk, (long long)total), total), hi = min(lo + chunk, total);
-    if (lo < hi) {
+    TreePiece w;
+    const int rank = tree_block_scan(mine, sm.scratch, w.total);
+    const bool one_pass = single && p.max_pairs == 1;  // the sums so far are the list's
+    const int total_heads = w.total;
+    w.total *= p.num_kv_heads;
+    w.ctas = max(1, min(p.ctas, w.total / 2));
+    w.lo = w.hi = 0;
+    if ((int)blockIdx.x < w.ctas) {
+        w.lo = (int)((long long)blockIdx.x * w.total / w.ctas);
+        w.hi = (int)(((long long)blockIdx.x + 1) * w.total / w.ctas);
+    }
+    if (w.lo < w.hi) {
         int before = 0;  // of the list
         bool found = false;
         for (int pair = 0; pair < p.max_pairs && !found; ++pair)
             for (int s0 = 0; s0 < p.num_seqs && !found; s0 += Shape::THREADS) {
                 if (!single) q = tree_seq(p, s0 + threadIdx.x, false);
-                const int x = q.pairs > pair ? q.tiles * p.num_kv_heads : 0;
-                int sum;
-                const int first = before + tree_block_scan(x, sm.scratch, sum);
-                if (lo >= first && lo < first + x) {
+                const int x = q.pairs > pair ? tree_item_length<Shape>(q.tiles) : 0;
+                int sum = total_heads, rank_here = rank;
+                if (!one_pass) rank_here = tree_block_scan(x, sm.scratch, sum);
+                const int first = (before + rank_here) * p.num_kv_heads;
+                if (w.lo >= first && w.lo < first + x * p.num_kv_heads) {
                     sm.start[0] = pair;
                     sm.start[1] = s0 + threadIdx.x;
-                    sm.start[2] = lo - first;
+                    sm.start[2] = w.lo - first;
+                    sm.start_seq[0] = q.row0;
+                    sm.start_seq[1] = q.n;
+                    sm.start_seq[2] = q.ctx;
                 }
                 before += sum;
-                found = lo < before;
+                found = w.lo < before * p.num_kv_heads;
             }
     }
     __syncthreads();
-    return make_int2(lo, hi);
+    return w;
 }
 
 // ---------------------------------------------------------------------------
@@ -275,7 +304,7 @@ __device__ inline void tma_load_4d(void* dst, const CUtensorMap* map, int group,
 }
 
 template <class Shape>
-__device__ void tree_load(const TreeAttnParams& p, typename Shape::Smem& sm, int lane, int2 piece,
+__device__ void tree_load(const TreeAttnParams& p, typename Shape::Smem& sm, int lane, const TreePiece& piece,
                           const CUtensorMap* tq, const CUtensorMap* tk, const CUtensorMap* tv) {
     const uint32_t q_bytes = (uint32_t)(Shape::SLABS * p.tile_tokens * p.group * 128);
     const int block_size = 1 << p.block_shift;
@@ -288,33 +317,71 @@ __device__ void tree_load(const TreeAttnParams& p, typename Shape::Smem& sm, int
     bool ok = true, wrong = false;
     if (lane == 0) p.splits[blockIdx.x] = make_int4(0, 0, 0, 0);
 
-    // Sequences [window, window + 32) are in the lanes.
-    int left = piece.y - piece.x, pair = 0, window = 0, cur = 0, off = 0;
+    // Half tiles left of the piece, and of the sequence (in this pair of query tiles) before
+    // what is left; sequences [window, window + 32) are in the lanes once one is done.
+    int left = piece.hi - piece.lo, off = 0, pair = 0, window = 0, cur = 0;
     TreeSeq mine{0, 0, 0, 0, 0};
+    int row0 = 0, nodes = 0, ctx = 0;
     if (left > 0) {
         pair = sm.start[0];
         window = sm.start[1] & ~31;
         cur = sm.start[1] & 31;
         off = sm.start[2];
-        mine = tree_seq(p, window + lane, false);
+        row0 = sm.start_seq[0], nodes = sm.start_seq[1], ctx = sm.start_seq[2];
     }
+    bool loaded = false;
+    // The next item of the piece with a tile in it; false at the end.
+    auto take = [&](TreeItem& w, int& nt) {
+        while (left > 0) {
+            nt = (ctx + 127) >> 7;
+            const int length = tree_item_length<Shape>(nt);
+            if (off == length * p.num_kv_heads) {
+                // the next sequence with nodes in this pair of query tiles, or in the next one
+                off = 0;
+                if (!loaded) mine = tree_seq(p, window + lane, false);
+                loaded = true;
+                unsigned later = __ballot_sync(kFullMask, mine.pairs > pair) & ~((2u << cur) - 1u);
+                while (later == 0) {
+                    window += 32;
+                    if (window >= p.num_seqs) {
+                        window = 0;
+                        if (++pair >= p.max_pairs) return false;  // lengths that changed under the call
+                    }
+                    mine = tree_seq(p, window + lane, false);
+                    later = __ballot_sync(kFullMask, mine.pairs > pair);
+                }
+                cur = __ffs(later) - 1;
+                row0 = __shfl_sync(kFullMask, mine.row0, cur);
+                nodes = __shfl_sync(kFullMask, mine.n, cur);
+                ctx = __shfl_sync(kFullMask, mine.ctx, cur);
+                continue;
+            }
+            const int head = off / length, from = off - head * length, to = min(length, from + left);
+            const int start = piece.hi - left - from;  // of the item in the list
+            left -= to - from;
+            off += to - from;
+            w.from = tree_tiles_before<Shape>(from);
+            w.to = tree_tiles_before<Shape>(to);
+            if (w.from == w.to) continue;
+            w.row0 = row0, w.n = nodes, w.ctx = ctx;
+            w.kv_head = head;
+            w.pair = pair;
+            w.seq = window + cur;
+            w.t0 = pair * 2 * p.tile_tokens;
+            w.one = nodes - w.t0 <= p.tile_tokens;
+            w.first_masked = (ctx - nodes) >> 7;
+            if (w.from == 0 && w.to < nt && lane == 0)  // goes on in the next CTAs
+                p.splits[blockIdx.x] =
+                    make_int4(row0 + w.t0, min(2 * p.tile_tokens, nodes - w.t0), head,
+                              piece.cta_of(start + Shape::LEAD + 2 * (nt - 1)) - (int)blockIdx.x + 1);
+            return true;
+        }
+        return false;
+    };
     for (int n = 0;; ++n) {
         TreeItem w{};
         int nt = 0;
-        if (left > 0) {
-            nt = __shfl_sync(kFullMask, mine.tiles, cur);
-            w.row0 = __shfl_sync(kFullMask, mine.row0, cur);
-            w.n = __shfl_sync(kFullMask, mine.n, cur);
-            w.ctx = __shfl_sync(kFullMask, mine.ctx, cur);
-            w.kv_head = off / nt;
-            w.pair = pair;
-            w.from = off - w.kv_head * nt;
-            w.to = min(nt, w.from + left);
-            w.seq = window + cur;
-            w.t0 = pair * 2 * p.tile_tokens;
-            w.one = w.n - w.t0 <= p.tile_tokens;
-            w.first_masked = (w.ctx - w.n) >> 7;
-        }
+        const bool more = take(w, nt);
         const int st = n % Shape::NITEM;
         tree_wait(p, sm, &sm.item_empty[st], ((uint32_t)(n / Shape::NITEM) & 1u) ^ 1u);
         if (__any_sync(kFullMask, prompt_aborted(&sm.abort_flag))) break;
@@ -324,13 +391,7 @@ __device__ void tree_load(const TreeAttnParams& p, typename Shape::Smem& sm, int
             mbar_arrive(&sm.item_full[st]);
         }
         __syncwarp();
-        if (left <= 0) break;
-        if (w.from == 0 && w.to < nt && lane == 0) {
-            // the item goes on in the next CTAs, each of which has as many tiles
-            const int chunk = piece.y - piece.x;
-            p.splits[blockIdx.x] = make_int4(w.row0 + w.t0, min(2 * p.tile_tokens, w.n - w.t0), w.kv_head,
-                                             1 + (nt - w.to + chunk - 1) / chunk);
-        }
+        if (!more) break;
         const int32_t* const table = p.block_tables + (int64_t)w.seq * p.max_blocks;
         const int blocks = (w.ctx + block_size - 1) >> p.block_shift;
         // Lane l: the l-th block of a tile, or -2.
@@ -398,24 +459,6 @@ __device__ void tree_load(const TreeAttnParams& p, typename Shape::Smem& sm, int
             id = next_id;
         }
         if (!ok) break;
-        left -= w.to - w.from;
-        off += w.to - w.from;
-        if (left > 0 && off == nt * p.num_kv_heads) {
-            // the next sequence with nodes in this pair of query tiles, or in the next one
-            off = 0;
-            unsigned later = __ballot_sync(kFullMask, mine.pairs > pair) & ~((2u << cur) - 1u);
-            while (later == 0) {
-                window += 32;
-                if (window >= p.num_seqs) {
-                    window = 0;
-                    if (++pair >= p.max_pairs) break;
-                }
-                mine = tree_seq(p, window + lane, false);
-                later = __ballot_sync(kFullMask, mine.pairs > pair);
-            }
-            if (later == 0) left = 0;  // lengths that changed under the call
-            cur = later ? __ffs(later) - 1 : 0;
-        }
     }
     if (wrong) set_error(p.err, PA_DEVERR_BLOCK_ID);
     pdl_launch_dependents();
@@ -970,9 +1013,11 @@ __global__ void __launch_bounds__(TreeShape<D>::THREADS, 1)
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = sm.tmem_base;
-    // The kernel that wrote the lengths, the queries and the pools may still be finishing.
+    // The lengths are read before the wait: no kernel that writes them lets its dependents
+    // start before they are written (common.cuh).  What wrote the queries, the masks and the
+    // pools may still be finishing.
+    const TreePiece piece = tree_piece<Shape>(p, sm);
     pdl_wait_prerequisites();
-    const int2 piece = tree_piece<Shape>(p, sm);
 
     if (warp < Shape::SOFTMAX_WARP) {
         regs_dec<Shape::REGS_OTHER>();
@@ -1007,23 +1052,27 @@ __global__ void __launch_bounds__(TreeShape<D>::THREADS, 1)
 // A warp per row; a lane holds D / 32 consecutive columns.  Part 0 is the one of the
 // CTA in which the item begins, part k the first piece of the k-th CTA after it.
 constexpr int kTreeReduceThreads = 256;
-constexpr int kTreeReduceRows = 16;  // rows of a CTA, two of a warp
+constexpr int kTreeReduceCtas = 8;  // of an item at most: 64 rows at a time
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kTreeReduceThreads) tree_reduce_kernel(const __grid_constant__ TreeAttnParams p) {
     constexpr int VPL = D / 32;
+    constexpr int PRE = 32 / VPL;  // parts whose values are loaded beside the maxima and sums
     const float NEG_INF = __int_as_float(0xff800000);
     const int lane = threadIdx.x & 31;
     pdl_wait_prerequisites();
+    pdl_launch_dependents();
     const int4 item = __ldcg(p.splits + blockIdx.x);
     const int parts = item.w;
     if (parts == 0) return;
     auto slot = [&](int k) { return ((int64_t)(blockIdx.x + k) * 2 + (k == 0 ? 1 : 0)) * p.row_cap; };
-    for (int row = blockIdx.y * kTreeReduceRows + (threadIdx.x >> 5); row < (int)(blockIdx.y + 1) * kTreeReduceRows;
-         row += kTreeReduceThreads / 32) {
+    // Rows of the second query tile stand 128 behind the first one's.
+    const int rows = item.y <= p.tile_tokens ? item.y * p.group : 128 + (item.y - p.tile_tokens) * p.group;
+    for (int row = blockIdx.y * (kTreeReduceThreads / 32) + (threadIdx.x >> 5); row < rows;
+         row += gridDim.y * (kTreeReduceThreads / 32)) {
         const int i = row >> 7, r = row & 127, t = r / p.group, g = r - t * p.group;
         const int node = i * p.tile_tokens + t;
-        if (row >= p.row_cap || t >= p.tile_tokens || node >= item.y) continue;
+        if (t >= p.tile_tokens) continue;
         float M = NEG_INF, L = 0.f, acc[VPL];
 #pragma unroll
         for (int v = 0; v < VPL; ++v) acc[v] = 0.f;
@@ -1031,6 +1080,23 @@ __global__ void __launch_bounds__(kTreeReduceThreads) tree_reduce_kernel(const _
             const int count = min(32, parts - k0);
             float2 ml = make_float2(NEG_INF, 0.f);
             if (lane < count) ml = __ldcg(p.part_ml + slot(k0 + lane) + row);
+            auto values = [&](int k, float (&o)[VPL]) {
+                const float* src = p.part_o + (slot(k0 + k) + row) * D + lane * VPL;
+                if constexpr (VPL == 4) {
+                    const float4 x = __ldcg(reinterpret_cast<const float4*>(src));
+                    o[0] = x.x, o[1] = x.y, o[2] = x.z, o[3] = x.w;
+                } else {
+                    const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
+                    o[0] = x.x, o[1] = x.y;
+                }
+            };
+            float pre[PRE][VPL];
+#pragma unroll
+            for (int k = 0; k < PRE; ++k) {
+#pragma unroll
+                for (int v = 0; v < VPL; ++v) pre[k][v] = 0.f;
+                if (k < count) values(k, pre[k]);
+            }
             float cm = ml.x;
 #pragma unroll
             for (int d = 16; d >= 1; d >>= 1) cm = fmaxf(cm, __shfl_xor_sync(kFullMask, cm, d));
@@ -1045,21 +1111,20 @@ __global__ void __launch_bounds__(kTreeReduceThreads) tree_reduce_kernel(const _
             M = m_new;
 #pragma unroll
             for (int v = 0; v < VPL; ++v) acc[v] *= old;
-#pragma unroll 4
-            for (int k = 0; k < count; ++k) {
+#pragma unroll
+            for (int k = 0; k < PRE; ++k) {
+                if (k >= count) break;
                 const float wk = __shfl_sync(kFullMask, weight, k);
-                const float* src = p.part_o + (slot(k0 + k) + row) * D + lane * VPL;
-                if constexpr (VPL == 4) {
-                    const float4 o = __ldcg(reinterpret_cast<const float4*>(src));
-                    acc[0] = fmaf(wk, o.x, acc[0]);
-                    acc[1] = fmaf(wk, o.y, acc[1]);
-                    acc[2] = fmaf(wk, o.z, acc[2]);
-                    acc[3] = fmaf(wk, o.w, acc[3]);
-                } else {
-                    const float2 o = __ldcg(reinterpret_cast<const float2*>(src));
-                    acc[0] = fmaf(wk, o.x, acc[0]);
-                    acc[1] = fmaf(wk, o.y, acc[1]);
-                }
+#pragma unroll
+                for (int v = 0; v < VPL; ++v) acc[v] = fmaf(wk, pre[k][v], acc[v]);
+            }
+#pragma unroll 4
+            for (int k = PRE; k < count; ++k) {
+                const float wk = __shfl_sync(kFullMask, weight, k);
+                float o[VPL];
+                values(k, o);
+#pragma unroll
+                for (int v = 0; v < VPL; ++v) acc[v] = fmaf(wk, o[v], acc[v]);
             }
         }
         const float inv = L == 0.f ? 0.f : 1.f / L;
@@ -1102,7 +1167,8 @@ cudaError_t launch_tree_attention_t(const TreeAttnParams& p, const CUtensorMap* 
     cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, tree_attn_kernel<T, D>, p, *tq, *tk, *tv);
     if (e != cudaSuccess || p.ctas == 1) return e;  // one CTA shares nothing
-    cfg.gridDim = dim3((unsigned)p.ctas, (unsigned)((p.row_cap + kTreeReduceRows - 1) / kTreeReduceRows));
+    const int slices = (p.row_cap + kTreeReduceThreads / 32 - 1) / (kTreeReduceThreads / 32);
+    cfg.gridDim = dim3((unsigned)p.ctas, (unsigned)(slices < kTreeReduceCtas ? slices : kTreeReduceCtas));
     cfg.blockDim = dim3(kTreeReduceThreads);
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, tree_reduce_kernel<T, D>, p);
