@@ -331,10 +331,9 @@ __device__ void tree_load(const TreeAttnParams& p, typename Shape::Smem& sm, int
     }
     bool loaded = false;
     // The next item of the piece with a tile in it; false at the end.
-    auto take = [&](TreeItem& w, int& nt) {
+    auto take = [&](TreeItem& w) {
         while (left > 0) {
-            nt = (ctx + 127) >> 7;
-            const int length = tree_item_length<Shape>(nt);
+            const int nt = (ctx + 127) >> 7, length = tree_item_length<Shape>(nt);
             if (off == length * p.num_kv_heads) {
                 // the next sequence with nodes in this pair of query tiles, or in the next one
                 off = 0;
@@ -378,31 +377,33 @@ __device__ void tree_load(const TreeAttnParams& p, typename Shape::Smem& sm, int
         }
         return false;
     };
+    // Lane l: the l-th block of tile j, or -2.
+    auto block_at = [&](const TreeItem& w, int j) {
+        const int at = j * blocks_per_tile + lane, blocks = (w.ctx + block_size - 1) >> p.block_shift;
+        return j < w.to && lane < blocks_per_tile && at < blocks
+                   ? __ldg(p.block_tables + (int64_t)w.seq * p.max_blocks + at)
+                   : -2;
+    };
+    // The next item is known, and its first blocks are loading, before one's last copies: a
+    // round trip to the table for every item otherwise (4096 items of 2 tiles: 144 us).
+    TreeItem w{}, next{};
+    bool more = take(w);
+    int id = more ? block_at(w, w.from) : -2, first_id = -2;
     for (int n = 0;; ++n) {
-        TreeItem w{};
-        int nt = 0;
-        const bool more = take(w, nt);
+        bool next_more = false;
         const int st = n % Shape::NITEM;
         tree_wait(p, sm, &sm.item_empty[st], ((uint32_t)(n / Shape::NITEM) & 1u) ^ 1u);
         if (__any_sync(kFullMask, prompt_aborted(&sm.abort_flag))) break;
         if (elect_one()) {
-            sm.item[st][0] = make_int4(w.row0, w.n, w.ctx, w.kv_head);
+            sm.item[st][0] = make_int4(w.row0, more ? w.n : 0, w.ctx, w.kv_head);
             sm.item[st][1] = make_int4(w.pair, w.from, w.to, w.seq);
             mbar_arrive(&sm.item_full[st]);
         }
         __syncwarp();
         if (!more) break;
-        const int32_t* const table = p.block_tables + (int64_t)w.seq * p.max_blocks;
-        const int blocks = (w.ctx + block_size - 1) >> p.block_shift;
-        // Lane l: the l-th block of a tile, or -2.
-        auto block_at = [&](int j) {
-            const int at = j * blocks_per_tile + lane;
-            return j < w.to && lane < blocks_per_tile && at < blocks ? __ldg(table + at) : -2;
-        };
-        int id = block_at(w.from);
 #pragma unroll 1
         for (int j = w.from; j < w.to; ++j) {
-            const int next_id = block_at(j + 1);
+            const int next_id = block_at(w, j + 1);
             const bool good = id >= 0 && (int64_t)id < p.num_blocks;
             wrong |= id != -2 && !good;
             const uint32_t bytes = (uint32_t)__popc(__ballot_sync(kFullMask, good)) * box_bytes;
@@ -457,8 +458,15 @@ __device__ void tree_load(const TreeAttnParams& p, typename Shape::Smem& sm, int
             }
             if (!ok) break;
             id = next_id;
+            if (j == w.from) {
+                next_more = take(next);
+                first_id = next_more ? block_at(next, next.from) : -2;
+            }
         }
         if (!ok) break;
+        w = next;
+        more = next_more;
+        id = first_id;
     }
     if (wrong) set_error(p.err, PA_DEVERR_BLOCK_ID);
     pdl_launch_dependents();
@@ -623,12 +631,21 @@ __device__ void tree_mma(const TreeAttnParams& p, typename Shape::Smem& sm, uint
 // ---------------------------------------------------------------------------
 // softmax warps of chain i (thread r = row r = TMEM lane r)
 // ---------------------------------------------------------------------------
-// Bit k: the row attends to position first + k of its sequence's tree (negative:
-// before the tree), k < 32.  `row` is its mask row.
-__device__ __forceinline__ uint32_t tree_mask_bits(const TreeAttnParams& p, const uint32_t* row, int first) {
+// Bit k: the row attends to node first + k of its sequence (negative: a position before
+// the tree), k < 32.  `row` is its mask row, `near` the first words of it, which were
+// loaded when the item began: a masked tile otherwise waits for up to three round trips.
+constexpr int kTreeNear = 4;
+__device__ __forceinline__ uint32_t tree_mask_bits(const TreeAttnParams& p, const uint32_t* row,
+                                                   const uint32_t (&near)[kTreeNear], int first) {
     if (first <= -32) return ~0u;
-    auto word = [&](int at) { return at < p.mask_words ? __ldg(row + at) : 0u; };
-    if (first < 0) return (word(0) << -first) | ((1u << -first) - 1u);
+    auto word = [&](int at) {
+        if (at >= kTreeNear) return at < p.mask_words ? __ldg(row + at) : 0u;
+        uint32_t w = 0u;
+#pragma unroll
+        for (int k = 0; k < kTreeNear; ++k) w = at == k ? near[k] : w;
+        return w;
+    };
+    if (first < 0) return (near[0] << -first) | ((1u << -first) - 1u);
     const int at = first >> 5;
     return __funnelshift_r(word(at), word(at + 1), first & 31);
 }
@@ -661,6 +678,9 @@ __device__ void tree_softmax(const TreeAttnParams& p, typename Shape::Smem& sm, 
         const bool any = __any_sync(kFullMask, valid);
         // Rows without a node compute something and are not stored.
         const uint32_t* const mask = p.tree_mask + (int64_t)(w.row0 + (valid ? node : w.t0)) * p.mask_words;
+        uint32_t near[kTreeNear];
+#pragma unroll
+        for (int k = 0; k < kTreeNear; ++k) near[k] = k < p.mask_words ? __ldg(mask + k) : 0u;
         float m = NEG_INF, l = 0.f;
         bool begun = false;
 #pragma unroll 1
@@ -672,7 +692,7 @@ __device__ void tree_softmax(const TreeAttnParams& p, typename Shape::Smem& sm, 
             if (masked && any) {
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    bits[q] = tree_mask_bits(p, mask, j * Shape::BN + 32 * q - w.base);
+                    bits[q] = tree_mask_bits(p, mask, near, j * Shape::BN + 32 * q - w.base);
                     const int here = cols - 32 * q;  // positions before the context's end
                     if (here < 32) bits[q] &= here <= 0 ? 0u : (1u << here) - 1u;
                 }
