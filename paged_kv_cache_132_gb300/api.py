@@ -7,8 +7,11 @@ PyTorch or the CPU.  PyTorch provides device memory and streams.
 """
 from __future__ import annotations
 
+import array
 import contextlib
 import ctypes
+import itertools
+import operator
 from typing import Iterator, NamedTuple, Optional, Sequence, Tuple
 
 import torch
@@ -396,6 +399,24 @@ def prompt_attention(query: torch.Tensor, key: torch.Tensor, value: torch.Tensor
     return out
 
 
+# The calls of drafted trees come once per layer or step, next to kernels of a few
+# microseconds: their checks are single expressions, and the device is asked for once.
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _stream_here(stream: Optional[torch.cuda.Stream], device: int) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_current_stream is not None:
+        return _raw_current_stream(device)
+    return torch.cuda.current_stream().cuda_stream
+
+
+def _refuse_elsewhere(cond: bool) -> None:
+    if not cond:
+        raise ValueError("tensors must be on the current CUDA device")
+
+
 class TreePlan(NamedTuple):
     """What plan_tree makes (device tensors)."""
     positions: torch.Tensor  # int32 [T], -1 for rows of no sequence
@@ -412,25 +433,31 @@ def plan_tree(parents: torch.Tensor, query_start_loc: torch.Tensor, context_lens
     less than its own (-1: none).  ``max_nodes`` is a host-side upper bound of the
     nodes of a sequence.  Positions are the depths behind the cached tokens; they
     and the slots of plan_step go to rotary_and_cache, the masks to tree_attention."""
-    lib = native.load()
-    t, i32 = parents.numel(), torch.int32
+    i32 = torch.int32
     _require(max_nodes >= 1, "max_nodes must be positive")
     words = (max_nodes + 63) // 64
-    _require(parents.dtype is i32 and parents.shape == (t,) and parents.is_contiguous(), "parents is int32 [T]")
+    _require(parents.dtype is i32 and parents.dim() == 1 and parents.is_contiguous(), "parents is int32 [T]")
     _require(context_lens.dtype is i32 and context_lens.dim() == 1 and context_lens.is_contiguous(),
              "context_lens is int32 [num_seqs]")
-    s = context_lens.numel()
-    _require(query_start_loc.dtype is i32 and query_start_loc.shape == (s + 1,) and query_start_loc.is_contiguous(),
-             "query_start_loc is int32 [num_seqs + 1]")
+    t, s = parents.numel(), context_lens.numel()
+    _require(query_start_loc.dtype is i32 and query_start_loc.dim() == 1 and query_start_loc.numel() == s + 1
+             and query_start_loc.is_contiguous(), "query_start_loc is int32 [num_seqs + 1]")
     if out is None:
-        out = TreePlan(_empty((t,), i32, parents.device, stream),
-                       _empty((t, words), torch.int64, parents.device, stream))
-    _require(out[0].dtype is i32 and out[0].shape == (t,) and out[0].is_contiguous()
-             and out[1].dtype is torch.int64 and out[1].shape == (t, words) and out[1].is_contiguous(),
-             "out is (positions int32 [T], tree_mask int64 [T][words])")
-    _require_here(parents, query_start_loc, context_lens, *out)
-    _raise(lib.pa_plan_tree(parents.data_ptr(), query_start_loc.data_ptr(), context_lens.data_ptr(), s, t,
-                            out[0].data_ptr(), out[1].data_ptr(), words, _stream_ptr(stream)), "pa_plan_tree")
+        positions = _empty((t,), i32, parents.device, stream)
+        mask = _empty((t, words), torch.int64, parents.device, stream)
+        out = TreePlan(positions, mask)
+    else:
+        positions, mask = out
+        _require(positions.dtype is i32 and positions.shape == (t,) and positions.is_contiguous()
+                 and mask.dtype is torch.int64 and mask.shape == (t, words) and mask.is_contiguous(),
+                 "out is (positions int32 [T], tree_mask int64 [T][words])")
+    dev = _current_device()
+    _refuse_elsewhere(parents.get_device() == query_start_loc.get_device() == context_lens.get_device()
+                      == positions.get_device() == mask.get_device() == dev)
+    status = native.load().pa_plan_tree(parents.data_ptr(), query_start_loc.data_ptr(), context_lens.data_ptr(), s, t,
+                                        positions.data_ptr(), mask.data_ptr(), words, _stream_here(stream, dev))
+    if status:
+        raise PaError(status, "pa_plan_tree")
     return out
 
 
@@ -454,40 +481,46 @@ def tree_attention(query: torch.Tensor, query_start_loc: torch.Tensor, tree_mask
     bit of its row of ``tree_mask`` (plan_tree's, or any other mask; int64
     [T][words]) is set; to nothing: 0.  The query may be a slice of a fused
     projection's rows.  Rows outside every sequence are not written."""
-    lib = native.load()
     _require(query.dim() == 3, "query is [num_tokens][num_heads][head_dim]")
     t, h, d = query.shape
+    dtype, i32 = k_cache.dtype, torch.int32
     desc = cache_desc(k_cache)
-    dtype = k_cache.dtype
-    _require(k_cache.shape == v_cache.shape and v_cache.dtype is dtype and k_cache.is_contiguous()
+    _require(v_cache.shape == k_cache.shape and v_cache.dtype is dtype and k_cache.is_contiguous()
              and v_cache.is_contiguous(), "K and V pools must match and be contiguous")
     _require(query.dtype is dtype and d == desc.head_dim, "query dtype/head_dim must match the pools")
-    i32 = torch.int32
     _require(block_tables.dtype is i32 and block_tables.dim() == 2 and block_tables.is_contiguous(),
              "block_tables is int32 [num_seqs][max_blocks]")
-    s = block_tables.shape[0]
-    _require(context_lens.dtype is i32 and context_lens.shape == (s,) and context_lens.is_contiguous(),
-             "context_lens is int32 [num_seqs]")
-    _require(query_start_loc.dtype is i32 and query_start_loc.shape == (s + 1,) and query_start_loc.is_contiguous(),
-             "query_start_loc is int32 [num_seqs + 1]")
-    _require(tree_mask.dtype is torch.int64 and tree_mask.dim() == 2 and tree_mask.shape[0] == t
-             and tree_mask.is_contiguous(), "tree_mask is int64 [num_tokens][words]")
+    s, max_blocks = block_tables.shape
+    _require(context_lens.dtype is i32 and context_lens.dim() == 1 and context_lens.numel() == s
+             and context_lens.is_contiguous(), "context_lens is int32 [num_seqs]")
+    _require(query_start_loc.dtype is i32 and query_start_loc.dim() == 1 and query_start_loc.numel() == s + 1
+             and query_start_loc.is_contiguous(), "query_start_loc is int32 [num_seqs + 1]")
+    _require(tree_mask.dtype is torch.int64 and tree_mask.dim() == 2 and tree_mask.is_contiguous()
+             and tree_mask.shape[0] == t, "tree_mask is int64 [num_tokens][words]")
+    words, hkv = tree_mask.shape[1], desc.num_kv_heads
     if out is None:
         out = _empty((t, h, d), dtype, query.device, stream)
-    _require(out.shape == query.shape and out.dtype is dtype and out.is_contiguous(),
-             "out is contiguous [num_tokens][num_heads][head_dim] of the pools' dtype")
-    words, hkv = tree_mask.shape[1], desc.num_kv_heads
+    else:
+        _require(out.shape == query.shape and out.dtype is dtype and out.is_contiguous(),
+                 "out is contiguous [num_tokens][num_heads][head_dim] of the pools' dtype")
+    lib = native.load()
     if workspace is None:
-        need = lib.pa_tree_attention_workspace_size(t, words, h, hkv, d)
-        workspace = _empty((max(need, 256),), torch.uint8, query.device, stream)
-    _require(workspace.dtype is torch.uint8 and workspace.is_contiguous(), "workspace is bytes")
-    _require_here(query, query_start_loc, tree_mask, k_cache, v_cache, block_tables, context_lens, out, workspace)
-    _raise(lib.pa_tree_attention(out.data_ptr(), query.data_ptr(), _token_stride(query, "query"),
-                                 query_start_loc.data_ptr(), t, tree_mask.data_ptr(), words, k_cache.data_ptr(),
-                                 v_cache.data_ptr(), ctypes.byref(desc), block_tables.data_ptr(),
-                                 block_tables.shape[1], context_lens.data_ptr(), s, h, hkv, float(scale),
-                                 workspace.data_ptr(), workspace.numel(), _stream_ptr(stream)),
-           "pa_tree_attention")
+        size = max(lib.pa_tree_attention_workspace_size(t, words, h, hkv, d), 256)
+        workspace = _empty((size,), torch.uint8, query.device, stream)
+    else:
+        size = workspace.numel()
+        _require(workspace.dtype is torch.uint8 and workspace.is_contiguous(), "workspace is bytes")
+    dev = _current_device()
+    _refuse_elsewhere(query.get_device() == query_start_loc.get_device() == tree_mask.get_device()
+                      == k_cache.get_device() == v_cache.get_device() == block_tables.get_device()
+                      == context_lens.get_device() == out.get_device() == workspace.get_device() == dev)
+    status = lib.pa_tree_attention(out.data_ptr(), query.data_ptr(), _token_stride(query, "query"),
+                                   query_start_loc.data_ptr(), t, tree_mask.data_ptr(), words, k_cache.data_ptr(),
+                                   v_cache.data_ptr(), desc, block_tables.data_ptr(), max_blocks,
+                                   context_lens.data_ptr(), s, h, hkv, float(scale), workspace.data_ptr(), size,
+                                   _stream_here(stream, dev))
+    if status:
+        raise PaError(status, "pa_tree_attention")
     return out
 
 
@@ -520,39 +553,52 @@ def verify_tree(tokens: torch.Tensor, parents: torch.Tensor, query_start_loc: to
     float32 in [0, 1).  Children are tried in order, a refused one leaves the
     residual distribution to the next, and the last token is drawn from what is
     left: the accepted tokens are distributed as the target's own."""
-    lib = native.load()
-    t, i32, f32 = tokens.numel(), torch.int32, torch.float32
-    _require(tokens.dtype is i32 and tokens.shape == (t,) and tokens.is_contiguous() and parents.dtype is i32
-             and parents.shape == (t,) and parents.is_contiguous(), "tokens and parents are int32 [T]")
-    _require(query_start_loc.dtype is i32 and query_start_loc.dim() == 1 and query_start_loc.numel() > 0
-             and query_start_loc.is_contiguous(), "query_start_loc is int32 [num_seqs + 1]")
+    i32, f32 = torch.int32, torch.float32
+    t = tokens.numel()
+    _require(tokens.dtype is i32 and tokens.dim() == 1 and tokens.is_contiguous() and parents.dtype is i32
+             and parents.dim() == 1 and parents.numel() == t and parents.is_contiguous(),
+             "tokens and parents are int32 [T]")
+    _require(query_start_loc.dtype is i32 and query_start_loc.dim() == 1 and query_start_loc.is_contiguous()
+             and query_start_loc.numel() > 0, "query_start_loc is int32 [num_seqs + 1]")
     s = query_start_loc.numel() - 1
-    _require(target_probs.dim() == 2 and target_probs.shape[0] == t and target_probs.dtype in DTYPE_CODE,
+    dtype = target_probs.dtype
+    _require(target_probs.dim() == 2 and target_probs.shape[0] == t and dtype in DTYPE_CODE,
              "target_probs is [T][vocab] of f32, f16 or bf16")
-    _require(draft_probs is None or (draft_probs.shape == target_probs.shape
-                                     and draft_probs.dtype is target_probs.dtype),
-             "draft_probs is like target_probs")
-    _require(accept_uniforms.dtype is f32 and accept_uniforms.shape == (t,) and accept_uniforms.is_contiguous()
-             and sample_uniforms.dtype is f32 and sample_uniforms.shape == (s,) and sample_uniforms.is_contiguous(),
+    _require(accept_uniforms.dtype is f32 and accept_uniforms.dim() == 1 and accept_uniforms.numel() == t
+             and accept_uniforms.is_contiguous() and sample_uniforms.dtype is f32 and sample_uniforms.dim() == 1
+             and sample_uniforms.numel() == s and sample_uniforms.is_contiguous(),
              "accept_uniforms is float32 [T], sample_uniforms float32 [num_seqs]")
     if out is None:
         dev = tokens.device
         out = TreeVerdict(_empty((s,), i32, dev, stream), _empty((t,), i32, dev, stream),
                           _empty((s,), i32, dev, stream))
-    for x, n in zip(out, (s, t, s)):
-        _require(x.dtype is i32 and x.shape == (n,) and x.is_contiguous(),
-                 "out is (accepted_lens int32 [S], path int32 [T], next_tokens int32 [S])")
-    _require_here(tokens, parents, query_start_loc, target_probs, accept_uniforms, sample_uniforms, *out)
+        accepted, path, following = out
+    else:
+        accepted, path, following = out
+        for x, n in ((accepted, s), (path, t), (following, s)):
+            _require(x.dtype is i32 and x.shape == (n,) and x.is_contiguous(),
+                     "out is (accepted_lens int32 [S], path int32 [T], next_tokens int32 [S])")
+    dev = _current_device()
+    _refuse_elsewhere(tokens.get_device() == parents.get_device() == query_start_loc.get_device()
+                      == target_probs.get_device() == accept_uniforms.get_device() == sample_uniforms.get_device()
+                      == accepted.get_device() == path.get_device() == following.get_device() == dev)
     draft_ptr, draft_stride = None, 0
     if draft_probs is not None:
-        _require_here(draft_probs)
+        _require(draft_probs.shape == target_probs.shape and draft_probs.dtype is dtype,
+                 "draft_probs is like target_probs")
+        _refuse_elsewhere(draft_probs.get_device() == dev)
         draft_ptr, draft_stride = draft_probs.data_ptr(), _row_stride(draft_probs, "draft_probs")
-    _raise(lib.pa_verify_tree(tokens.data_ptr(), parents.data_ptr(), query_start_loc.data_ptr(), s, t,
-                              target_probs.data_ptr(), _row_stride(target_probs, "target_probs"), draft_ptr,
-                              draft_stride, target_probs.shape[1], DTYPE_CODE[target_probs.dtype],
-                              accept_uniforms.data_ptr(), sample_uniforms.data_ptr(), out[0].data_ptr(),
-                              out[1].data_ptr(), out[2].data_ptr(), _stream_ptr(stream)), "pa_verify_tree")
+    status = native.load().pa_verify_tree(tokens.data_ptr(), parents.data_ptr(), query_start_loc.data_ptr(), s, t,
+                                          target_probs.data_ptr(), _row_stride(target_probs, "target_probs"), draft_ptr,
+                                          draft_stride, target_probs.shape[1], DTYPE_CODE[dtype],
+                                          accept_uniforms.data_ptr(), sample_uniforms.data_ptr(), accepted.data_ptr(),
+                                          path.data_ptr(), following.data_ptr(), _stream_here(stream, dev))
+    if status:
+        raise PaError(status, "pa_verify_tree")
     return out
+
+
+_SHAPE, _DTYPE = operator.attrgetter("shape"), operator.attrgetter("dtype")
 
 
 class TreeCommit(NamedTuple):
@@ -571,50 +617,54 @@ def commit_tree(k_caches: Sequence[torch.Tensor], v_caches: Sequence[torch.Tenso
     plan_step's ring (``free_ring`` and ``free_state``; None: the host's manager
     keeps the blocks).  ``path`` and ``accepted_lens`` are verify_tree's.  ``out`` may
     reuse buffers, context_lens and free_state among them."""
-    lib = native.load()
-    i32 = torch.int32
-    _require(len(k_caches) == len(v_caches) and len(k_caches) > 0, "one K and one V pool per layer")
+    i32, n = torch.int32, len(k_caches)
+    _require(n == len(v_caches) and n > 0, "one K and one V pool per layer")
     pools = [*k_caches, *v_caches]
     desc, first = cache_desc(pools[0]), pools[0]
-    for x in pools:
-        _require(x.shape == first.shape and x.dtype is first.dtype and x.is_contiguous(),
-                 "all pools must match and be contiguous")
+    shape, dtype = first.shape, first.dtype
+    # 64 pools and more: one pass of a C loop for each property
+    _require(all(map(operator.eq, map(_SHAPE, pools), itertools.repeat(shape)))
+             and all(map(operator.is_, map(_DTYPE, pools), itertools.repeat(dtype)))
+             and all(map(torch.Tensor.is_contiguous, pools)), "all pools must match and be contiguous")
     s, t = context_lens.numel(), path.numel()
-    _require(context_lens.dtype is i32 and context_lens.shape == (s,) and context_lens.is_contiguous()
-             and accepted_lens.dtype is i32 and accepted_lens.shape == (s,) and accepted_lens.is_contiguous(),
-             "context_lens and accepted_lens are int32 [num_seqs]")
-    _require(path.dtype is i32 and path.shape == (t,) and path.is_contiguous(), "path is int32 [T]")
-    _require(query_start_loc.dtype is i32 and query_start_loc.shape == (s + 1,) and query_start_loc.is_contiguous(),
-             "query_start_loc is int32 [num_seqs + 1]")
-    _require(block_tables.dtype is i32 and block_tables.dim() == 2 and block_tables.shape[0] == s
-             and block_tables.is_contiguous(), "block_tables is int32 [num_seqs][max_blocks]")
+    _require(context_lens.dtype is i32 and context_lens.dim() == 1 and context_lens.is_contiguous()
+             and accepted_lens.dtype is i32 and accepted_lens.dim() == 1 and accepted_lens.numel() == s
+             and accepted_lens.is_contiguous(), "context_lens and accepted_lens are int32 [num_seqs]")
+    _require(path.dtype is i32 and path.dim() == 1 and path.is_contiguous(), "path is int32 [T]")
+    _require(query_start_loc.dtype is i32 and query_start_loc.dim() == 1 and query_start_loc.numel() == s + 1
+             and query_start_loc.is_contiguous(), "query_start_loc is int32 [num_seqs + 1]")
+    _require(block_tables.dtype is i32 and block_tables.dim() == 2 and block_tables.is_contiguous()
+             and block_tables.shape[0] == s, "block_tables is int32 [num_seqs][max_blocks]")
     _require((free_ring is None) == (free_state is None), "free_ring and free_state come together")
+    if out is None:
+        where = context_lens.device
+        out = TreeCommit(_empty((s,), i32, where, stream),
+                         None if free_ring is None else _empty((2,), i32, where, stream))
+    lens, state = out
+    _require(lens.dtype is i32 and lens.dim() == 1 and lens.numel() == s and lens.is_contiguous(),
+             "out is (context_lens int32 [S], free_state int32 [2] or None)")
+    dev = _current_device()
+    ring_ptr, ring_size, state_ptr, state_out = None, 0, None, None
     if free_ring is not None:
         _require(free_ring.dtype is i32 and free_ring.dim() == 1 and free_ring.is_contiguous()
                  and free_state.dtype is i32 and free_state.shape == (2,) and free_state.is_contiguous(),
                  "free_ring is int32 [ring_size], free_state int32 [2]")
-        _require_here(free_ring, free_state)
-    if out is None:
-        dev = context_lens.device
-        out = TreeCommit(_empty((s,), i32, dev, stream),
-                         None if free_ring is None else _empty((2,), i32, dev, stream))
-    _require(out[0].dtype is i32 and out[0].shape == (s,) and out[0].is_contiguous(),
-             "out is (context_lens int32 [S], free_state int32 [2] or None)")
-    ring_ptr, ring_size, state_ptr, state_out = None, 0, None, None
-    if free_ring is not None:
-        _require(out[1] is not None and out[1].dtype is i32 and out[1].shape == (2,) and out[1].is_contiguous(),
+        _require(state is not None and state.dtype is i32 and state.shape == (2,) and state.is_contiguous(),
                  "out is (context_lens int32 [S], free_state int32 [2])")
-        _require_here(out[1])
+        _refuse_elsewhere(free_ring.get_device() == free_state.get_device() == state.get_device() == dev)
         ring_ptr, ring_size, state_ptr, state_out = (free_ring.data_ptr(), free_ring.numel(), free_state.data_ptr(),
-                                                     out[1].data_ptr())
-    _require_here(*pools, query_start_loc, path, accepted_lens, context_lens, block_tables, out[0])
-    n = len(k_caches)
-    kp = (ctypes.c_void_p * n)(*[x.data_ptr() for x in k_caches])
-    vp = (ctypes.c_void_p * n)(*[x.data_ptr() for x in v_caches])
-    _raise(lib.pa_commit_tree(kp, vp, n, ctypes.byref(desc), query_start_loc.data_ptr(), s, t, path.data_ptr(),
-                              accepted_lens.data_ptr(), context_lens.data_ptr(), out[0].data_ptr(),
-                              block_tables.data_ptr(), block_tables.shape[1], ring_ptr, ring_size, state_ptr,
-                              state_out, _stream_ptr(stream)), "pa_commit_tree")
+                                                     state.data_ptr())
+    _refuse_elsewhere(query_start_loc.get_device() == path.get_device() == accepted_lens.get_device()
+                      == context_lens.get_device() == block_tables.get_device() == lens.get_device() == dev
+                      and all(map(operator.eq, map(torch.Tensor.get_device, pools), itertools.repeat(dev))))
+    ptrs = array.array("Q", map(torch.Tensor.data_ptr, pools))  # host array of both kinds of pools
+    at = ptrs.buffer_info()[0]
+    status = native.load().pa_commit_tree(at, at + 8 * n, n, desc, query_start_loc.data_ptr(), s, t, path.data_ptr(),
+                                          accepted_lens.data_ptr(), context_lens.data_ptr(), lens.data_ptr(),
+                                          block_tables.data_ptr(), block_tables.shape[1], ring_ptr, ring_size,
+                                          state_ptr, state_out, _stream_here(stream, dev))
+    if status:
+        raise PaError(status, "pa_commit_tree")
     return out
 
 

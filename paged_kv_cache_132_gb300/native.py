@@ -87,7 +87,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.pa_tree_attention.argtypes = [vp, vp, i64, vp, i32, vp, i32, vp, vp, desc, vp, i32, vp, i32, i32, i32,
                                           ctypes.c_float, vp, sz, vp]
         lib.pa_verify_tree.argtypes = [vp, vp, vp, i32, i32, vp, i64, vp, i64, i32, i32, vp, vp, vp, vp, vp, vp]
-        lib.pa_commit_tree.argtypes = [ctypes.POINTER(vp), ctypes.POINTER(vp), i32, desc, vp, i32, i32, vp, vp, vp, vp,
+        lib.pa_commit_tree.argtypes = [vp, vp, i32, desc, vp, i32, i32, vp, vp, vp, vp,
                                        vp, i32, vp, i32, vp, vp, vp]
         lib.pa_get_device_error.argtypes = [vp, ctypes.POINTER(i32)]
         lib.pa_status_string.argtypes = [ctypes.c_int]
