@@ -117,6 +117,7 @@ int pa_tree_attention(void* out, const void* query, int64_t query_stride, const 
     if (!aligned(workspace, 256) || workspace_bytes < lay.total) return PA_ERR_WORKSPACE;
     char* ws = static_cast<char*>(workspace);
     p.splits = reinterpret_cast<int4*>(ws);
+    p.aborted = reinterpret_cast<int*>(ws + lay.aborted);
     p.part_ml = reinterpret_cast<float2*>(ws + lay.part_ml);
     p.part_o = reinterpret_cast<float*>(ws + lay.part_o);
 

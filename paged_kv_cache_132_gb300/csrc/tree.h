@@ -102,6 +102,7 @@ struct TreeAttnParams {
     // begins before it in slot 2 c, of one that goes on behind it in slot 2 c + 1.
     int4* splits;                 // [ctas] of the item that begins in CTA c: first row, nodes, KV head, parts
                                   // (0: it does not go on behind the CTA)
+    int* aborted;                 // [ctas] 1: a wait of the CTA ran out, its parts are not there
     int row_cap;                  // rows of a slot
     float2* part_ml;              // [2 ctas][row_cap] maximum, sum
     float* part_o;                // [2 ctas][row_cap][head_dim] sums of weighted values
@@ -111,7 +112,7 @@ struct TreeAttnParams {
 };
 
 struct TreeWorkspaceLayout {
-    size_t splits, part_ml, part_o, total;
+    size_t splits, aborted, part_ml, part_o, total;
 };
 // Rows of a slot, for sequences of at most max_nodes nodes.
 inline int tree_row_cap(int max_nodes, int group) {
@@ -122,6 +123,8 @@ inline int tree_row_cap(int max_nodes, int group) {
 inline TreeWorkspaceLayout tree_workspace_layout(int row_cap, int head_dim) {
     TreeWorkspaceLayout w{};
     size_t off = (size_t)kTreeCtas * sizeof(int4);
+    w.aborted = off;
+    off += (size_t)kTreeCtas * sizeof(int);
     w.part_ml = off = (off + 255) / 256 * 256;
     off += 2 * (size_t)kTreeCtas * row_cap * sizeof(float2);
     w.part_o = off = (off + 255) / 256 * 256;

@@ -17,9 +17,11 @@
 // only an item that lies across a border between CTAs is computed in parts: at most
 // two per CTA, which the reduce kernel joins.  The list is never written: each CTA
 // finds its piece by a prefix sum over the lengths.  Pieces are counted in half tiles,
-// and an item begins with LEAD of them for what it costs beside its tiles (0.75 us,
-// against 1.45 us for a tile of 64 KiB: 64 sequences of 16 to 8192 tokens, 8 KV heads,
-// ended between 76 and 90 us by the CTA without it).
+// and an item begins with LEAD of them for what it costs beside its tiles: its first
+// copies, the tile with the nodes, the outputs -- some 2 us, a tile of 64 KiB 1.43 us at
+// the memory's rate.  (24 sequences of 128 to 2048 tokens of 40 KV heads: 121.7 us with a
+// LEAD of 1, when CTAs of short sequences ended at 126 us and the others at 98; 117.4 with
+// 2, 110.4 with 3.)
 //
 // Per K/V tile j and query tile:
 //   S  = Q K_j^T      tcgen05.mma M=128 N=128 K=d, into TMEM
@@ -43,7 +45,7 @@
 // flops a row and position), tensor cores above.
 //
 // Values a row must not see: its weight is 0, but 0 * NaN is NaN on the tensor
-// cores.  So before P V reads a V tile with positions of the tree, a warp clears
+// cores.  So before P V reads a V tile with positions of the tree, an MMA warp clears
 // its rows after the context's end and replaces non-finite elements of nodes by 0;
 // those are added again, to the rows that do attend them, by the output warps.
 //
@@ -53,9 +55,13 @@
 // apart, slabs 1 KiB.
 //
 // Warp roles (512 threads, registers moved between the groups by setmaxnreg):
-//   warps 0, 1       MMA issuers of chain 0 / 1 (warp 0 owns the TMEM allocation)
+//   warps 0, 1       MMA issuers of chain 0 / 1, and while P is made, what the V tiles with
+//                    nodes need (above); warp 0 owns the TMEM allocation
 //   warp 2           items, Q, K and V copies (TMA)
-//   warp 3           the V tiles with nodes (above)
+//   warp 3           V copies at head_dim 64, idle otherwise.  (A tile's copies cost a warp
+//                    some 2500 cycles, as long as 64 KiB take but twice as long as 32 KiB:
+//                    19 sequences of 8192 tokens with one warp 82 us, with two 62; at
+//                    head_dim 128 two are no faster.)
 //   warps 4-7, 8-11  softmax of chain 0 / 1
 //   warps 12-15      outputs, or an item's part
 // Every wait is bounded; a wait that runs out sets PA_DEVERR_TIMEOUT and makes
@@ -75,17 +81,18 @@ struct TreeShape {
     static constexpr int Q_SLAB = 128 * 128;     // bytes of one slab of 128 query rows
     static constexpr int GROUP = SLABS * 1024;   // bytes of 8 rows of keys or values
     static constexpr int TILE = 16 * GROUP;      // bytes of a K or V tile
-    static constexpr int NSLOT = D == 128 ? 5 : 8;  // K/V ring: K_0, V_0, K_1, V_1, ... one tile per slot
+    static constexpr int NSLOT = D == 128 ? 5 : 10;  // K/V ring: K_0, V_0, K_1, V_1, ... one tile per slot
+    static constexpr int NGO = 8;                // K tiles that their warp is ahead of the V tiles' warp, and more
     static constexpr int NITEM = 4;              // items announced ahead of their last reader
     static constexpr int LEAD = D == 128 ? 1 : 2;  // an item's cost beside its tiles, in half tiles
     static constexpr int SOFTMAX_WARPS = 4;      // per chain
-    static constexpr int LOAD_WARP = 2;
-    static constexpr int CHECK_WARP = 3;
+    static constexpr int LOAD_WARP = 2;          // and the next one, if K and V have a warp each
+    static constexpr bool TWO_LOADERS = D == 64;
     static constexpr int SOFTMAX_WARP = 4;       // first of eight
     static constexpr int OUT_WARP = 12;          // first of four
     static constexpr int THREADS = 512;
-    static constexpr int ITEM_READERS = 8 + 4 + 2 + 1;  // softmax, output, MMA, check warps
-    static constexpr int REGS_SOFTMAX = 176, REGS_OUT = 64, REGS_OTHER = 96;
+    static constexpr int ITEM_READERS = 8 + 4 + 2;  // softmax, output, MMA warps
+    static constexpr int REGS_SOFTMAX = 168, REGS_OUT = 80, REGS_OTHER = 96;
     static_assert(256 * REGS_SOFTMAX + 128 * REGS_OUT + 128 * REGS_OTHER <= THREADS * 128, "register split");
     // TMEM columns: S of chain i (and P over it, two per column) at 128 i, O after both.
     static constexpr uint32_t TMEM_COLS = 512;
@@ -110,10 +117,11 @@ struct TreeShape {
         uint64_t q_one[2];          // query tile of both chains landed in buffer 0 / 1 (taken in turn)
         uint64_t q_pair[2];         // query tile of chain 0 / 1 landed
         uint64_t q_empty[2];        // last S of the item from buffer 0 / 1 complete (two arrivals)
-        uint64_t kv_full[3][NSLOT]; // tile landed
+        uint64_t k_full[3][NSLOT];  // tile landed
+        uint64_t v_full[3][NSLOT];
         uint64_t kv_empty[NSLOT];   // the MMAs that read it complete (two arrivals, both by one chain if only it does)
-        uint64_t check_go[NSLOT];   // the copy of a V tile with nodes was issued (load warp)
-        uint64_t v_checked[3][NSLOT];  // ... and the tile is fit for P V (check warp)
+        uint64_t k_go[NGO];         // the copy of a K tile was issued
+        uint64_t v_checked[NSLOT];  // a V tile with nodes that both chains read is fit for P V (chain 0's warp)
         uint64_t s_full[2];         // S complete
         uint64_t p_full[2][2];      // each half of P written (softmax warps)
         uint64_t o_full[2];         // last P V of the item complete
@@ -293,7 +301,7 @@ __device__ __forceinline__ TreePiece tree_piece(const TreeAttnParams& p, typenam
 }
 
 // ---------------------------------------------------------------------------
-// load warp: items and copies
+// copies, items and query tiles
 // ---------------------------------------------------------------------------
 __device__ inline void tma_load_4d(void* dst, const CUtensorMap* map, int group, uint64_t* bar) {
     asm volatile(
@@ -303,19 +311,27 @@ __device__ inline void tma_load_4d(void* dst, const CUtensorMap* map, int group,
         : "memory");
 }
 
-template <class Shape>
+// KINDS: bit 0, K tiles (and with them items and query tiles); bit 1, V tiles.
+template <class Shape, int KINDS>
 __device__ void tree_load(const TreeAttnParams& p, typename Shape::Smem& sm, int lane, const TreePiece& piece,
                           const CUtensorMap* tq, const CUtensorMap* tk, const CUtensorMap* tv) {
+    constexpr bool LEADS = KINDS & 1;
+    constexpr int NSLOT = Shape::NSLOT;
     const uint32_t q_bytes = (uint32_t)(Shape::SLABS * p.tile_tokens * p.group * 128);
     const int block_size = 1 << p.block_shift;
     const uint32_t box_bytes = (uint32_t)block_size * Shape::SLABS * 128u;
     const int blocks_per_tile = 128 >> p.block_shift, groups_per_block = block_size >> 3;
     uint32_t q_loads = 0;                  // query tiles so far
-    uint32_t slot = 0, round = 0;
+    // The ring's entries are K_0, V_0, K_1, ...; with a warp for each kind, a V tile is copied
+    // behind the K tile of its number (k_go).
     uint32_t q_ones = 0, q_pairs = 0;      // of them for both chains, for each one
-    uint32_t filled[3] = {}, parity[3] = {};  // bit slot: whether kv_full[k][slot] was used, parity of its next phase
+    uint32_t number = 0;                  // tiles so far
+    uint32_t slot = KINDS == 2 ? 1 : 0, round = 0;  // of the next entry
+    // [kind] bit (barrier * NSLOT + slot): whether it was used, parity of its next phase
+    static_assert(3 * NSLOT <= 32, "bits");
+    uint32_t filled[2] = {}, parity[2] = {};
     bool ok = true, wrong = false;
-    if (lane == 0) p.splits[blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (LEADS && lane == 0) p.splits[blockIdx.x] = make_int4(0, 0, 0, 0);
 
     // Half tiles left of the piece, and of the sequence (in this pair of query tiles) before
     // what is left; sequences [window, window + 32) are in the lanes once one is done.
@@ -369,7 +385,7 @@ __device__ void tree_load(const TreeAttnParams& p, typename Shape::Smem& sm, int
             w.t0 = pair * 2 * p.tile_tokens;
             w.one = nodes - w.t0 <= p.tile_tokens;
             w.first_masked = (ctx - nodes) >> 7;
-            if (w.from == 0 && w.to < nt && lane == 0)  // goes on in the next CTAs
+            if (LEADS && w.from == 0 && w.to < nt && lane == 0)  // goes on in the next CTAs
                 p.splits[blockIdx.x] =
                     make_int4(row0 + w.t0, min(2 * p.tile_tokens, nodes - w.t0), head,
                               piece.cta_of(start + Shape::LEAD + 2 * (nt - 1)) - (int)blockIdx.x + 1);
@@ -377,62 +393,71 @@ __device__ void tree_load(const TreeAttnParams& p, typename Shape::Smem& sm, int
         }
         return false;
     };
-    // Lane l: the l-th block of tile j, or -2.
-    auto block_at = [&](const TreeItem& w, int j) {
-        const int at = j * blocks_per_tile + lane, blocks = (w.ctx + block_size - 1) >> p.block_shift;
-        return j < w.to && lane < blocks_per_tile && at < blocks
-                   ? __ldg(p.block_tables + (int64_t)w.seq * p.max_blocks + at)
-                   : -2;
+    // Lane l: the l-th block from tile j on, or -2 behind the item's last one.  32 blocks at a
+    // time, and the next ones while these are used: no tile waits for the table.
+    const int tiles_per_load = 32 / blocks_per_tile;
+    auto blocks_from = [&](const TreeItem& w, int j) {
+        const int at = j * blocks_per_tile + lane;
+        const int end = min(w.to * blocks_per_tile, (w.ctx + block_size - 1) >> p.block_shift);
+        return at < end ? __ldg(p.block_tables + (int64_t)w.seq * p.max_blocks + at) : -2;
     };
-    // The next item is known, and its first blocks are loading, before one's last copies: a
-    // round trip to the table for every item otherwise (4096 items of 2 tiles: 144 us).
+    // The next item is known, and its first blocks are loading, before one's last copies.
     TreeItem w{}, next{};
     bool more = take(w);
-    int id = more ? block_at(w, w.from) : -2, first_id = -2;
+    int ids = more ? blocks_from(w, w.from) : -2, next_ids = -2, first_ids = -2;
     for (int n = 0;; ++n) {
-        bool next_more = false;
-        const int st = n % Shape::NITEM;
-        tree_wait(p, sm, &sm.item_empty[st], ((uint32_t)(n / Shape::NITEM) & 1u) ^ 1u);
-        if (__any_sync(kFullMask, prompt_aborted(&sm.abort_flag))) break;
-        if (elect_one()) {
-            sm.item[st][0] = make_int4(w.row0, more ? w.n : 0, w.ctx, w.kv_head);
-            sm.item[st][1] = make_int4(w.pair, w.from, w.to, w.seq);
-            mbar_arrive(&sm.item_full[st]);
+        if (LEADS) {
+            const int st = n % Shape::NITEM;
+            tree_wait(p, sm, &sm.item_empty[st], ((uint32_t)(n / Shape::NITEM) & 1u) ^ 1u);
+            if (__any_sync(kFullMask, prompt_aborted(&sm.abort_flag))) break;
+            if (elect_one()) {
+                sm.item[st][0] = make_int4(w.row0, more ? w.n : 0, w.ctx, w.kv_head);
+                sm.item[st][1] = make_int4(w.pair, w.from, w.to, w.seq);
+                mbar_arrive(&sm.item_full[st]);
+            }
+            __syncwarp();
         }
-        __syncwarp();
         if (!more) break;
+        bool next_more = false;
 #pragma unroll 1
         for (int j = w.from; j < w.to; ++j) {
-            const int next_id = block_at(w, j + 1);
+            const int r = j - w.from, sub = r & (tiles_per_load - 1);
+            if (sub == 0) {
+                if (r > 0) ids = next_ids;
+                next_ids = blocks_from(w, j + tiles_per_load);
+            }
+            const int mine_id = __shfl_sync(kFullMask, ids, sub * blocks_per_tile + (lane & (blocks_per_tile - 1)));
+            const int id = lane < blocks_per_tile ? mine_id : -2;
             const bool good = id >= 0 && (int64_t)id < p.num_blocks;
             wrong |= id != -2 && !good;
             const uint32_t bytes = (uint32_t)__popc(__ballot_sync(kFullMask, good)) * box_bytes;
-            const int group = ((good ? id : 0) * p.num_kv_heads + w.kv_head) * groups_per_block;  // rows are below 2^31
-#pragma unroll 1
-            for (int is_v = 0; is_v < 2; ++is_v) {
+            const int group = good ? (id * p.num_kv_heads + w.kv_head) * groups_per_block : 0;  // rows are below 2^31
+            const int readers = w.readers(r);
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                if (!(KINDS >> v & 1)) continue;
+                uint64_t* const full = v ? &sm.v_full[readers][slot] : &sm.k_full[readers][slot];
+                if (v && !LEADS) tree_wait(p, sm, &sm.k_go[number % Shape::NGO], (number / Shape::NGO) & 1u);
                 tree_wait(p, sm, &sm.kv_empty[slot], round ^ 1u);
-                ok = !__any_sync(kFullMask, prompt_aborted(&sm.abort_flag));
-                if (!ok) break;
-                const int readers = w.readers(j - w.from);
-                uint64_t* const full = &sm.kv_full[readers][slot];
+                if (v == (LEADS ? 0 : 1)) {
+                    ok = !__any_sync(kFullMask, prompt_aborted(&sm.abort_flag));
+                    if (!ok) break;
+                }
                 if (elect_one()) mbar_arrive_expect_tx(full, bytes);
                 __syncwarp();
-                if (good) tma_load_4d(sm.kv[slot] + lane * box_bytes, is_v ? tv : tk, group, full);
+                if (good) tma_load_4d(sm.kv[slot] + lane * box_bytes, v ? tv : tk, group, full);
                 __syncwarp();
-                if (is_v && j >= w.first_masked && elect_one()) mbar_arrive(&sm.check_go[slot]);
-#pragma unroll
-                for (int k = 0; k < 3; ++k)
-                    if (k == readers) {
-                        filled[k] |= 1u << slot;
-                        parity[k] ^= 1u << slot;
-                    }
-                if (++slot == Shape::NSLOT) {
-                    slot = 0;
+                if (Shape::TWO_LOADERS && !v && elect_one()) mbar_arrive(&sm.k_go[number % Shape::NGO]);
+                filled[v] |= 1u << (readers * NSLOT + slot);
+                parity[v] ^= 1u << (readers * NSLOT + slot);
+                slot += KINDS == 3 ? 1 : 2;
+                if (slot >= NSLOT) {
+                    slot -= NSLOT;
                     round ^= 1u;
                 }
-                // Query tiles behind the first K and V: what the item before does not hold up first.
-                const int i = is_v;
-                if (j == w.from && (i == 0 || !w.one)) {
+                // Query tiles behind the first K tile, which the item before does not hold up.
+#pragma unroll 1
+                for (int i = 0; !v && r == 0 && i < (w.one ? 1 : 2); ++i) {
                     const uint32_t b = q_loads & 1u;
                     tree_wait(p, sm, &sm.q_empty[b], ((q_loads >> 1) & 1u) ^ 1u);
                     ok = !__any_sync(kFullMask, prompt_aborted(&sm.abort_flag));
@@ -455,21 +480,21 @@ __device__ void tree_load(const TreeAttnParams& p, typename Shape::Smem& sm, int
                         q_pairs |= 4u << i;
                     }
                 }
+                if (!ok) break;
             }
             if (!ok) break;
-            id = next_id;
-            if (j == w.from) {
-                next_more = take(next);
-                first_id = next_more ? block_at(next, next.from) : -2;
-            }
+            ++number;
+            if (r > 0) continue;
+            next_more = take(next);
+            first_ids = next_more ? blocks_from(next, next.from) : -2;
         }
         if (!ok) break;
         w = next;
         more = next_more;
-        id = first_id;
+        ids = first_ids;
     }
     if (wrong) set_error(p.err, PA_DEVERR_BLOCK_ID);
-    pdl_launch_dependents();
+    if (LEADS) pdl_launch_dependents();
     if (lane == 0) {
         // Every copy this warp issued lands before the CTA exits (bounded).
         bool drained = true;
@@ -481,14 +506,54 @@ __device__ void tree_load(const TreeAttnParams& p, typename Shape::Smem& sm, int
                 drained = mbar_wait_bounded(&sm.q_pair[b], (q_pairs >> b & 1u) ^ 1u, p.wait_limit_ns) && drained;
         }
 #pragma unroll
-        for (int k = 0; k < 3; ++k)
+        for (int v = 0; v < 2; ++v)
 #pragma unroll 1
-            for (int s = 0; s < Shape::NSLOT; ++s)
-                if (filled[k] >> s & 1u)
-                    drained = mbar_wait_bounded(&sm.kv_full[k][s], (parity[k] >> s & 1u) ^ 1u, p.wait_limit_ns) && drained;
+            for (int k = 0; k < 3 * NSLOT; ++k)
+                if (filled[v] >> k & 1u)
+                    drained = mbar_wait_bounded(v ? &sm.v_full[0][k] : &sm.k_full[0][k], (parity[v] >> k & 1u) ^ 1u,
+                                                p.wait_limit_ns) && drained;
         if (!drained) set_error(p.err, PA_DEVERR_TIMEOUT);
     }
     __syncwarp();
+}
+
+// ---------------------------------------------------------------------------
+// V tiles with nodes (a warp)
+// ---------------------------------------------------------------------------
+// Clears rows [rows, all) of a tile and replaces non-finite elements of rows [first, rows)
+// by 0; true in the lanes that found any.
+template <typename T, class Shape>
+__device__ __noinline__ bool tree_check_tile(uint8_t* tile, int first, int rows, int all, int lane) {
+    constexpr int CHUNKS = Shape::SLABS * 8;  // 16-byte chunks of a row
+    constexpr int STEP = 32 / CHUNKS;         // rows of one pass of the warp
+    const int my_chunk = lane % CHUNKS, my_row = lane / CHUNKS;
+    // This lane's chunk of rows my_row, + STEP, ...
+    uint8_t* const column = tile + (my_chunk >> 3) * 1024 + (my_chunk & 7) * 16;
+    auto at = [&](int row) { return reinterpret_cast<uint4*>(column + (row >> 3) * Shape::GROUP + (row & 7) * 128); };
+    for (int row = rows + my_row; row < all; row += STEP) *at(row) = make_uint4(0u, 0u, 0u, 0u);
+    // 0 * v: NaN where v is infinite or NaN, and then for good in the sum.
+    uint32_t acc = 0u;
+#pragma unroll 4
+    for (int row = first + my_row; row < rows; row += STEP) {
+        const uint4 v = *at(row);
+        acc = times_zero_plus<T>(v.x, acc);
+        acc = times_zero_plus<T>(v.y, acc);
+        acc = times_zero_plus<T>(v.z, acc);
+        acc = times_zero_plus<T>(v.w, acc);
+    }
+    const bool bad_here = (acc & 0x7fff7fffu) != 0;
+    if (bad_here) {
+#pragma unroll 1
+        for (int row = first + my_row; row < rows; row += STEP) {
+            uint32_t* v = reinterpret_cast<uint32_t*>(at(row));
+#pragma unroll 1
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t bad = nonfinite2<T>(v[e]);
+                v[e] &= ~(((bad >> 31) * 0xffff0000u) | ((bad >> 15 & 1u) * 0xffffu));
+            }
+        }
+    }
+    return bad_here;
 }
 
 // ---------------------------------------------------------------------------
@@ -518,10 +583,11 @@ __device__ __forceinline__ void tree_mma_ts(uint32_t d_tmem, uint32_t a_tmem, ui
         : "memory");
 }
 
-template <class Shape, bool BF16>
+template <typename T, class Shape>
 __device__ void tree_mma(const TreeAttnParams& p, typename Shape::Smem& sm, uint32_t tmem, int i, int lane) {
     using Smem = typename Shape::Smem;
     constexpr int D = Shape::SLABS * 64;
+    constexpr bool BF16 = std::is_same<T, __nv_bfloat16>::value;
     constexpr uint32_t IDESC_O = mma_idesc_f16(BF16, true, Shape::BM, D);
     constexpr uint32_t IDESC_S = mma_idesc_f16(BF16, false, Shape::BM, 128);
     constexpr uint32_t IDESC_S64 = mma_idesc_f16(BF16, false, Shape::BM, 64);
@@ -550,12 +616,12 @@ __device__ void tree_mma(const TreeAttnParams& p, typename Shape::Smem& sm, uint
                                first && ks == 0);
     };
 
-    uint32_t ring = 0;       // tiles of the ring before the item
+    uint32_t before = 0;     // K/V tiles before the item
     uint32_t nq = 0;         // query tiles before the item
     uint32_t no = 0, np = 0; // parities of the chain's O and P so far
-    // Bit slot: parity of the next phase of kv_full and v_checked, of this chain's own
-    // barriers and of both chains'; bit b of q_ones: of q_one[b].
-    uint32_t full_own = 0, full_both = 0, checked_own = 0, checked_both = 0, q_ones = 0, q_pairs = 0;
+    // Bit slot: parity of the next phase of k_full and v_full, of this chain's own
+    // barriers and of both chains', and of v_checked; bit b of q_ones: of q_one[b].
+    uint32_t k_own = 0, k_both = 0, v_own = 0, v_both = 0, checked = 0, q_ones = 0, q_pairs = 0;
     int n = 0;
     TreeItem w;
     while (tree_next_item<Shape>(p, sm, lane, n, w)) {
@@ -572,19 +638,18 @@ __device__ void tree_mma(const TreeAttnParams& p, typename Shape::Smem& sm, uint
         } else {
             tree_wait(p, sm, &sm.q_pair[i], q_pairs++ & 1u);
         }
-        uint32_t& full = w.one ? full_own : full_both;
-        uint32_t& checked = w.one ? checked_own : checked_both;
+        uint32_t& k_par = w.one ? k_own : k_both;
+        uint32_t& v_par = w.one ? v_own : v_both;
         const int readers = w.one ? i : 2;
         const int last = w.one ? (((tiles - 1) & 1) == i ? tiles - 1 : tiles - 2) : tiles - 1;  // own tile
         bool first = true;
 #pragma unroll 1
         for (int r = 0; r < tiles; ++r) {
-            const uint32_t kat = ring + 2 * r, vat = kat + 1;
-            const uint32_t kslot = kat % Shape::NSLOT, vslot = vat % Shape::NSLOT;
             if (!w.own(i, r)) continue;
+            const uint32_t entry = 2 * (before + r), kslot = entry % Shape::NSLOT, vslot = (entry + 1) % Shape::NSLOT;
             const int cols = w.ctx - (w.from + r) * Shape::BN;
-            tree_wait(p, sm, &sm.kv_full[readers][kslot], full >> kslot & 1u);
-            full ^= 1u << kslot;
+            tree_wait(p, sm, &sm.k_full[readers][kslot], k_par >> kslot & 1u);
+            k_par ^= 1u << kslot;
             tc_fence_after_sync();
             if (elect_one()) {
                 issue_s(q_lo + t * Q16, kslot, cols > 64);
@@ -597,11 +662,22 @@ __device__ void tree_mma(const TreeAttnParams& p, typename Shape::Smem& sm, uint
                 }
             }
             __syncwarp();
-            tree_wait(p, sm, &sm.kv_full[readers][vslot], full >> vslot & 1u);
-            full ^= 1u << vslot;
+            tree_wait(p, sm, &sm.v_full[readers][vslot], v_par >> vslot & 1u);
+            v_par ^= 1u << vslot;
             if (w.from + r >= w.first_masked) {
-                tree_wait(p, sm, &sm.v_checked[readers][vslot], checked >> vslot & 1u);
-                checked ^= 1u << vslot;
+                if (w.one || i == 0) {
+                    // Rows before the first node are attended by all.
+                    const int rows = min(Shape::BN, cols);
+                    if (tree_check_tile<T, Shape>(sm.kv[vslot], max(w.base - (w.from + r) * Shape::BN, 0), rows,
+                                                  (rows + 63) & ~63, lane))
+                        atomicMax(&sm.last_dirty, n - 1);  // n: items announced so far
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (!w.one && lane == 0) mbar_arrive(&sm.v_checked[vslot]);
+                } else {
+                    tree_wait(p, sm, &sm.v_checked[vslot], checked >> vslot & 1u);
+                    checked ^= 1u << vslot;
+                }
             }
             if (first) tree_wait(p, sm, &sm.o_empty[i], (no++ & 1u) ^ 1u);  // read by the output warps
             tree_wait(p, sm, &sm.p_full[i][0], np & 1u);
@@ -619,7 +695,7 @@ __device__ void tree_mma(const TreeAttnParams& p, typename Shape::Smem& sm, uint
             __syncwarp();
             first = false;
         }
-        ring += 2 * tiles;
+        before += tiles;
     }
     // Nothing this warp issued may still be running when TMEM is released.
     if (elect_one()) mma_commit(&sm.mma_done[i]);
@@ -781,80 +857,9 @@ __device__ void tree_softmax(const TreeAttnParams& p, typename Shape::Smem& sm, 
 }
 
 // ---------------------------------------------------------------------------
-// check warp: V tiles with nodes
-// ---------------------------------------------------------------------------
-template <typename T, class Shape>
-__device__ void tree_check(const TreeAttnParams& p, typename Shape::Smem& sm, int lane) {
-    constexpr int CHUNKS = Shape::SLABS * 8;  // 16-byte chunks of a row
-    constexpr int STEP = 32 / CHUNKS;         // rows of one pass of the warp
-    const int my_chunk = lane % CHUNKS, my_row = lane / CHUNKS;
-    uint32_t ring = 0;    // tiles of the ring before the item
-    uint32_t parity = 0;  // bit slot: of the slot's next V tile with nodes
-    uint32_t full[3] = {};  // bit slot: of the next phase of kv_full
-    int n = 0;
-    TreeItem w;
-    while (tree_next_item<Shape>(p, sm, lane, n, w)) {
-        for (int j = w.from; j < w.to; ++j) {
-            const uint32_t tile = ring + 2 * (j - w.from) + 1;
-            const uint32_t slot = tile % Shape::NSLOT, kslot = (tile - 1) % Shape::NSLOT;
-            const int readers = w.readers(j - w.from);
-            uint32_t full_parity = 0;
-#pragma unroll
-            for (int k = 0; k < 3; ++k)
-                if (k == readers) {
-                    full[k] ^= 1u << kslot;
-                    full_parity = full[k] >> slot & 1u;
-                    full[k] ^= 1u << slot;
-                }
-            if (j < w.first_masked) continue;
-            // Issued first: before that the barrier may still be two phases back,
-            // which its parity does not tell from complete.
-            tree_wait(p, sm, &sm.check_go[slot], (parity >> slot) & 1u);
-            tree_wait(p, sm, &sm.kv_full[readers][slot], full_parity);
-            parity ^= 1u << slot;
-            // Rows before the first node are attended by all.
-            const int first = max(w.base - j * Shape::BN, 0);
-            const int rows = min(Shape::BN, w.ctx - j * Shape::BN), all = (rows + 63) & ~63;
-            // This lane's chunk of rows lane / CHUNKS, + STEP, ...
-            uint8_t* const column = sm.kv[slot] + (my_chunk >> 3) * 1024 + (my_chunk & 7) * 16;
-            auto at = [&](int row) {
-                return reinterpret_cast<uint4*>(column + (row >> 3) * Shape::GROUP + (row & 7) * 128);
-            };
-            for (int row = rows + my_row; row < all; row += STEP) *at(row) = make_uint4(0u, 0u, 0u, 0u);
-            // 0 * v: NaN where v is infinite or NaN, and then for good in the sum.
-            uint32_t acc[4] = {0u, 0u, 0u, 0u};
-#pragma unroll 8
-            for (int row = first + my_row; row < rows; row += STEP) {
-                const uint4 v = *at(row);
-                acc[0] = times_zero_plus<T>(v.x, acc[0]);
-                acc[1] = times_zero_plus<T>(v.y, acc[1]);
-                acc[2] = times_zero_plus<T>(v.z, acc[2]);
-                acc[3] = times_zero_plus<T>(v.w, acc[3]);
-            }
-            if ((acc[0] | acc[1] | acc[2] | acc[3]) & 0x7fff7fffu) {
-#pragma unroll 1
-                for (int row = first + my_row; row < rows; row += STEP) {
-                    uint32_t* v = reinterpret_cast<uint32_t*>(at(row));
-#pragma unroll 1
-                    for (int e = 0; e < 4; ++e) {
-                        const uint32_t bad = nonfinite2<T>(v[e]);
-                        v[e] &= ~(((bad >> 31) * 0xffff0000u) | ((bad >> 15 & 1u) * 0xffffu));
-                    }
-                }
-                atomicMax(&sm.last_dirty, n - 1);  // n: items announced so far
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.v_checked[readers][slot]);
-        }
-        ring += 2 * w.tiles();
-    }
-}
-
-// ---------------------------------------------------------------------------
 // output warps
 // ---------------------------------------------------------------------------
-// The non-finite values of nodes that the check warp took out of the item's V tiles:
+// The non-finite values of nodes that were taken out of the item's V tiles:
 // each decides its column of the rows that attend it.  Added to `dst` (the stored
 // output, or the stored part) by the thread that stored it.
 template <typename T, int D, typename O>
@@ -1005,12 +1010,13 @@ __global__ void __launch_bounds__(TreeShape<D>::THREADS, 1)
         }
         for (int s = 0; s < Shape::NSLOT; ++s) {
             for (int k = 0; k < 3; ++k) {
-                mbar_init(&sm.kv_full[k][s], s == 0 && (p.debug_flags & kDebugDropFirstFill) ? 2 : 1);
-                mbar_init(&sm.v_checked[k][s], 1);
+                mbar_init(&sm.k_full[k][s], s == 0 && (p.debug_flags & kDebugDropFirstFill) ? 2 : 1);
+                mbar_init(&sm.v_full[k][s], 1);
             }
             mbar_init(&sm.kv_empty[s], 2);
-            mbar_init(&sm.check_go[s], 1);
+            mbar_init(&sm.v_checked[s], 1);
         }
+        for (int s = 0; s < Shape::NGO; ++s) mbar_init(&sm.k_go[s], 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.q_one[i], 1);
             mbar_init(&sm.q_pair[i], 1);
@@ -1042,11 +1048,13 @@ __global__ void __launch_bounds__(TreeShape<D>::THREADS, 1)
     if (warp < Shape::SOFTMAX_WARP) {
         regs_dec<Shape::REGS_OTHER>();
         if (warp < Shape::LOAD_WARP)
-            tree_mma<Shape, std::is_same<T, __nv_bfloat16>::value>(p, sm, tmem, warp, lane);
-        else if (warp == Shape::LOAD_WARP)
-            tree_load<Shape>(p, sm, lane, piece, &tmap_q, &tmap_k, &tmap_v);
-        else
-            tree_check<T, Shape>(p, sm, lane);
+            tree_mma<T, Shape>(p, sm, tmem, warp, lane);
+        else if (!Shape::TWO_LOADERS && warp == Shape::LOAD_WARP)
+            tree_load<Shape, 3>(p, sm, lane, piece, &tmap_q, &tmap_k, &tmap_v);
+        else if (Shape::TWO_LOADERS && warp == Shape::LOAD_WARP)
+            tree_load<Shape, 1>(p, sm, lane, piece, &tmap_q, &tmap_k, &tmap_v);
+        else if (Shape::TWO_LOADERS)
+            tree_load<Shape, 2>(p, sm, lane, piece, &tmap_q, &tmap_k, &tmap_v);
     } else if (warp < Shape::OUT_WARP) {
         regs_inc<Shape::REGS_SOFTMAX>();
         const int v = warp - Shape::SOFTMAX_WARP;
@@ -1059,7 +1067,10 @@ __global__ void __launch_bounds__(TreeShape<D>::THREADS, 1)
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    if (threadIdx.x == 0 && sm.abort_flag) set_error(p.err, PA_DEVERR_TIMEOUT);
+    if (threadIdx.x == 0) {
+        p.aborted[blockIdx.x] = sm.abort_flag;
+        if (sm.abort_flag) set_error(p.err, PA_DEVERR_TIMEOUT);
+    }
     __syncwarp();
     if (warp == 0) tmem_dealloc(tmem, Shape::TMEM_COLS);
 }
@@ -1085,6 +1096,10 @@ __global__ void __launch_bounds__(kTreeReduceThreads) tree_reduce_kernel(const _
     const int4 item = __ldcg(p.splits + blockIdx.x);
     const int parts = item.w;
     if (parts == 0) return;
+    // A part that is not there: the rows stay as they were.
+    bool missing = false;
+    for (int k = lane; k < parts; k += 32) missing |= __ldcg(p.aborted + blockIdx.x + k) != 0;
+    if (__any_sync(kFullMask, missing)) return;
     auto slot = [&](int k) { return ((int64_t)(blockIdx.x + k) * 2 + (k == 0 ? 1 : 0)) * p.row_cap; };
     // Rows of the second query tile stand 128 behind the first one's.
     const int rows = item.y <= p.tile_tokens ? item.y * p.group : 128 + (item.y - p.tile_tokens) * p.group;
