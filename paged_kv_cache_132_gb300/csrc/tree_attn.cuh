@@ -84,7 +84,7 @@ struct TreeShape {
     static constexpr int NSLOT = D == 128 ? 5 : 10;  // K/V ring: K_0, V_0, K_1, V_1, ... one tile per slot
     static constexpr int NGO = 8;                // K tiles that their warp is ahead of the V tiles' warp, and more
     static constexpr int NITEM = 4;              // items announced ahead of their last reader
-    static constexpr int LEAD = D == 128 ? 1 : 2;  // an item's cost beside its tiles, in half tiles
+    static constexpr int LEAD = D == 128 ? 3 : 4;  // an item's cost beside its tiles, in half tiles
     static constexpr int SOFTMAX_WARPS = 4;      // per chain
     static constexpr int LOAD_WARP = 2;          // and the next one, if K and V have a warp each
     static constexpr bool TWO_LOADERS = D == 64;
