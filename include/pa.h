@@ -17,6 +17,9 @@
  *   - pa_prefill           : prompt-phase attention of new tokens over a
  *       cached prefix, causal within the new tokens
  *       ("PagedAttention 论文精读笔记", §6.3 and §5.3)
+ * and on the steps around it (pa_plan_step, pa_rotary_and_cache,
+ * pa_prompt_attention), those of drafted trees among them (pa_plan_tree,
+ * pa_tree_attention, pa_verify_tree, pa_commit_tree).
  *
  * Conventions shared by every call
  *   - Pointers named "device" are CUDA device pointers of the current device;
@@ -416,7 +419,8 @@ int pa_prompt_attention(void *out, const void *query, int64_t query_stride,
  * 0 in a sequence, parents before children; node 0 is the sequence's last token, whose
  * row of the target predicts the first drafted ones.  At most PA_MAX_TREE_NODES nodes
  * a sequence.  A sequence whose start rows or lengths break the rules (rows decreasing
- * or past num_tokens, n_s > context_lens[s]) sets PA_DEVERR_CONTEXT_LEN.
+ * or past num_tokens, n_s > context_lens[s]) sets PA_DEVERR_CONTEXT_LEN.  An output of
+ * these calls shares memory with an input only where a call says so.
  */
 #define PA_MAX_TREE_NODES 1024
 

@@ -17,6 +17,12 @@ struct NvtxRange {
     ~NvtxRange() { nvtxRangePop(); }
 };
 
+// Does an output of `bytes` bytes share memory with an input of `input_bytes`?
+bool overlap(const void* out, int64_t bytes, const void* in, int64_t input_bytes) {
+    const auto a = reinterpret_cast<uintptr_t>(out), b = reinterpret_cast<uintptr_t>(in);
+    return in && bytes > 0 && input_bytes > 0 && a < b + (uint64_t)input_bytes && b < a + (uint64_t)bytes;
+}
+
 }  // namespace
 
 extern "C" {
@@ -30,6 +36,11 @@ int pa_plan_tree(const int32_t* parents, const int32_t* query_start_loc, const i
     if (!aligned(query_start_loc, 4) || (num_seqs > 0 && !aligned(context_lens, 4))) return PA_ERR_INVALID_ARG;
     if (mask_words > PA_MAX_TREE_NODES / 64) return PA_ERR_UNSUPPORTED;
     if (num_tokens == 0) return PA_OK;
+    const int64_t rows = 4LL * num_tokens, mask_bytes = 8LL * num_tokens * mask_words;
+    for (const void* in : {parents, query_start_loc, context_lens}) {
+        const int64_t bytes = in == parents ? rows : 4LL * (num_seqs + (in == query_start_loc));
+        if (overlap(positions, rows, in, bytes) || overlap(tree_mask, mask_bytes, in, bytes)) return PA_ERR_INVALID_ARG;
+    }
     const int dev = current_device();
     if (dev < 0) return PA_ERR_CUDA;
     int* err = error_word(dev);
@@ -81,7 +92,7 @@ int pa_tree_attention(void* out, const void* query, int64_t query_stride, const 
     if (!(shape.head_dim == 64 || shape.head_dim == 128)) return PA_ERR_UNSUPPORTED;
     if (!(shape.block_size == 8 || shape.block_size == 16 || shape.block_size == 32)) return PA_ERR_UNSUPPORTED;
     constexpr int64_t kMaxStride = (1LL << 39) - 1;  // a tensor copy's strides are below 2^40 bytes
-    if (query_stride > kMaxStride) return PA_ERR_UNSUPPORTED;
+    if (query_stride > kMaxStride || (double)query_stride * num_tokens > 1e17) return PA_ERR_UNSUPPORTED;
 
     pa::TreeAttnParams p{};
     p.out = out;
@@ -109,12 +120,17 @@ int pa_tree_attention(void* out, const void* query, int64_t query_stride, const 
     p.row_cap = pa::tree_row_cap(nodes, group);
     p.wait_limit_ns = wait_limit_ns();
     p.debug_flags = option(PA_OPT_DROP_FIRST_FILL) ? pa::kDebugDropFirstFill : 0;
-    // The longest list of K/V tiles these tables allow; its half tiles stay 32-bit numbers.
+    // The longest list of K/V tiles these tables allow; its half tiles, with those that each
+    // item begins with, stay 32-bit numbers.
     const double items = (double)num_seqs * p.max_pairs * num_kv_heads;
     const double tiles = items * (double)((p.ctx_cap + 127LL) / 128);
-    if (2. * tiles + 2. * items > 2147483647.) return PA_ERR_UNSUPPORTED;
+    if (2. * tiles + pa::kTreeMaxLead * items > 2147483647.) return PA_ERR_UNSUPPORTED;
     const pa::TreeWorkspaceLayout lay = pa::tree_workspace_layout(p.row_cap, shape.head_dim);
     if (!aligned(workspace, 256) || workspace_bytes < lay.total) return PA_ERR_WORKSPACE;
+    const int64_t row = (int64_t)num_heads * shape.head_dim;
+    if (overlap(out, num_tokens * row * shape.elem_bytes, query,
+                ((num_tokens - 1) * query_stride + row) * shape.elem_bytes))
+        return PA_ERR_INVALID_ARG;
     char* ws = static_cast<char*>(workspace);
     p.splits = reinterpret_cast<int4*>(ws);
     p.aborted = reinterpret_cast<int*>(ws + lay.aborted);
@@ -161,6 +177,14 @@ int pa_verify_tree(const int32_t* tokens, const int32_t* parents, const int32_t*
                            !aligned(path, 4)))
         return PA_ERR_INVALID_ARG;
     if (vocab_size > pa::kMaxVocab || num_seqs > (1 << 24)) return PA_ERR_UNSUPPORTED;
+    // A sequence's results are written while others, and its own path, are still read.
+    const int64_t rows = 4LL * num_tokens, seqs = 4LL * num_seqs;
+    for (const void* in : {tokens, parents})
+        if (overlap(path, rows, in, rows) || overlap(accepted_lens, seqs, in, rows) || overlap(next_tokens, seqs, in, rows))
+            return PA_ERR_INVALID_ARG;
+    if (overlap(path, rows, query_start_loc, seqs + 4) || overlap(accepted_lens, seqs, query_start_loc, seqs + 4) ||
+        overlap(next_tokens, seqs, query_start_loc, seqs + 4))
+        return PA_ERR_INVALID_ARG;
     const int dev = current_device();
     if (dev < 0) return PA_ERR_CUDA;
     int* err = error_word(dev);
@@ -207,6 +231,12 @@ int pa_commit_tree(void* const* k_caches, void* const* v_caches, int32_t num_lay
     for (int l = 0; l < num_layers; ++l)
         if (!aligned(k_caches[l], 16) || !aligned(v_caches[l], 16)) return PA_ERR_INVALID_ARG;
     if (num_seqs > pa::kMaxStepSeqs || (free_ring && ring_size >= pa::kMaxStepCount)) return PA_ERR_UNSUPPORTED;
+    // The moves read what the lengths are made of; context_lens itself is overwritten behind them.
+    const int64_t seqs = 4LL * num_seqs;
+    if (overlap(context_lens_out, seqs, accepted_lens, seqs) || overlap(context_lens_out, seqs, path, 4LL * num_tokens) ||
+        overlap(context_lens_out, seqs, query_start_loc, seqs + 4) ||
+        (context_lens_out != context_lens && overlap(context_lens_out, seqs, context_lens, seqs)))
+        return PA_ERR_INVALID_ARG;
     const int dev = current_device();
     if (dev < 0) return PA_ERR_CUDA;
     int* err = error_word(dev);

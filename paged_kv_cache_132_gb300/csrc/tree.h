@@ -74,6 +74,7 @@ cudaError_t launch_tree_verify(const TreeVerifyParams& p, int dtype, int sms, cu
 
 // ---- attention of the nodes over the cache (tree_attn*.cu) ----------------------
 constexpr int kTreeCtas = 152;    // CTAs of a call at most: what the workspace has room for
+constexpr int kTreeMaxLead = 4;   // half tiles that an item begins with, at most
 constexpr int kTreePairRows = 256;  // query rows (node, grouped head) of a work item at most: two tiles of 128
 
 struct TreeAttnParams {

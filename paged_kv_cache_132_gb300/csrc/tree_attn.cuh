@@ -98,6 +98,7 @@ struct TreeShape {
     static constexpr uint32_t TMEM_COLS = 512;
     static constexpr uint32_t O_COL = 2 * BN;
     static_assert(D == 64 || D == 128, "head_dim 64 or 128");
+    static_assert(LEAD <= kTreeMaxLead, "the host's bound of the list");
 
     struct Smem {
         alignas(1024) uint8_t q[2][SLABS][Q_SLAB];

@@ -136,3 +136,32 @@ def _commit(lib, **over):
 ])
 def test_commit_tree(lib, over, status):
     assert _commit(lib, **over) == status
+
+
+# Buffers apart, so that only the overlap that a case makes is one.
+def _apart(*names):
+    return {n: FAKE + (i + 1) * (1 << 24) for i, n in enumerate(names)}
+
+
+def test_outputs_that_overlap_inputs(lib):
+    a = _apart("parents", "qsl", "ctx", "pos", "mask")
+    for over in (dict(pos=a["parents"]), dict(pos=a["parents"] + 16), dict(pos=a["parents"] - 16), dict(pos=a["qsl"] + 8),
+                 dict(mask=a["ctx"]), dict(mask=a["parents"] - 32)):
+        assert _plan(lib, **{**a, **over}) == -1, over
+    a = _apart("out", "q", "qsl", "mask", "k", "v", "tables", "ctx", "ws")
+    a.update(qs=512)                            # a slice of wider rows
+    for at in (0, 9 * 512 - 32, 8 * 1024 + 480, -(9 * 512 - 32)):
+        assert _attend(lib, **{**a, "out": a["q"] + at}) == -1, at
+    a = _apart("ids", "parents", "qsl", "p", "q", "au", "su", "lens", "path", "next")
+    for over in (dict(path=a["ids"]), dict(path=a["parents"] + 4), dict(lens=a["qsl"]), dict(next=a["qsl"] + 8),
+                 dict(next=a["parents"] - 4)):
+        assert _verify(lib, **{**a, **over}) == -1, over
+    a = _apart("qsl", "path", "lens", "ctx", "ctx_out", "tables", "ring", "free", "free_out")
+    for over in (dict(ctx_out=a["lens"]), dict(ctx_out=a["path"] + 32), dict(ctx_out=a["qsl"] + 8),
+                 dict(ctx_out=a["ctx"] + 4)):
+        assert _commit(lib, **{**a, **over}) == -1, over
+
+
+def test_list_of_tiles_with_what_items_begin_with(lib):
+    # 4e8 items of one tile: 2 half tiles each and up to 4 that an item begins with pass 2^31
+    assert _attend(lib, seqs=200_000_000, max_blocks=8) == -2
