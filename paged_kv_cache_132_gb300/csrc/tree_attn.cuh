@@ -42,7 +42,13 @@
 // time, not two, and the chain (2700 cycles) is hidden behind the other one.
 //
 // Bound: HBM up to about 128 rows (2 d e bytes a position and KV head against 4 d
-// flops a row and position), tensor cores above.
+// flops a row and position), tensor cores above.  Measured (graph replay): 64 sequences
+// of 16 nodes, lognormal contexts up to 8192, 32/8 heads of 128, bf16: 92.4-94.5 us, 5.4
+// TB/s; 32 of 40 to 64 nodes, 1024 to 8192 tokens: 152 us, 4.7 TB/s and 0.93 PFLOP/s at
+// once; 24 of 1 to 25 nodes, 128 to 2048 tokens, 40/40 heads, f16: 111 us, 5.4 TB/s; 3 of
+// 31 nodes and 30 to 33 thousand tokens, 16/4 heads of 64: 30.4 us, 3.2 TB/s.  One
+// short sequence, all of it latency: 10.9 us (launch, the list's prefix sum, the first
+// copies, S, softmax, P V, a part, the reduce kernel), which the others pay beside theirs.
 //
 // Values a row must not see: its weight is 0, but 0 * NaN is NaN on the tensor
 // cores.  So before P V reads a V tile with positions of the tree, an MMA warp clears

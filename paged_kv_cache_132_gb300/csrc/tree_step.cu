@@ -6,7 +6,8 @@
 // from its node (in shared memory, one step some 30 cycles) and sets a bit for each.
 // Parents stand before their nodes, so the words of the mask row are finished from
 // the last to the first.  Its position is the tree's first one plus its depth (a
-// chain's is plan_step's).  Bound: latency.
+// chain's is plan_step's).  Bound: latency: 2.7 us for 64 trees of 16 nodes (graph
+// replay, launch included), 4.4 us for 2048 trees of up to 61.
 //
 // Commit.  Node path[i] of the accepted path becomes the i-th token behind the cached
 // ones: its rows move to that place in every layer's pools.  As path[i] >= i and
@@ -16,7 +17,9 @@
 // sequence and some of the layers).  The lengths are cut, and the blocks that only
 // held refused nodes go back behind the ring's last free entry, sequence after
 // sequence (a prefix sum), by one CTA: of the same launch, unless it overwrites the
-// lengths that the others read.  Bound: HBM for batches, latency below.
+// lengths that the others read.  Bound: HBM for batches, latency below: 2.9 us for one
+// sequence and four layers; 7.7 us for 96 sequences and 32 layers (graph replay; 26 MB
+// read and written in pieces of 256 bytes, 3.4 TB/s).
 #include "common.cuh"
 #include "tree.h"
 

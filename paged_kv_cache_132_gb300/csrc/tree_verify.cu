@@ -32,7 +32,11 @@
 // needed: at a refusal, and for the last token unless the last refusal's sums serve.
 // The segments' sums stay in shared memory, so the token costs one more segment.
 //
-// Bound: HBM for batches (a row of p and mostly one of q each sequence), latency below.
+// Bound: latency.  A sum is one pass over the row by all CTAs at the rate of issue, and a
+// refusal's sum must be known before the next child is tried.  Graph replay: 9.4 us for one
+// sequence of 6 nodes and 32 000 tokens; 32.9 us for 64 sequences of 12 nodes and 128 256
+// tokens in f32, which need 1.3 passes on average and up to 3; 16.6 us for 200 sequences
+// of looked-up tokens out of 50 021 in bf16, of which the last token's segment 3.5 us.
 #include <cooperative_groups.h>
 #include <type_traits>
 
@@ -571,6 +575,7 @@ cudaError_t launch_t(const TreeVerifyParams& p, int ranks, cudaStream_t stream) 
 
 cudaError_t launch_tree_verify(const TreeVerifyParams& p, int dtype, int sms, cudaStream_t stream) {
     // As many CTAs to a sequence as keep two on every SM, each with 8 segments at least.
+    // (The 200 sequences above: 18.3 us so, 22.9 us with up to three or four CTAs an SM.)
     int ranks = 8;
     while (ranks > 1 && ((int64_t)p.num_seqs * ranks > 2LL * sms || p.vocab < ranks * 8 * kSegment)) ranks /= 2;
     switch (dtype) {
