@@ -31,7 +31,7 @@ constexpr unsigned kAll = 0xffffffffu;
 // ---------------------------------------------------------------------------
 // plan
 // ---------------------------------------------------------------------------
-constexpr int kTreeStaged = 1024;  // parents in shared memory
+constexpr int kTreeStaged = PA_MAX_TREE_NODES;  // parents in shared memory
 
 __global__ void __launch_bounds__(128) tree_plan_kernel(const TreePlanParams p) {
     __shared__ int staged[kTreeStaged];
@@ -55,7 +55,6 @@ __global__ void __launch_bounds__(128) tree_plan_kernel(const TreePlanParams p) 
         }
         return;
     }
-    const bool in_shared = n <= kTreeStaged;
     bool bad = false;
     for (int i = threadIdx.x; i < n; i += blockDim.x) {
         int up = p.parents[row0 + i];
@@ -63,7 +62,7 @@ __global__ void __launch_bounds__(128) tree_plan_kernel(const TreePlanParams p) 
             bad = true;
             up = -1;
         }
-        if (in_shared) staged[i] = up;
+        staged[i] = up;
     }
     if (bad) set_error(p.err, PA_DEVERR_TREE);
     __syncthreads();
@@ -77,8 +76,8 @@ __global__ void __launch_bounds__(128) tree_plan_kernel(const TreePlanParams p) 
                 bits = 0;
             }
             bits |= 1ull << (at & 63);
-            const int up = in_shared ? staged[at] : p.parents[row0 + at];
-            if (up < 0 || up >= at) break;
+            const int up = staged[at];
+            if (up < 0) break;
             ++depth;
             at = up;
         }

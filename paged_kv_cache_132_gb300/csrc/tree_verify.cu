@@ -51,7 +51,7 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kNodes = 1024;        // PA_MAX_TREE_NODES
+constexpr int kNodes = PA_MAX_TREE_NODES;
 constexpr int kSegment = 512;       // entries of a segment: 16 a lane
 constexpr int kSegments = kMaxVocab / kSegment + 1;
 constexpr int kRanks = 8;            // CTAs of a cluster at most
