@@ -520,9 +520,11 @@ int pa_tree_attention(void *out, const void *query, int64_t query_stride, const 
  *   path              device, int32 [num_tokens]: from each sequence's first row on the
  *                     accepted nodes, then -1; other rows are not written
  *   next_tokens       device, int32 [num_seqs]
- * Sums are exact to 2^-56 a weight, whatever the order.  A sequence without nodes or
- * with bad lengths gets accepted length 0 and token -1; a row without any weight sets
- * PA_DEVERR_PROBS and gives token -1.  vocab_size <= 2^20, else PA_ERR_UNSUPPORTED.
+ * A sum is the same whatever the order of its weights.  Each of them is within 2^-57 for
+ * c = 0 and c = 1 (the row, and what the first refusal leaves), within 2^-46 for any other
+ * c, next to c's own rounding in binary64.  A sequence without nodes or with bad lengths
+ * gets accepted length 0 and token -1; a row without any weight sets PA_DEVERR_PROBS and
+ * gives token -1.  vocab_size <= 2^20, else PA_ERR_UNSUPPORTED.
  */
 int pa_verify_tree(const int32_t *tokens, const int32_t *parents, const int32_t *query_start_loc,
                    int32_t num_seqs, int32_t num_tokens, const void *target_probs, int64_t target_stride,

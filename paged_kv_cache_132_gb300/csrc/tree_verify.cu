@@ -21,8 +21,8 @@
 // of 128 000 tokens by 2^-24, binary64 additions run at a sixtieth of the rate.  A weight
 // is d + e, the difference in binary32 and its rounding error (exact: e = (p - d) - q for
 // p >= q), and falls into two whole numbers by additions alone: d + 1 has its multiple of
-// 2^-23 in the low bits, what is left of it its multiple of 2^-45.  A lane adds those
-// words, and what is left then (2^-46 and less) in binary32, over its 16 entries of a
+// 2^-23 in the low bits, what is left of it and e their multiple of 2^-44.  A lane adds those
+// words, and what is left then (2^-44 and less) in binary32, over its 16 entries of a
 // segment, and takes the constants out once; which entries are a lane's goes by the row
 // alone.  Two entries go through the additions of one instruction.
 //
@@ -65,31 +65,36 @@ __device__ inline float as_float(__nv_bfloat16 x) { return __bfloat162float(x); 
 // A probability: NaN and negative entries count as 0, those above 1 as 1.
 __device__ inline float clean(float x) { return __saturatef(x); }
 
-// Sum of up to 16 weights d + e, d in [0, 1], |e| <= 2^-24, in units of 2^-56.
+// Sum of up to 16 weights d + e, d in [0, 1], |e| <= 2^-23, in units of 2^-56.
 struct Sum {
     static constexpr float A = 1.f;         // [1, 2]: steps of 2^-23
-    static constexpr float B = 0x1.8p-22f;  // steps of 2^-45, +- 2^-23
+    static constexpr float B = 0x1.8p-21f;  // steps of 2^-44, +- 2^-22
     uint32_t a = 0, b = 0;
     float rest0 = 0.f, rest1 = 0.f;
     int count = 0;
+    template <bool HAS_E>
     __device__ inline void add2(float d0, float d1, float e0, float e1) {
         float x0 = d0, x1 = d1;
         add2_rn(x0, x1, A, A);
         a += __float_as_uint(x0) + __float_as_uint(x1);
         add2_rn(x0, x1, -A, -A);
         sub2_rn(d0, d1, x0, x1);
-        add2_rn(d0, d1, e0, e1);
+        // B + d + e in steps of 2^-44, then B + d + e without it: d + e by itself would be
+        // rounded by 2^-48.  Each difference is exact: of numbers that are multiples of 2^-44,
+        // or that are less than that apart.
         x0 = d0, x1 = d1;
         add2_rn(x0, x1, B, B);
+        if constexpr (HAS_E) add2_rn(x0, x1, e0, e1);
         b += __float_as_uint(x0) + __float_as_uint(x1);
         add2_rn(x0, x1, -B, -B);
         sub2_rn(d0, d1, x0, x1);
+        if constexpr (HAS_E) add2_rn(d0, d1, e0, e1);
         add2_rn(rest0, rest1, d0, d1);
         count += 2;
     }
     __device__ inline u64 value() const {
         const int64_t hi = (int32_t)(a - count * __float_as_uint(A)), mid = (int32_t)(b - count * __float_as_uint(B));
-        const int64_t v = hi * (1LL << 33) + mid * (1LL << 11) + __float2int_rn((rest0 + rest1) * 0x1p56f);
+        const int64_t v = hi * (1LL << 33) + mid * (1LL << 12) + __float2int_rn((rest0 + rest1) * 0x1p56f);
         return v > 0 ? (u64)v : 0;
     }
 };
@@ -113,30 +118,40 @@ enum Kind { kRow, kDifference, kGeneral };  // c = 0, 1, any
 struct Weights {
     Kind kind;
     float hi, lo;
-    // d + e of one entry, d in the place of p.
-    __device__ inline void general(float& p, float q, float& e) const {
-        const float x = clean(q), b = __fmul_rn(x, hi), d = __fsub_rn(p, b);
-        e = __fsub_rn(__fsub_rn(__fsub_rn(p, d), b), __fmaf_rn(x, lo, __fmaf_rn(x, hi, -b)));
-        e = d > 0.f ? fmaxf(e, -d) : 0.f;
-        p = fmaxf(d, 0.f);
+    // d + e of two entries, d in the place of p.  Where d = p - rn(q hi) cancels, what the
+    // product and the difference left, up to 2^-23 for c q < 1, may be the larger part of the
+    // weight and have its sign: the larger of the two counts as d.  A positive weight (c q < p
+    // <= 1) is off by the split of c, 2^-48 c q, and by two roundings of numbers up to 2^-23:
+    // less than 2^-46.
+    __device__ inline void general(float& p0, float& p1, float q0, float q1, float& e0, float& e1) const {
+        float x0 = clean(q0), x1 = clean(q1), b0 = x0, b1 = x1, t0 = x0, t1 = x1, d0 = p0, d1 = p1;
+        fma2_rn(b0, b1, hi, hi, 0.f, 0.f);
+        fma2_rn(t0, t1, hi, hi, -b0, -b1);
+        fma2_rn(x0, x1, lo, lo, t0, t1);
+        sub2_rn(d0, d1, b0, b1);
+        sub2_rn(p0, p1, d0, d1);
+        sub2_rn(p0, p1, b0, b1);
+        sub2_rn(p0, p1, x0, x1);
+        const bool some0 = d0 > -p0, some1 = d1 > -p1;
+        e0 = some0 ? fminf(d0, p0) : 0.f, e1 = some1 ? fminf(d1, p1) : 0.f;
+        p0 = some0 ? fmaxf(d0, p0) : 0.f, p1 = some1 ? fmaxf(d1, p1) : 0.f;
     }
     template <Kind KIND>
     __device__ inline void add2(Sum& sum, float p0, float p1, float q0, float q1) const {
         p0 = clean(p0), p1 = clean(p1);
         if constexpr (KIND == kRow) {
-            sum.add2(p0, p1, 0.f, 0.f);
+            sum.template add2<false>(p0, p1, 0.f, 0.f);
         } else if constexpr (KIND == kDifference) {
             q0 = fminf(clean(q0), p0), q1 = fminf(clean(q1), p1);
             float d0 = p0, d1 = p1;
             sub2_rn(d0, d1, q0, q1);
             sub2_rn(p0, p1, d0, d1);
             sub2_rn(p0, p1, q0, q1);
-            sum.add2(d0, d1, p0, p1);
+            sum.template add2<true>(d0, d1, p0, p1);
         } else {
             float e0, e1;
-            general(p0, q0, e0);
-            general(p1, q1, e1);
-            sum.add2(p0, p1, e0, e1);
+            general(p0, p1, q0, q1, e0, e1);
+            sum.template add2<true>(p0, p1, e0, e1);
         }
     }
     __device__ inline u64 one(float p, float q) const {
