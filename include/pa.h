@@ -520,9 +520,10 @@ int pa_tree_attention(void *out, const void *query, int64_t query_stride, const 
  *   path              device, int32 [num_tokens]: from each sequence's first row on the
  *                     accepted nodes, then -1; other rows are not written
  *   next_tokens       device, int32 [num_seqs]
- * A sum is the same whatever the order of its weights.  Each of them is within 2^-57 for
- * c = 0 and c = 1 (the row, and what the first refusal leaves), within 2^-46 for any other
- * c, next to c's own rounding in binary64.  A sequence without nodes or with bad lengths
+ * Weights count as whole numbers of 2^-56, each rounded by itself, so that sums are exact
+ * whatever the order and a token of less than half of that is not drawn.  A weight is within
+ * 2^-57 for c = 0 and c = 1 (the row, and what the first refusal leaves), within 2^-46 for any
+ * other c, next to c's own rounding in binary64.  A sequence without nodes or with bad lengths
  * gets accepted length 0 and token -1; a row without any weight sets PA_DEVERR_PROBS and
  * gives token -1.  vocab_size <= 2^20, else PA_ERR_UNSUPPORTED.
  */

@@ -20,11 +20,12 @@
 // border of the cumulative weights is missed by a rounding: binary32 sums move the borders
 // of 128 000 tokens by 2^-24, binary64 additions run at a sixtieth of the rate.  A weight
 // is d + e, the difference in binary32 and its rounding error (exact: e = (p - d) - q for
-// p >= q), and falls into two whole numbers by additions alone: d + 1 has its multiple of
-// 2^-23 in the low bits, what is left of it and e their multiple of 2^-44.  A lane adds those
-// words, and what is left then (2^-44 and less) in binary32, over its 16 entries of a
-// segment, and takes the constants out once; which entries are a lane's goes by the row
-// alone.  Two entries go through the additions of one instruction.
+// p >= q), and falls into three whole numbers by additions alone: d + 1 has its multiple of
+// 2^-23 in the low bits, what is left of it and e their multiple of 2^-44, and what is left
+// then its multiple of 2^-56.  A lane adds those words over its 16 entries of a segment and
+// takes the constants out once.  Each entry is rounded by itself, so the sums of a row, a
+// segment, a vector and an entry agree to the last unit.  Two entries go through the
+// additions of one instruction.
 //
 // A cluster of CTAs per sequence, one CTA for large batches, shares the row's segments
 // of 512 entries.  All its CTAs walk the tree alike (one warp, from probabilities of the
@@ -69,8 +70,8 @@ __device__ inline float clean(float x) { return __saturatef(x); }
 struct Sum {
     static constexpr float A = 1.f;         // [1, 2]: steps of 2^-23
     static constexpr float B = 0x1.8p-21f;  // steps of 2^-44, +- 2^-22
-    uint32_t a = 0, b = 0;
-    float rest0 = 0.f, rest1 = 0.f;
+    static constexpr float C = 0x1.8p-33f;  // steps of 2^-56, +- 2^-34 (2^-44 at most are left)
+    uint32_t a = 0, b = 0, c = 0;
     int count = 0;
     template <bool HAS_E>
     __device__ inline void add2(float d0, float d1, float e0, float e1) {
@@ -89,13 +90,15 @@ struct Sum {
         add2_rn(x0, x1, -B, -B);
         sub2_rn(d0, d1, x0, x1);
         if constexpr (HAS_E) add2_rn(d0, d1, e0, e1);
-        add2_rn(rest0, rest1, d0, d1);
+        add2_rn(d0, d1, C, C);
+        c += __float_as_uint(d0) + __float_as_uint(d1);
         count += 2;
     }
+    // An entry is d + e >= 0 rounded to units: never below 0.
     __device__ inline u64 value() const {
         const int64_t hi = (int32_t)(a - count * __float_as_uint(A)), mid = (int32_t)(b - count * __float_as_uint(B));
-        const int64_t v = hi * (1LL << 33) + mid * (1LL << 12) + __float2int_rn((rest0 + rest1) * 0x1p56f);
-        return v > 0 ? (u64)v : 0;
+        const int64_t low = (int32_t)(c - count * __float_as_uint(C));
+        return (u64)(hi * (1LL << 33) + mid * (1LL << 12) + low);
     }
 };
 constexpr double kUnit = 0x1p-56;
@@ -110,7 +113,7 @@ __device__ inline u64 sum_of_lanes(u64 x) {
     const uint32_t a = __reduce_add_sync(kAll, (uint32_t)x & 0x7ffffffu);
     const uint32_t b = __reduce_add_sync(kAll, (uint32_t)(x >> 27) & 0x7ffffffu);
     const uint32_t c = __reduce_add_sync(kAll, (uint32_t)(x >> 54));
-    return c < 960 ? ((u64)c << 54) + ((u64)b << 27) + a : ~0ull;
+    return c < 1024 ? add_sat((u64)c << 54, ((u64)b << 27) + a) : ~0ull;
 }
 
 // max(p - c q, 0), c = hi + lo.
@@ -347,9 +350,16 @@ struct Verify {
         return x;
     }
 
-    // The first entry of the CTA's segments whose cumulative weight exceeds `left`, by
-    // one warp.  (The whole numbers of an entry or a vector may differ from a segment's by
-    // its last units: where they leave `left` beyond them all, the last entry with a weight.)
+    // Of inclusive sums, the one of the lanes before `owner`.
+    static __device__ inline u64 before_lane(u64 incl, int owner) {
+        const u64 x = __shfl_sync(kAll, incl, owner > 0 ? owner - 1 : 0);
+        return owner > 0 ? x : 0;
+    }
+
+    // The first entry of the CTA's segments whose cumulative weight exceeds `left`, less
+    // than their sum, by one warp.  The sums that are searched are those that were added, so
+    // each search ends at an entry, a vector and a segment that pass `left`.  (Saturated sums
+    // pass it; what is before them is then not their difference to the next.)
     __device__ int find(int node, const Weights& w, u64 left, int lane) {
         constexpr int N = 16 / (int)sizeof(T), V = kSegment / (32 * N);
         const bool use_q = w.kind != kRow;
@@ -361,10 +371,8 @@ struct Verify {
         u64 mine = 0;
         for (int k = k0; k < k1; ++k) mine = add_sat(mine, sm.segment[k]);
         u64 incl = scan(mine, lane);
-        unsigned past = __ballot_sync(kAll, incl > left);
-        if (past == 0) return -1;
-        int owner = __ffs(past) - 1, seg = k0;
-        left -= __shfl_sync(kAll, incl - mine, owner);
+        int owner = __ffs(__ballot_sync(kAll, incl > left)) - 1, seg = k0;
+        left -= before_lane(incl, owner);
         if (lane == owner)
             for (; seg < k1 - 1 && sm.segment[seg] <= left; ++seg) left -= sm.segment[seg];
         seg = __shfl_sync(kAll, seg, owner);
@@ -400,11 +408,8 @@ struct Verify {
             left -= all;
         }
         incl = scan(sum, lane);
-        past = __ballot_sync(kAll, incl > left);
-        const unsigned some = __ballot_sync(kAll, sum > 0);
-        if (some == 0) return -1;  // (a segment whose weight is a rounding)
-        owner = past ? __ffs(past) - 1 : 31 - __clz(some);
-        left -= min(left, __shfl_sync(kAll, incl - sum, owner));
+        owner = __ffs(__ballot_sync(kAll, incl > left)) - 1;
+        left -= before_lane(incl, owner);
         // Its entries, a lane to each.
         const int e = (s0 + seg) * kSegment + (v * 32 + owner) * N - a.skew + lane;
         float f[1] = {0.f}, h = 0.f;
@@ -413,10 +418,7 @@ struct Verify {
             if (use_q) h = as_float(b.at[e]);
             take_out(f, e, sm.num_refused);
         }
-        const u64 one = w.one(f[0], h);
-        past = __ballot_sync(kAll, scan(one, lane) > left);
-        const unsigned heavy = __ballot_sync(kAll, one > 0);
-        return __shfl_sync(kAll, e, past ? __ffs(past) - 1 : heavy ? 31 - __clz(heavy) : 0);
+        return __shfl_sync(kAll, e, __ffs(__ballot_sync(kAll, scan(w.one(f[0], h), lane) > left)) - 1);
     }
 };
 

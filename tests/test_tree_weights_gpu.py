@@ -1,5 +1,6 @@
-"""The weights p - c q of a verification: how near their sums come to the exact ones.  Per weight:
-2^-57 for the first difference (c = 1), 2^-46 for any c."""
+"""The weights p - c q of a verification.  They count in units of 2^-56, each entry by itself, so
+that a row's sum, a segment's, a vector's and an entry's agree.  A weight is within 2^-57 for the
+row itself and the first difference (c = 0 and 1), within 2^-46 for any c."""
 from fractions import Fraction
 
 import pytest
@@ -10,11 +11,104 @@ from trees import i32, starts
 
 pytestmark = pytest.mark.gpu
 
+UNIT = 2 ** 56
+
 
 @pytest.fixture(scope="module", autouse=True)
 def _library():
     assert torch.cuda.is_available(), "GPU tests need a CUDA device"
     native.load()
+
+
+def units(x):
+    """A weight in units, rounded to nearest, ties to even."""
+    return round(Fraction(x) * UNIT)
+
+
+def place(values, dtype, skew):
+    """Rows [n][V] that begin `skew` entries behind a 16-byte boundary, NaN around them."""
+    n, v = values.shape
+    wide = torch.full((n, -(-(v + skew) // 16) * 16), float("nan"), dtype=dtype, device="cuda")
+    wide[:, skew:skew + v] = values.to(dtype)
+    return wide[:, skew:skew + v]
+
+
+def token_of(row, u):
+    """The lowest t whose cumulative units exceed u times their sum, which stays below 2^64."""
+    w = [units(x) for x in row]
+    left = int(Fraction(u) * min(sum(w), 2 ** 64 - 1))
+    for t, x in enumerate(w):
+        if x > left:
+            return t
+        left -= x
+    return -1
+
+
+# ---------------------------------------------------------------------------
+# weights of a unit and less: every level of the sums counts them alike
+# ---------------------------------------------------------------------------
+SMALL = [2.0 ** -60, 0.3 * 2.0 ** -56, 0.5 * 2.0 ** -56, 0.6 * 2.0 ** -56, 1.4 * 2.0 ** -56]
+
+
+@pytest.mark.parametrize("small", SMALL)
+@pytest.mark.parametrize("skew", [0, 1, 3])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("vocab", [5, 512, 1024, 6000])
+def test_first_token_behind_small_weights(vocab, dtype, skew, small):
+    rows = torch.full((2, vocab), small, dtype=torch.float64)
+    rows[:, -1] = 1.0
+    p = place(rows, dtype, skew)
+    u = torch.tensor([0.0, 2.0 ** -40], device="cuda")
+    got = api.verify_tree(i32([0, 0]), i32([-1, -1]), starts([1, 1]), p, None, torch.zeros(2, device="cuda"), u)
+    assert api.get_device_error() == (0, 0)
+    assert got.next_tokens.tolist() == [token_of(r, x) for r, x in zip(p.double().tolist(), u.tolist())]
+
+
+@pytest.mark.parametrize("skew", [0, 1, 2])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
+def test_rows_of_small_weights(dtype, skew):
+    """Nothing but weights around a unit (16-bit floats of 5 exponent bits: their smallest, 2^-24)."""
+    g = torch.Generator().manual_seed(3 + skew)
+    n, vocab = 96, 1201
+    low = 2.0 ** -24 if dtype is torch.float16 else 2.0 ** -60
+    rows = low * 2.0 ** (8 * torch.rand(n, vocab, generator=g, dtype=torch.float64))
+    rows[torch.rand(n, vocab, generator=g) < 0.4] = 0.0
+    p = place(rows, dtype, skew)
+    u = torch.rand(n, generator=g).cuda()
+    u[:8] = 0.0
+    got = api.verify_tree(i32([0] * n), i32([-1] * n), starts([1] * n), p, None, torch.zeros(n, device="cuda"), u)
+    assert api.get_device_error() == (0, 0)
+    assert got.next_tokens.tolist() == [token_of(r, x) for r, x in zip(p.double().tolist(), u.tolist())]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_a_refused_token_beside_small_weights(dtype):
+    """Token 0 is refused and out of the row; what is left of its vector is below half a unit."""
+    rows = torch.full((2, 700), 0.3 / UNIT, dtype=torch.float64)
+    rows[:, 0], rows[:, 600] = 0.25, 0.5
+    p = place(rows, dtype, 1)
+    got = api.verify_tree(i32([0, 0]), i32([-1, 0]), starts([2]), p, None, torch.full((2,), 0.9, device="cuda"),
+                          torch.zeros(1, device="cuda"))
+    assert api.get_device_error() == (0, 0)
+    assert got.accepted_lens.tolist() == [1] and got.next_tokens.tolist() == [600]
+
+
+def test_a_row_below_half_a_unit_has_no_weight():
+    p = place(torch.full((1, 900), 0.49 / UNIT, dtype=torch.float64), torch.float32, 0)
+    got = api.verify_tree(i32([0]), i32([-1]), starts([1]), p, None, torch.zeros(1, device="cuda"),
+                          torch.zeros(1, device="cuda"))
+    assert api.get_device_error() == (-5, native.DEVERR_PROBS)
+    assert got.next_tokens.tolist() == [-1]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("vocab", [239, 240, 241, 245, 255, 256, 257, 500, 40000])
+def test_rows_of_ones(vocab, dtype):
+    """No probabilities: sums around 2^64 units and beyond."""
+    p = place(torch.ones(7, vocab, dtype=torch.float64), dtype, 1)
+    u = torch.tensor([0.0, 0.3, 0.9375, 0.95, 0.98, 0.997, 0.99999994], device="cuda")
+    got = api.verify_tree(i32([0] * 7), i32([-1] * 7), starts([1] * 7), p, None, torch.zeros(7, device="cuda"), u)
+    assert got.next_tokens.tolist() == [token_of([1.0] * vocab, x) for x in u.tolist()]
 
 
 # ---------------------------------------------------------------------------
