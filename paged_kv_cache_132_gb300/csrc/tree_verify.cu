@@ -491,18 +491,19 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(const __grid_c
                 if (i >= n) break;
                 from = i + 1;
                 const bool plain = c == 0. && sum == 1.;
-                const int x = sm.token[i];
+                const int x = sm.token[i], num_refused = sm.num_refused;
                 bool accept;
                 double w = 0.;
                 if (drafted) {
                     accept = plain ? sm.first[i] : (double)sm.u[i] * sm.q[i] * sum < fmax(sm.p[i] - c * sm.q[i], 0.);
-                } else if (plain && sm.num_refused == 0) {
+                } else if (plain && num_refused == 0) {
                     accept = sm.first[i];
                     w = sm.p[i];
                 } else {
                     w = v.refused(x, lane) ? 0. : sm.p[i];
                     accept = (double)sm.u[i] * sum < w;
                 }
+                __syncwarp();  // every lane has read the list that lane 0 changes
                 if (accept) {
                     if (lane == 0) {
                         if (rank == 0) p.path[row0 + count] = i;
@@ -518,7 +519,10 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(const __grid_c
                     break;
                 } else {
                     sum = fmax(sum - w, 0.);
-                    if (lane == 0 && w > 0.) sm.refused[sm.num_refused++] = x;
+                    if (lane == 0 && w > 0.) {
+                        sm.refused[num_refused] = x;
+                        sm.num_refused = num_refused + 1;
+                    }
                 }
                 __syncwarp();
             }
