@@ -1046,11 +1046,11 @@ __global__ void __launch_bounds__(TreeShape<D>::THREADS, 1)
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = sm.tmem_base;
-    // The lengths are read before the wait: no kernel that writes them lets its dependents
-    // start before they are written (common.cuh).  What wrote the queries, the masks and the
-    // pools may still be finishing.
-    const TreePiece piece = tree_piece<Shape>(p, sm);
+    // Before the lengths are read too: a caller's kernel may write them after it has let its
+    // dependents start, and pieces of old lengths with items of new ones would leave parts
+    // that are not there.
     pdl_wait_prerequisites();
+    const TreePiece piece = tree_piece<Shape>(p, sm);
 
     if (warp < Shape::SOFTMAX_WARP) {
         regs_dec<Shape::REGS_OTHER>();
