@@ -543,7 +543,8 @@ int pa_verify_tree(const int32_t *tokens, const int32_t *parents, const int32_t 
  * context_lens[s] - n_s + accepted_lens[s]; and the blocks behind it go back to the ring
  * of pa_plan_step, behind its last free entry, sequence after sequence.
  *   k_caches, v_caches  HOST arrays of num_layers device pool pointers (1 <=
- *                     num_layers <= 256), all shaped by `cache`
+ *                     num_layers <= 256), all shaped by `cache`.  No two may share
+ *                     memory (layers that share a pool: give it once)
  *   path              device, int32 [num_tokens]: as pa_verify_tree's, entries from the
  *                     sequence's first row on, 0 <= path[0] < path[1] < ... < n_s
  *   accepted_lens     device, int32 [num_seqs], 0 .. n_s (0: no node stays)

@@ -615,7 +615,7 @@ def commit_tree(k_caches: Sequence[torch.Tensor], v_caches: Sequence[torch.Tenso
     """Keep the accepted paths of drafted trees: move their K/V rows together in
     every layer's pools, cut the lengths to them, and give the blocks behind back to
     plan_step's ring (``free_ring`` and ``free_state``; None: the host's manager
-    keeps the blocks).  ``path`` and ``accepted_lens`` are verify_tree's.  ``out`` may
+    keeps the blocks).  A pool that several layers share is given once.  ``path`` and ``accepted_lens`` are verify_tree's.  ``out`` may
     reuse buffers, context_lens and free_state among them."""
     i32, n = torch.int32, len(k_caches)
     _require(n == len(v_caches) and n > 0, "one K and one V pool per layer")

@@ -3,6 +3,7 @@
 // reaches the GPU.
 #include <nvtx3/nvToolsExt.h>
 
+#include <algorithm>
 #include <cmath>
 
 #include "host.h"
@@ -21,6 +22,19 @@ struct NvtxRange {
 bool overlap(const void* out, int64_t bytes, const void* in, int64_t input_bytes) {
     const auto a = reinterpret_cast<uintptr_t>(out), b = reinterpret_cast<uintptr_t>(in);
     return in && bytes > 0 && input_bytes > 0 && a < b + (uint64_t)input_bytes && b < a + (uint64_t)bytes;
+}
+
+// Do any two of the layers' pools, of `bytes` bytes each, share memory?
+bool pools_overlap(void* const* k_caches, void* const* v_caches, int num_layers, uint64_t bytes) {
+    uintptr_t at[2 * pa::kMaxCopyLayers];
+    for (int l = 0; l < num_layers; ++l) {
+        at[2 * l] = reinterpret_cast<uintptr_t>(k_caches[l]);
+        at[2 * l + 1] = reinterpret_cast<uintptr_t>(v_caches[l]);
+    }
+    std::sort(at, at + 2 * num_layers);
+    for (int i = 1; i < 2 * num_layers; ++i)
+        if (at[i] - at[i - 1] < bytes) return true;
+    return false;
 }
 
 }  // namespace
@@ -231,6 +245,10 @@ int pa_commit_tree(void* const* k_caches, void* const* v_caches, int32_t num_lay
     for (int l = 0; l < num_layers; ++l)
         if (!aligned(k_caches[l], 16) || !aligned(v_caches[l], 16)) return PA_ERR_INVALID_ARG;
     if (num_seqs > pa::kMaxStepSeqs || (free_ring && ring_size >= pa::kMaxStepCount)) return PA_ERR_UNSUPPORTED;
+    // A path's rows move in every pool at once: in one that is given twice they would move twice.
+    const uint64_t pool_bytes = (uint64_t)shape.num_blocks * shape.num_kv_heads * shape.block_size * shape.head_dim *
+                                shape.elem_bytes;
+    if (pools_overlap(k_caches, v_caches, num_layers, pool_bytes)) return PA_ERR_INVALID_ARG;
     // The moves read what the lengths are made of; context_lens itself is overwritten behind them.
     const int64_t seqs = 4LL * num_seqs;
     if (overlap(context_lens_out, seqs, accepted_lens, seqs) || overlap(context_lens_out, seqs, path, 4LL * num_tokens) ||
