@@ -38,3 +38,25 @@ def test_many_looked_up_children(vocab):
         assert api.get_device_error() == (0, 0)
         c.check(got)
     assert max(got.accepted_lens.tolist()) > 1
+
+
+@pytest.mark.parametrize("drafted", [True, False])
+@pytest.mark.parametrize("lens", [[1025, 4], [4, 1025, 6, 1200, 3], [1100]])
+def test_beside_a_sequence_of_too_many_nodes(lens, drafted):
+    """The sequences beside it get their own verdicts; its rows of the path are not written."""
+    c = Case(lens, 64, drafted=drafted, seed=len(lens))
+    out = api.TreeVerdict(*(torch.full((n,), -7, dtype=torch.int32, device="cuda")
+                            for n in (len(lens), sum(lens), len(lens))))
+    got = c.call(out=out)
+    assert api.get_device_error() == (-5, native.DEVERR_CONTEXT_LEN)
+    at = 0
+    for s, n in enumerate(lens):
+        rows = slice(at, at + n)
+        at += n
+        if n > native.MAX_TREE_NODES:
+            assert got.accepted_lens[s] == 0 and got.next_tokens[s] == -1 and (got.path[rows] == -7).all()
+            continue
+        want, token = expected(c.ids[rows].tolist(), c.up[rows].tolist(), weight(c.p[rows]),
+                               weight(c.q[rows]) if drafted else None, c.accept[rows].tolist(), c.sample[s].item())
+        assert got.path[rows].tolist() == want + [-1] * (n - len(want))
+        assert got.accepted_lens[s] == len(want) and got.next_tokens[s] == token
