@@ -555,9 +555,9 @@ int pa_verify_tree(const int32_t *tokens, const int32_t *parents, const int32_t 
  *                     are given back (a host manager does), the others are not used
  * A sequence with bad lengths (PA_DEVERR_CONTEXT_LEN) or a bad path (PA_DEVERR_TREE)
  * stays as it is.  A ring without room, or a free_state out of range, sets PA_DEVERR_STEP
- * and no block is given back.  A bad block id sets PA_DEVERR_BLOCK_ID, and rows from or
- * to it are not moved.  num_seqs <= 16384, ring_size below 2^30 - 1, else
- * PA_ERR_UNSUPPORTED.
+ * and no block is given back.  A bad block id sets PA_DEVERR_BLOCK_ID; rows from or to it
+ * are not moved, and one that is given back goes into the ring as the table has it.
+ * num_seqs <= 16384, ring_size below 2^30 - 1, else PA_ERR_UNSUPPORTED.
  */
 int pa_commit_tree(void *const *k_caches, void *const *v_caches, int32_t num_layers, const pa_cache_desc *cache,
                    const int32_t *query_start_loc, int32_t num_seqs, int32_t num_tokens,

@@ -43,11 +43,11 @@
 //
 // Bound: HBM up to about 128 rows (2 d e bytes a position and KV head against 4 d
 // flops a row and position), tensor cores above.  Measured (graph replay): 64 sequences
-// of 16 nodes, lognormal contexts up to 8192, 32/8 heads of 128, bf16: 92.4-94.5 us, 5.4
+// of 16 nodes, lognormal contexts up to 8192, 32/8 heads of 128, bf16: 93.8 us, 5.4
 // TB/s; 32 of 40 to 64 nodes, 1024 to 8192 tokens: 152 us, 4.7 TB/s and 0.93 PFLOP/s at
 // once; 24 of 1 to 25 nodes, 128 to 2048 tokens, 40/40 heads, f16: 111 us, 5.4 TB/s; 3 of
-// 31 nodes and 30 to 33 thousand tokens, 16/4 heads of 64: 30.4 us, 3.2 TB/s.  One
-// short sequence, all of it latency: 10.9 us (launch, the list's prefix sum, the first
+// 31 nodes and 30 to 33 thousand tokens, 16/4 heads of 64: 31.9 us, 3.1 TB/s.  One
+// short sequence, all of it latency: 11.9 us (launch, the list's prefix sum, the first
 // copies, S, softmax, P V, a part, the reduce kernel), which the others pay beside theirs.
 //
 // Values a row must not see: its weight is 0, but 0 * NaN is NaN on the tensor
@@ -1048,7 +1048,8 @@ __global__ void __launch_bounds__(TreeShape<D>::THREADS, 1)
     const uint32_t tmem = sm.tmem_base;
     // Before the lengths are read too: a caller's kernel may write them after it has let its
     // dependents start, and pieces of old lengths with items of new ones would leave parts
-    // that are not there.
+    // that are not there.  (1.1 us for one short sequence, 1.4 for the long ones, 0.7 or less
+    // for the others, against lengths read before the wait.)
     pdl_wait_prerequisites();
     const TreePiece piece = tree_piece<Shape>(p, sm);
 

@@ -33,11 +33,12 @@
 // needed: at a refusal, and for the last token unless the last refusal's sums serve.
 // The segments' sums stay in shared memory, so the token costs one more segment.
 //
-// Bound: latency.  A sum is one pass over the row by all CTAs at the rate of issue, and a
-// refusal's sum must be known before the next child is tried.  Graph replay: 9.4 us for one
-// sequence of 6 nodes and 32 000 tokens; 32.9 us for 64 sequences of 12 nodes and 128 256
-// tokens in f32, which need 1.3 passes on average and up to 3; 16.6 us for 200 sequences
-// of looked-up tokens out of 50 021 in bf16, of which the last token's segment 3.5 us.
+// Bound: latency.  A sum is one pass over the row by all CTAs, a warp's segments one after
+// the other (issue active 29%, 1.4 TB/s), and a refusal's sum must be known before the next
+// child is tried.  Graph replay: 9.4 us for one sequence of 6 nodes and 32 000 tokens; 35.0 us
+// for 64 sequences of 12 nodes and 128 256 tokens in f32, which need 1.3 passes on average and
+// up to 3; 16.6 us for 200 sequences of looked-up tokens out of 50 021 in bf16, of which the
+// last token's segment 3.5 us.
 #include <cooperative_groups.h>
 #include <type_traits>
 
@@ -82,7 +83,7 @@ struct Sum {
         sub2_rn(d0, d1, x0, x1);
         // B + d + e in steps of 2^-44, then B + d + e without it: d + e by itself would be
         // rounded by 2^-48.  Each difference is exact: of numbers that are multiples of 2^-44,
-        // or that are less than that apart.
+        // or that are less than that apart.  (The 64 sequences above: 35.0 us so, 34.4 without e.)
         x0 = d0, x1 = d1;
         add2_rn(x0, x1, B, B);
         if constexpr (HAS_E) add2_rn(x0, x1, e0, e1);
@@ -596,7 +597,8 @@ cudaError_t launch_t(const TreeVerifyParams& p, int ranks, cudaStream_t stream) 
 
 cudaError_t launch_tree_verify(const TreeVerifyParams& p, int dtype, int sms, cudaStream_t stream) {
     // As many CTAs to a sequence as keep two on every SM, each with 8 segments at least.
-    // (The 200 sequences above: 18.3 us so, 22.9 us with up to three or four CTAs an SM.)
+    // (The 200 sequences above: 16.5 us so and with one CTA an SM, 21.4 with up to four; the 64
+    // with draft rows: 34.7 us, 40.8 with one, 40.2 with four.)
     int ranks = 8;
     while (ranks > 1 && ((int64_t)p.num_seqs * ranks > 2LL * sms || p.vocab < ranks * 8 * kSegment)) ranks /= 2;
     switch (dtype) {
