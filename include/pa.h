@@ -34,9 +34,9 @@
  *     asynchronous on it; the caller keeps every buffer alive until the
  *     stream reaches the call.
  *   - A caller's kernel may let its dependents start before it has written what a call reads
- *     (programmatic dependent launch): the calls wait for its end.  Only pa_decode and
- *     pa_decode_noalloc read context_lens before that; a kernel that writes it writes it
- *     before it signals.
+ *     (programmatic dependent launch): the calls wait for its end.  Only what pa_decode,
+ *     pa_decode_noalloc and pa_prefill read of lengths, start rows and tables is written
+ *     before such a signal.
  *   - KV pool layout: [num_blocks][num_kv_heads][block_size][head_dim], the
  *     head_dim elements of one token contiguous.  K and V are separate pools.
  *   - A slot number is physical_block * block_size + offset_in_block.

@@ -406,7 +406,7 @@ __device__ void tree_load(const TreeAttnParams& p, typename Shape::Smem& sm, int
     auto blocks_from = [&](const TreeItem& w, int j) {
         const int at = j * blocks_per_tile + lane;
         const int end = min(w.to * blocks_per_tile, (w.ctx + block_size - 1) >> p.block_shift);
-        return at < end ? __ldg(p.block_tables + (int64_t)w.seq * p.max_blocks + at) : -2;
+        return at < end ? __ldcg(p.block_tables + (int64_t)w.seq * p.max_blocks + at) : -2;
     };
     // The next item is known, and its first blocks are loading, before one's last copies.
     TreeItem w{}, next{};
@@ -714,6 +714,7 @@ __device__ void tree_mma(const TreeAttnParams& p, typename Shape::Smem& sm, uint
 // ---------------------------------------------------------------------------
 // softmax warps of chain i (thread r = row r = TMEM lane r)
 // ---------------------------------------------------------------------------
+// Masks and tables are read past L1: they may be written after this grid was launched.
 // Bit k: the row attends to node first + k of its sequence (negative: a position before
 // the tree), k < 32.  `row` is its mask row, `near` the first words of it, which were
 // loaded when the item began: a masked tile otherwise waits for up to three round trips.
@@ -722,7 +723,7 @@ __device__ __forceinline__ uint32_t tree_mask_bits(const TreeAttnParams& p, cons
                                                    const uint32_t (&near)[kTreeNear], int first) {
     if (first <= -32) return ~0u;
     auto word = [&](int at) {
-        if (at >= kTreeNear) return at < p.mask_words ? __ldg(row + at) : 0u;
+        if (at >= kTreeNear) return at < p.mask_words ? __ldcg(row + at) : 0u;
         uint32_t w = 0u;
 #pragma unroll
         for (int k = 0; k < kTreeNear; ++k) w = at == k ? near[k] : w;
@@ -763,7 +764,7 @@ __device__ void tree_softmax(const TreeAttnParams& p, typename Shape::Smem& sm, 
         const uint32_t* const mask = p.tree_mask + (int64_t)(w.row0 + (valid ? node : w.t0)) * p.mask_words;
         uint32_t near[kTreeNear];
 #pragma unroll
-        for (int k = 0; k < kTreeNear; ++k) near[k] = k < p.mask_words ? __ldg(mask + k) : 0u;
+        for (int k = 0; k < kTreeNear; ++k) near[k] = k < p.mask_words ? __ldcg(mask + k) : 0u;
         float m = NEG_INF, l = 0.f;
         bool begun = false;
 #pragma unroll 1
@@ -876,8 +877,8 @@ __device__ __noinline__ void tree_add_nonfinite(const TreeAttnParams& p, const T
     const int end = min(w.to * 128, w.ctx);
     for (int at = max(w.from * 128, w.base); at < end; ++at) {
         const int m = at - w.base;
-        if (!((__ldg(mask + (m >> 5)) >> (m & 31)) & 1u)) continue;
-        const int id = __ldg(table + (at >> p.block_shift));
+        if (!((__ldcg(mask + (m >> 5)) >> (m & 31)) & 1u)) continue;
+        const int id = __ldcg(table + (at >> p.block_shift));
         if (id < 0 || (int64_t)id >= p.num_blocks) continue;
         const int64_t slot = (((int64_t)id * p.num_kv_heads + w.kv_head) << p.block_shift) + (at & ((1 << p.block_shift) - 1));
         const T* v = static_cast<const T*>(p.v_cache) + slot * D;

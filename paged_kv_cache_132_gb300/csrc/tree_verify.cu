@@ -35,9 +35,9 @@
 //
 // Bound: latency.  A sum is one pass over the row by all CTAs, a warp's segments one after
 // the other (issue active 29%, 1.4 TB/s), and a refusal's sum must be known before the next
-// child is tried.  Graph replay: 9.4 us for one sequence of 6 nodes and 32 000 tokens; 35.0 us
+// child is tried.  Graph replay: 9.3 us for one sequence of 6 nodes and 32 000 tokens; 34.3 us
 // for 64 sequences of 12 nodes and 128 256 tokens in f32, which need 1.3 passes on average and
-// up to 3; 16.6 us for 200 sequences of looked-up tokens out of 50 021 in bf16, of which the
+// up to 3; 16.8 us for 200 sequences of looked-up tokens out of 50 021 in bf16, of which the
 // last token's segment 3.5 us.
 #include <cooperative_groups.h>
 #include <type_traits>
@@ -83,7 +83,7 @@ struct Sum {
         sub2_rn(d0, d1, x0, x1);
         // B + d + e in steps of 2^-44, then B + d + e without it: d + e by itself would be
         // rounded by 2^-48.  Each difference is exact: of numbers that are multiples of 2^-44,
-        // or that are less than that apart.  (The 64 sequences above: 35.0 us so, 34.4 without e.)
+        // or that are less than that apart.  (0.6 us of the 64 sequences above.)
         x0 = d0, x1 = d1;
         add2_rn(x0, x1, B, B);
         if constexpr (HAS_E) add2_rn(x0, x1, e0, e1);
@@ -175,11 +175,12 @@ struct Row {
     }
 };
 
-// Vector v of COUNT, 32 lanes x N entries apart, from entry `e` of the row on.
+// Vector v of COUNT, 32 lanes x N entries apart, from entry `e` of the row on.  Past L1: rows
+// are read once, and may be written after this grid was launched.
 template <typename T, int N, int COUNT>
 __device__ inline void load_inside(const Row<T>& r, int e, uint4 (&x)[COUNT]) {
 #pragma unroll
-    for (int v = 0; v < COUNT; ++v) x[v] = __ldg(reinterpret_cast<const uint4*>(r.at + e) + v * 32);
+    for (int v = 0; v < COUNT; ++v) x[v] = __ldcg(reinterpret_cast<const uint4*>(r.at + e) + v * 32);
 }
 // N entries one by one, 0 outside the row.
 template <typename T, int N>
@@ -202,7 +203,7 @@ __device__ inline void load_edge(const Row<T>& r, int skew, int e, int vocab, ui
         const int at = e + v * 32 * N;
         const bool whole = skew == r.skew && at >= 0 && at + N <= vocab;
         x[v] = make_uint4(0u, 0u, 0u, 0u);
-        if (whole) x[v] = __ldg(reinterpret_cast<const uint4*>(r.at + at));
+        if (whole) x[v] = __ldcg(reinterpret_cast<const uint4*>(r.at + at));
         across |= !whole && at + N > 0 && at < vocab;
     }
     if (!__any_sync(kAll, across)) return;

@@ -9,6 +9,7 @@ import pytest
 import torch
 
 from paged_kv_cache_132_gb300 import api, build, native
+from test_tree_verify_gpu import Case
 from trees import Cache, i32, random_trees, starts
 
 pytestmark = pytest.mark.gpu
@@ -74,29 +75,28 @@ class Step:
     def plan(self, start, ctx):
         return api.plan_tree(self.parents, start, ctx, 64)
 
-    def attend(self, start, ctx, mask, **kw):
-        return api.tree_attention(self.q, start, mask, self.k, self.v, self.tables, ctx, self.scale, **kw)
-
 
 @pytest.mark.parametrize("d,dtype", [(128, torch.bfloat16), (64, torch.float16)])
 def test_lengths_written_late(write_late, d, dtype):
     s = Step(d, dtype)
     tree = s.plan(s.start, s.ctx)
-    want = s.attend(s.start, s.ctx, tree.tree_mask)
+    want = api.tree_attention(s.q, s.start, tree.tree_mask, s.k, s.v, s.tables, s.ctx, s.scale)
     torch.cuda.synchronize()
     assert api.get_device_error() == (0, 0)
-    for late in ("ctx", "start", "mask"):
+    for late in ("ctx", "start", "mask", "tables"):
         start = (s.old_start if late == "start" else s.start).clone()
         ctx = (s.old_ctx if late == "ctx" else s.ctx).clone()
         mask = torch.zeros_like(tree.tree_mask) if late == "mask" else tree.tree_mask
+        tables = s.tables.flip(0).contiguous() if late == "tables" else s.tables
         # the call's workspace and output exist, and its code is loaded: nothing comes between
         out = torch.zeros_like(s.q)
         size = api.tree_attention_workspace_size(s.q.shape[0], 1, 16, 4, d)
         work = torch.empty(size, dtype=torch.uint8, device="cuda")
         torch.cuda.synchronize()
-        src, dst = {"ctx": (s.ctx, ctx), "start": (s.start, start), "mask": (tree.tree_mask, mask)}[late]
+        src, dst = {"ctx": (s.ctx, ctx), "start": (s.start, start), "mask": (tree.tree_mask, mask),
+                    "tables": (s.tables, tables)}[late]
         write_late(dst, src)
-        s.attend(start, ctx, mask, out=out, workspace=work)
+        api.tree_attention(s.q, start, mask, s.k, s.v, tables, ctx, s.scale, out=out, workspace=work)
         torch.cuda.synchronize()
         assert api.get_device_error() == (0, 0)
         assert torch.equal(out, want), late
@@ -112,3 +112,24 @@ def test_plans_of_lengths_written_late(write_late):
     api.plan_tree(s.parents, start, ctx, 64, out=out)
     torch.cuda.synchronize()
     assert api.get_device_error() == (0, 0) and all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+@pytest.mark.parametrize("drafted", [True, False])
+def test_probabilities_written_late(write_late, drafted):
+    """The rows and the nodes of a verification, which a call on the same SMs has just read."""
+    c, other = Case([6] * 40, 3000, drafted=drafted), Case([6] * 40, 3000, drafted=drafted, seed=2)
+    want = [x.clone() for x in other.call()]
+    out = c.call()
+    names = ["p", "ids", "up", "accept", "sample"] + (["q"] if drafted else [])
+    own = {n: getattr(c, n) for n in names}
+    for name in names:
+        for n in names:
+            buffer = getattr(other, n).contiguous() if n != name else own[n].contiguous()
+            setattr(c, n, buffer.clone())
+        torch.cuda.synchronize()
+        c.call(out=out)
+        write_late(getattr(c, name), getattr(other, name).contiguous())
+        c.call(out=out)
+        torch.cuda.synchronize()
+        assert api.get_device_error() == (0, 0)
+        assert all(torch.equal(a, b) for a, b in zip(out, want)), name
